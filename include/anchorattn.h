@@ -365,6 +365,196 @@ aa_status aa_shard_plan(const int32_t* cu_doclens_host, int32_t num_docs, int32_
                         int32_t num_shards, aa_shard_piece* pieces, int32_t max_pieces, int32_t* num_pieces,
                         int64_t* shard_cost);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions with several axes
+ *
+ * Tokens of images and video carry one position per axis (time, height,
+ * width); text tokens carry the same number on every axis. Pair p of a head
+ * belongs to one axis a(p) and turns by pos[a(p)][t] * theta_p, in the pairing
+ * of `layout` (Eq. 6's 2x2 block, [ARCH §3.4 RoPE]). With one axis this is
+ * Eq. 6 itself for positions that the caller gives per token.
+ *
+ * aa_rope_axes is a plain value that the caller owns: it holds no device
+ * memory, may be copied, and serves any number of calls, threads and
+ * devices. Fill it with aa_rope_axes_init; the fields are the library's. */
+typedef struct {
+  int32_t head_dim, num_axes, layout, ready;
+  int32_t axis_of_pair[64];
+  uint64_t turn[64]; /* theta_p / (2 pi) modulo 1, in units of 2^-64 */
+} aa_rope_axes;
+
+/* head_dim 64 or 128; num_axes 1..4; layout AA_ROPE_ADJACENT or AA_ROPE_HALF;
+ * axis_of_pair host int32[head_dim / 2], each in [0, num_axes); theta host
+ * double[head_dim / 2], finite and >= 0 (0 leaves the pair as it is). */
+aa_status aa_rope_axes_init(aa_rope_axes* rope, int32_t head_dim, int32_t num_axes, int32_t layout,
+                            const int32_t* axis_of_pair, const double* theta);
+
+/* Rotate q [T, q_heads, D] and k [T, k_heads, D] (bf16) into q_out and k_out
+ * (contiguous, same shapes) in one launch; inverse = 1 turns back, which is
+ * also the gradient of the forward rotation.
+ *  - pos: device int32 [num_axes, total_tokens], any value (negative ones
+ *    turn the other way). The angle is reduced exactly in 64-bit fixed point,
+ *    so it stays within 2^-20 rad for |pos| * theta_p up to 2^30.
+ *  - q_stride, k_stride: elements from one token to the next, a multiple of 8
+ *    and >= heads * D (a slice of a joint projection is fine); the heads of a
+ *    token are contiguous. fp32 arithmetic, rounded once to bf16.
+ *  - k may be NULL with k_heads = 0. q_out = q (k_out = k) rotates in place
+ *    if that input is contiguous; outputs overlap nothing else.
+ *  - total_tokens = 0 is an empty call. */
+aa_status aa_rope_axes_apply(const aa_rope_axes* rope, const int32_t* pos, int32_t total_tokens, const void* q,
+                             int64_t q_stride, void* q_out, int32_t q_heads, const void* k, int64_t k_stride,
+                             void* k_out, int32_t k_heads, int32_t inverse, aa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key/value cache: answering with a model that this library trained
+ *
+ * The pool is two caller-owned bf16 arrays, k_pages and v_pages, each
+ * [num_layers, num_pages, Hkv, page_size, D]: a page holds page_size
+ * consecutive tokens of one sequence, and one head's part of it is contiguous
+ * (page_size * D * 2 bytes, what one copy into shared memory takes). Keys are
+ * stored ROTATED, so a page needs no positions.
+ *
+ * Two halves:
+ *  - Bookkeeping on the host (aa_cache_resize, _fork, _compact, _tables,
+ *    _stats): which page belongs to which sequence, with a reference count
+ *    for each page, so that forked sequences share what they have in common.
+ *    The handle is not thread-safe. A caller with its own scheduler leaves
+ *    this half alone (max_seqs = 0) and passes its own page tables below.
+ *  - Device calls (aa_cache_append, _attend, _copy_pages): stream-ordered,
+ *    no allocation, no host synchronisation. Everything that changes from
+ *    step to step (page tables, lengths) is read on the device, so a step can
+ *    be captured in a CUDA graph once and replayed with new contents.
+ *
+ * Batch layout of the device calls. B sequences; the new tokens of all of
+ * them lie one after the other in [T, H, D] tensors, sequence b's in rows
+ * [cu_q[b], cu_q[b + 1]) (device int32[B + 1], from 0, not decreasing; a
+ * sequence may have none). kv_len[b] (device int32[B]) counts the sequence's
+ * tokens INCLUDING the new ones: new token i of n_b has position
+ * kv_len[b] - n_b + i. page_table: device int32 [B, table_width], entry w the
+ * page of positions [w * page_size, (w + 1) * page_size); entries past a
+ * sequence's last page are never read. Rows at or behind cu_q[B] are left as
+ * they were.
+ *
+ * A page number outside [0, num_pages), or a position outside the table, is
+ * never used as an address: the token is skipped (append) or reads as zeros
+ * (attend), an error word is set, and aa_cache_check_error() reports it. */
+typedef struct {
+  int32_t num_layers;        /* >= 1                                             */
+  int32_t num_pages;         /* >= 1; num_layers * num_pages * Hkv * page_size < 2^31 */
+  int32_t page_size;         /* 16, 32, 64 or 128 tokens                         */
+  int32_t num_kv_heads;      /* Hkv >= 1                                         */
+  int32_t head_dim;          /* D: 64 or 128                                     */
+  int32_t max_seqs;          /* sequences that the bookkeeping can hold; 0: none */
+  int32_t host_only;         /* 1: bookkeeping only (no GPU needed)              */
+} aa_cache_config;
+
+typedef struct aa_cache_s* aa_cache_t;
+
+/* k_pages, v_pages: the pool, 16-byte aligned, alive as long as the handle
+ * (NULL with host_only). The handle belongs to the current device; the device
+ * calls below refuse another one. Its contents need no clearing. */
+aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, void* v_pages, aa_cache_t* out);
+
+/* Free a handle (synchronises the device). NULL is accepted. */
+aa_status aa_cache_destroy(aa_cache_t cache);
+
+/* Set the lengths of n sequences (host arrays; seqs distinct, in
+ * [0, max_seqs)): lens[i] is sequence seqs[i]'s length in tokens after the
+ * call. Growing takes free pages; shrinking, down to 0, gives pages back once
+ * no fork shares them. Where a sequence grows into a partly filled page that
+ * another one shares, the page is first copied (all layers, one launch for
+ * the whole call, on `stream`): aa_cache_append after it writes only pages
+ * that are the sequence's own. All or nothing: AA_ERR_NO_MEMORY if the free
+ * pages do not suffice.
+ * Pages given back may be handed out again at once, so the device calls
+ * of one pool must be ordered with one another (one stream, or events). A
+ * call that has to copy is refused while `stream` is being captured. */
+aa_status aa_cache_resize(aa_cache_t cache, const int32_t* seqs, const int32_t* lens, int32_t n, aa_stream_t stream);
+
+/* Make dst (an empty sequence) share all of src's pages and its length.
+ * Nothing is copied until one of them grows into a shared page. */
+aa_status aa_cache_fork(aa_cache_t cache, int32_t src, int32_t dst);
+
+/* Move the pages in use to the front of the pool, [0, pages in use), so that
+ * the rest can be handed to something else. *moved (may be NULL) receives the
+ * number of pages moved; page tables taken earlier are then stale. Refused
+ * while `stream` is being captured. */
+aa_status aa_cache_compact(aa_cache_t cache, aa_stream_t stream, int32_t* moved);
+
+/* Page tables and lengths of n sequences into host buffers: table
+ * [n, table_width], entries past the last page -1; lens [n]. Either may be
+ * NULL. AA_ERR_INVALID_ARG if a sequence has more than table_width pages. */
+aa_status aa_cache_tables(aa_cache_t cache, const int32_t* seqs, int32_t n, int32_t* table_host, int32_t table_width,
+                          int32_t* lens_host);
+
+/* Pages not in use, pages that more than one sequence shares, and the most
+ * pages that one sequence has. Any pointer may be NULL. */
+aa_status aa_cache_stats(aa_cache_t cache, int32_t* free_pages, int32_t* shared_pages, int32_t* longest);
+
+/* Copy page src[i] to page dst[i], all layers, keys and values (host arrays of
+ * n). The pairs are checked before anything is launched and travel with the
+ * launch, so they need no device memory and may be captured. Page numbers
+ * must lie in the pool; no page may be the target of two pairs or both a
+ * target and a source (the copies run at once), except src[i] = dst[i], which
+ * is a copy of nothing. */
+aa_status aa_cache_copy_pages(aa_cache_t cache, const int32_t* src, const int32_t* dst, int32_t n, aa_stream_t stream);
+
+/* One batch of new tokens. Strides count elements from one token to the next
+ * (multiples of 8, >= heads * D), so slices of a joint projection need no
+ * copy. */
+typedef struct {
+  const int32_t* page_table; /* device [num_seqs, table_width]                    */
+  const int32_t* cu_q;       /* device [num_seqs + 1]                             */
+  const int32_t* kv_len;     /* device [num_seqs]                                 */
+  int32_t num_seqs;          /* B >= 1                                            */
+  int32_t table_width;       /* >= 1                                              */
+  int32_t total_tokens;      /* T: rows of the tensors; >= cu_q[B]                */
+  int32_t layer;             /* in [0, num_layers)                                */
+} aa_cache_batch;
+
+/* Write the new tokens' keys and values (k, v [T, Hkv, D]) to their pages, the
+ * keys rotated by `rope` at pos (device int32 [num_axes, T]; both NULL: stored
+ * as they are). With q != NULL the same launch rotates q [T, q_heads, D] into
+ * q_out (contiguous; may be q if that is contiguous), which is what
+ * aa_cache_attend takes; it needs `rope`. */
+aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const aa_rope_axes* rope, const int32_t* pos, const void* q,
+                          int64_t q_stride, void* q_out, int32_t q_heads, aa_stream_t stream);
+
+/* Attention of the new tokens over their sequences' cached keys and values
+ * (the new ones included: append first). For new token i of sequence b, at
+ * position p, and every query head h, over the visible keys
+ *   j in [max(key_lo, 0), p], and j = 0 if anchor != 0 and p >= 0
+ * (the mask of [ARCH §3.4 Anchor]: key_lo is the first token of the query's
+ * document; or p - W + 1 for a sliding window):
+ *   O_i = sum_j softmax_j(scale * q_i . k_j) v_j,  LSE_i = ln sum_j exp(...).
+ * A row that sees no key gives O = 0 and LSE = -inf. Keys that no row of the
+ * call sees do not reach the result, whatever their values (NaN, infinities).
+ *  - q [T, q_heads, D] bf16, ROTATED (q_stride elements from token to token);
+ *    q_heads % Hkv == 0, at most 64 query heads per kv head.
+ *  - max_q: the most new tokens of a sequence. It chooses the kernel; a
+ *    sequence with more is still computed, only slower.
+ *  - key_lo: device int32 [T] or NULL (0 for every row).
+ *  - softmax_scale <= 0 selects 1/sqrt(D).
+ *  - o [T, q_heads, D] bf16; lse [q_heads, T] fp32 or NULL.
+ *  - workspace: aa_cache_attend_workspace_bytes() bytes, 256-byte aligned,
+ *    contents ignored; calls that may overlap need one each. */
+aa_status aa_cache_attend(aa_cache_t cache, const aa_cache_batch* batch, const void* q, int64_t q_stride, int32_t q_heads,
+                          int32_t max_q, const int32_t* key_lo, int32_t anchor, float softmax_scale, void* o, float* lse,
+                          void* workspace, size_t workspace_bytes, aa_stream_t stream);
+
+/* Bytes of device scratch aa_cache_attend needs for a batch of these sizes
+ * (partial results of keys split among CTAs; it grows with no argument but
+ * total_tokens and q_heads beyond a few hundred rows). 0 for invalid ones. */
+size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
+                                       int32_t table_width, int32_t q_heads);
+
+/* Synchronise `stream`, read and clear the cache's device error word:
+ * AA_ERR_INVALID_ARG if a device call met a page number or a position outside
+ * its range since the last check, AA_ERR_TIMEOUT if a bounded device wait ran
+ * out, AA_OK otherwise. */
+aa_status aa_cache_check_error(aa_cache_t cache, aa_stream_t stream);
+
 const char* aa_status_string(aa_status status);
 const char* aa_last_error(void);
 

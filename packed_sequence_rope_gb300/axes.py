@@ -1,0 +1,170 @@
+"""Rotary positions with several axes: aa_rope_axes_init / aa_rope_axes_apply and their autograd entry.
+
+Tokens of images and video carry a position per axis (time, height, width); pair p of a head turns by
+pos[axis of p][t] * theta_p (Eq. 6 of "When Precision Meets Position", architecture page, §3.4 "Rotary
+Positional Embedding (RoPE)", with one position per axis).
+
+    rope = RopeAxes(128, sections=(16, 24, 24), base=5e6)
+    q, k = rope_axes(rope, pos, q, k)                      # pos: int32 [3, T]; differentiable in q and k
+    with Plan(cu_doclens, T, Hq, Hkv, 128, rope_layout=ROPE_NONE) as plan:
+        o = anchor_attention(plan, q, k, v)                # the plan does not rotate again
+
+Like the rest of the binding this marshals arguments: the rotation is the library's kernel. Forward and backward may be
+captured in a CUDA graph under PyTorch's own rule: warm up on a side stream, and keep no eager autograd graph of the same
+leaves alive while capturing.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from .binding import AARopeAxes, ROPE_ADJACENT, _check, _stream, lib
+
+__all__ = ["RopeAxes", "RopeAxesFn", "rope_axes"]
+
+
+def _on(stream):
+    """Allocate on the stream that the kernels will run on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _check_tensor(name, x, shape, dtype, device=None):
+    """x is a CUDA tensor of `dtype`, `shape` (None: any size) and, if given, `device`."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
+    if x.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
+        raise ValueError(f"{name} must have shape {tuple('any' if n is None else n for n in shape)}, got {tuple(x.shape)}")
+    if device is not None and x.device != device:
+        raise ValueError(f"{name} is on {x.device}, expected {device}")
+
+
+def _rows(x):
+    """(x, token stride) as the kernels read it: a token's heads contiguous, 16-byte aligned rows; copied if it is not."""
+    T, H, D = x.shape
+    a, b, c = x.stride()
+    if c == 1 and (b == D or H == 1) and x.data_ptr() % 16 == 0:
+        if T <= 1:
+            return x, H * D
+        if a >= H * D and a % 8 == 0:
+            return x, a
+    x = x.contiguous()
+    return (x if x.data_ptr() % 16 == 0 else x.clone()), H * D
+
+
+def _out(name, out, like):
+    """The caller's output tensor, checked, or a new one of the shape of `like`."""
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _check_tensor(name, out, like.shape, like.dtype, like.device)
+    if not out.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return out
+
+
+class RopeAxes:
+    """A multi-axis rotation: which axis and frequency each pair has. Holds no device memory.
+
+    sections: pairs per axis, adding up to head_dim / 2; laid one after the other, or, with interleaved=True, dealt
+    to the axes in turn until each has its count. axis_of_pair gives the map itself instead. theta: [head_dim / 2]
+    frequencies in place of base^(-2p/D)."""
+
+    def __init__(self, head_dim, sections=None, base=1e4, theta=None, layout=ROPE_ADJACENT, interleaved=False,
+                 axis_of_pair=None):
+        head_dim = int(head_dim)
+        half = head_dim // 2
+        if (sections is None) == (axis_of_pair is None):
+            raise ValueError("give either sections or axis_of_pair")
+        if axis_of_pair is None:
+            left = [int(n) for n in sections]
+            if any(n < 0 for n in left) or sum(left) != half:
+                raise ValueError(f"sections must be >= 0 and add up to head_dim / 2 = {half}")
+            self.num_axes = len(left)
+            if interleaved:
+                axis_of_pair = []
+                while sum(left):
+                    for a, n in enumerate(left):
+                        if n:
+                            axis_of_pair.append(a)
+                            left[a] -= 1
+            else:
+                axis_of_pair = [a for a, n in enumerate(left) for _ in range(n)]
+        else:
+            if interleaved:
+                raise ValueError("interleaved goes with sections")
+            axis_of_pair = [int(a) for a in axis_of_pair]
+            if len(axis_of_pair) != half:
+                raise ValueError(f"axis_of_pair must have head_dim / 2 = {half} entries")
+            self.num_axes = max(axis_of_pair, default=0) + 1
+        if theta is None:
+            if not (base > 1.0 and base != float("inf")):
+                raise ValueError("base must be finite and > 1")
+            theta = [float(base) ** (-2.0 * p / head_dim) for p in range(half)]
+        elif len(theta) != half:
+            raise ValueError(f"theta must have head_dim / 2 = {half} entries")
+        self.head_dim, self.layout, self.axis_of_pair = head_dim, int(layout), axis_of_pair
+        self._c = AARopeAxes()
+        _check(lib().aa_rope_axes_init(ctypes.addressof(self._c), head_dim, self.num_axes, self.layout,
+                                       (ctypes.c_int32 * max(half, 1))(*axis_of_pair),
+                                       (ctypes.c_double * max(half, 1))(*[float(x) for x in theta])))
+        self._at = ctypes.addressof(self._c)
+
+    def _positions(self, pos, T, device):
+        if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype != torch.int32 or pos.device != device:
+            raise ValueError(f"pos must be an int32 tensor on {device}")
+        if pos.shape != (self.num_axes, T) and not (self.num_axes == 1 and pos.shape == (T,)):
+            raise ValueError(f"pos must have shape ({self.num_axes}, {T}), got {tuple(pos.shape)}")
+        return pos.contiguous()
+
+    def apply(self, pos, q, k=None, inverse=False, out_q=None, out_k=None, stream=None):
+        """Rotate q [T, Hq, D] (and k [T, Hk, D]) by pos, int32 [axes, T]; inverse=True turns back. Token strides of
+        slices are taken as they are; out_q = q works in place on a contiguous q."""
+        _check_tensor("q", q, (None, None, self.head_dim), torch.bfloat16)
+        T, dev = q.shape[0], q.device
+        if dev.index != torch.cuda.current_device():
+            raise ValueError(f"q is on {dev}, which is not the current device")
+        if k is not None:
+            _check_tensor("k", k, (T, None, self.head_dim), torch.bfloat16, dev)
+        elif out_k is not None:
+            raise ValueError("out_k goes with k")
+        with _on(stream):
+            pos = self._positions(pos, T, dev)
+            yq = _out("out_q", out_q, q)
+            yk = None if k is None else _out("out_k", out_k, k)
+            q, sq = _rows(q)
+            kp, sk, hk = None, 0, 0
+            if k is not None:
+                k, sk = _rows(k)
+                kp, hk = k.data_ptr(), k.shape[1]
+            _check(lib().aa_rope_axes_apply(self._at, pos.data_ptr(), T, q.data_ptr(), sq, yq.data_ptr(), q.shape[1], kp,
+                                            sk, None if k is None else yk.data_ptr(), hk, int(bool(inverse)),
+                                            _stream(stream)))
+        return yq if k is None else (yq, yk)
+
+
+class RopeAxesFn(torch.autograd.Function):
+    """The rotation is orthogonal: its gradient is the rotation back."""
+
+    @staticmethod
+    def forward(ctx, rope, pos, inverse, q, k):
+        ctx.rope, ctx.inverse = rope, inverse
+        ctx.save_for_backward(pos)
+        out = rope.apply(pos, q, k, inverse=inverse)
+        return (out, None) if k is None else out
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        (pos,) = ctx.saved_tensors
+        need_q, need_k = ctx.needs_input_grad[3:]
+        if need_q:
+            gq, gk = RopeAxesFn.apply(ctx.rope, pos, not ctx.inverse, gq, gk if need_k else None)
+        elif need_k:
+            gq, gk = None, RopeAxesFn.apply(ctx.rope, pos, not ctx.inverse, gk, None)[0]
+        return None, None, None, gq if need_q else None, gk if need_k else None
+
+
+def rope_axes(rope, pos, q, k=None):
+    """RopeAxes.apply as a differentiable op: q, or (q, k), rotated."""
+    yq, yk = RopeAxesFn.apply(rope, pos, False, q, k)
+    return yq if k is None else (yq, yk)

@@ -25,12 +25,32 @@ EXPORTS = ["aa_plan", "aa_plan_with_theta", "aa_plan_segments", "aa_plan_destroy
            "aa_rope_apply", "aa_fwd", "aa_fwd_workspace_bytes", "aa_bwd_workspace_bytes", "aa_bwd", "aa_bwd_from_fwd",
            "aa_bwd_from_fwd_workspace_bytes", "aa_bwd_static_workspace", "aa_check_device_error",
            "aa_set_wait_limit", "aa_set_bwd_timing_events", "aa_selftest_bounded_wait", "aa_status_string",
-           "aa_last_error", "aa_shift_diag_workspace_bytes", "aa_shift_diag", "aa_shard_plan"]
+           "aa_last_error", "aa_shift_diag_workspace_bytes", "aa_shift_diag", "aa_shard_plan",
+           "aa_rope_axes_init", "aa_rope_axes_apply", "aa_cache_create", "aa_cache_destroy", "aa_cache_resize",
+           "aa_cache_fork", "aa_cache_compact", "aa_cache_tables", "aa_cache_stats", "aa_cache_copy_pages",
+           "aa_cache_append", "aa_cache_attend", "aa_cache_attend_workspace_bytes", "aa_cache_check_error"]
 
 
 class AAShardPiece(ctypes.Structure):
     _fields_ = [("shard", ctypes.c_int32), ("doc", ctypes.c_int32), ("kv_head_begin", ctypes.c_int32),
                 ("kv_head_end", ctypes.c_int32), ("cost", ctypes.c_int64)]
+
+
+class AARopeAxes(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("ready", ctypes.c_int32), ("axis_of_pair", ctypes.c_int32 * 64), ("turn", ctypes.c_uint64 * 64)]
+
+
+class AACacheConfig(ctypes.Structure):
+    _fields_ = [("num_layers", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+                ("host_only", ctypes.c_int32)]
+
+
+class AACacheBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("num_seqs", ctypes.c_int32), ("table_width", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("layer", ctypes.c_int32)]
 
 
 class AAConfig(ctypes.Structure):
@@ -59,6 +79,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: run __graft_entry__.build() first")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64p = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)
+        i64 = ctypes.c_int64
         i32p = ctypes.POINTER(ctypes.c_int32)
         sig = {
             "aa_plan": ([ctypes.POINTER(AAConfig), i32p, i32, vp, ctypes.POINTER(vp)], ctypes.c_int),
@@ -87,6 +108,21 @@ def lib():
             "aa_shift_diag": ([vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp], ctypes.c_int),
             "aa_shard_plan": ([i32p, i32, i32, i32, i32, ctypes.POINTER(AAShardPiece), i32, i32p, i64p],
                               ctypes.c_int),
+            "aa_rope_axes_init": ([vp, i32, i32, i32, i32p, ctypes.POINTER(ctypes.c_double)], ctypes.c_int),
+            "aa_rope_axes_apply": ([vp, vp, i32, vp, i64, vp, i32, vp, i64, vp, i32, i32, vp], ctypes.c_int),
+            "aa_cache_create": ([vp, vp, vp, ctypes.POINTER(vp)], ctypes.c_int),
+            "aa_cache_destroy": ([vp], ctypes.c_int),
+            "aa_cache_resize": ([vp, i32p, i32p, i32, vp], ctypes.c_int),
+            "aa_cache_fork": ([vp, i32, i32], ctypes.c_int),
+            "aa_cache_compact": ([vp, vp, i32p], ctypes.c_int),
+            "aa_cache_tables": ([vp, i32p, i32, i32p, i32, i32p], ctypes.c_int),
+            "aa_cache_stats": ([vp, i32p, i32p, i32p], ctypes.c_int),
+            "aa_cache_copy_pages": ([vp, vp, vp, i32, vp], ctypes.c_int),
+            "aa_cache_append": ([vp, vp, vp, i64, vp, i64, vp, vp, vp, i64, vp, i32, vp], ctypes.c_int),
+            "aa_cache_attend": ([vp, vp, vp, i64, i32, i32, vp, i32, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp],
+                                ctypes.c_int),
+            "aa_cache_attend_workspace_bytes": ([vp, i32, i32, i32, i32, i32], ctypes.c_size_t),
+            "aa_cache_check_error": ([vp, vp], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
