@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libanchorattn.so")
 SOURCES = ["plan.cpp", "rope.cu", "fwd.cu", "bwd.cu", "bwd_static.cu", "shift_diag.cu", "segments.cu",
-           "rope_axes.cu", "cache.cpp", "cache_io.cu", "cache_attend.cu"]
+           "rope_axes.cu", "cache.cpp", "cache_io.cu", "cache_attend.cu",
+           "cache_attend_short.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

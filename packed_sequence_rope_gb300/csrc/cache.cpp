@@ -243,6 +243,9 @@ extern "C" aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, 
     // the clear runs on the legacy stream: done before any call on another one
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) st = cuda_fail(e, "cache set-up");
+    const int box = std::min(cfg->page_size, 64);
+    if (st == AA_OK) st = make_pool_map(&c->k_map64, k_pages, (int64_t)rows, cfg->head_dim, box);
+    if (st == AA_OK) st = make_pool_map(&c->v_map64, v_pages, (int64_t)rows, cfg->head_dim, box);
   }
   if (st != AA_OK) {
     if (c && c->err) cudaFree(c->err);

@@ -6,28 +6,19 @@
 //   visible keys: [max(key_lo, 0), p], and key 0 with the anchor (p >= 0)
 //   O_i = sum_j softmax_j(scale * q_i . k_j) v_j, LSE_i = ln sum_j exp(...)
 // in one pass with the running maximum and sum of the softmax.
+#include <algorithm>
 #include <cmath>
 
-#include "cache_common.cuh"
+#include "cache_attend.cuh"
 
 namespace aa {
 namespace {
 
-struct AttendParams {
-  BatchParams batch;
-  const __nv_bfloat16 *q, *k_pages, *v_pages;
-  __nv_bfloat16* o;
-  float* lse;
-  const int32_t* key_lo;
-  int64_t q_stride;
-  int Hq, group, anchor, page_shift;
-  float scale;
-};
-
 // One warp per (row, query head): each lane holds HD / 32 channels, the keys
 // come one after the other.
 template <int HD>
-__global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant__ AttendParams P) {
+__global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant__ AttendParams P,
+                                                          const __nv_bfloat16* k_pages, const __nv_bfloat16* v_pages) {
   constexpr int kPer = HD / 32;
   const BatchParams& b = P.batch;
   const int lane = threadIdx.x & 31;
@@ -51,18 +42,18 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
     if (!ok && lane == 0) atomicCAS(b.err, 0, kCacheBadPage);
     const int64_t row = ((((b.layer_page0 + page) * b.Hkv + g) << P.page_shift) + (j & ((1 << P.page_shift) - 1))) * HD;
     float s = 0.f;
-    for (int e = 0; e < kPer; ++e) s += ok ? q[e] * __bfloat162float(P.k_pages[row + lane * kPer + e]) : 0.f;
+    for (int e = 0; e < kPer; ++e) s += ok ? q[e] * __bfloat162float(k_pages[row + lane * kPer + e]) : 0.f;
     for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= P.scale;
-    const float mn = fmaxf(m, s), f = expf(m - mn), w_j = expf(s - mn);
+    s *= P.scale_log2;
+    const float mn = fmaxf(m, s), f = exp2f(m - mn), w_j = exp2f(s - mn);
     m = mn;
     l = l * f + w_j;
     for (int e = 0; e < kPer; ++e)
-      acc[e] = acc[e] * f + (ok ? w_j * __bfloat162float(P.v_pages[row + lane * kPer + e]) : 0.f);
+      acc[e] = acc[e] * f + (ok ? w_j * __bfloat162float(v_pages[row + lane * kPer + e]) : 0.f);
   }
   for (int e = 0; e < kPer; ++e)
     P.o[((int64_t)t * P.Hq + h) * HD + lane * kPer + e] = __float2bfloat16(l > 0.f ? acc[e] / l : 0.f);
-  if (P.lse && lane == 0) P.lse[(int64_t)h * b.T + t] = m + logf(l);
+  if (P.lse && lane == 0) P.lse[(int64_t)h * b.T + t] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -86,6 +77,8 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   const int D = c->cfg.head_dim, Hkv = c->cfg.num_kv_heads, T = batch->total_tokens;
   if (q_heads < 1 || q_heads % Hkv || q_heads / Hkv > 64)
     return fail(AA_ERR_INVALID_ARG, "q_heads must be a multiple of Hkv, at most 64 per kv head");
+  if ((int64_t)batch->num_seqs * Hkv >= (1 << 27))
+    return fail(AA_ERR_INVALID_ARG, "num_seqs * Hkv must stay below 2^27");
   if (max_q < 0) return fail(AA_ERR_INVALID_ARG, "max_q must be >= 0");
   if ((int64_t)q_heads * T >= (1ll << 31)) return fail(AA_ERR_INVALID_ARG, "q_heads * total_tokens must stay below 2^31");
   if (!std::isfinite(softmax_scale)) return fail(AA_ERR_INVALID_ARG, "softmax_scale is not finite");
@@ -104,8 +97,6 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   AttendParams P;
   P.batch = batch_params(c, batch);
   P.q = static_cast<const __nv_bfloat16*>(q);
-  P.k_pages = static_cast<const __nv_bfloat16*>(c->k_pages);
-  P.v_pages = static_cast<const __nv_bfloat16*>(c->v_pages);
   P.o = static_cast<__nv_bfloat16*>(o);
   P.lse = lse;
   P.key_lo = key_lo;
@@ -114,13 +105,19 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   P.group = q_heads / Hkv;
   P.anchor = anchor != 0;
   P.page_shift = __builtin_ctz((unsigned)c->cfg.page_size);
-  P.scale = softmax_scale > 0.f ? softmax_scale : (float)(1.0 / std::sqrt((double)D));
+  P.scale_log2 = (float)((softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((int64_t)std::max(max_q, 1) * P.group <= kShortRows) {
+    cudaError_t e = launch_attend_short(c, P, max_q, s);
+    return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
+  }
   const unsigned grid = (unsigned)(((int64_t)T * q_heads + 3) / 4);
+  const auto* kp = static_cast<const __nv_bfloat16*>(c->k_pages);
+  const auto* vp = static_cast<const __nv_bfloat16*>(c->v_pages);
   if (D == 128)
-    attend_rows_kernel<128><<<grid, 128, 0, s>>>(P);
+    attend_rows_kernel<128><<<grid, 128, 0, s>>>(P, kp, vp);
   else
-    attend_rows_kernel<64><<<grid, 128, 0, s>>>(P);
+    attend_rows_kernel<64><<<grid, 128, 0, s>>>(P, kp, vp);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_rows_kernel launch");
 }

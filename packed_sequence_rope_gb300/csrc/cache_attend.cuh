@@ -1,0 +1,72 @@
+// What the kernels of aa_cache_attend share: parameters, the keys that a group
+// of rows visits, and where those keys lie in the pool.
+#pragma once
+
+#include "cache_common.cuh"
+
+namespace aa {
+
+constexpr uint64_t kAttendWaitNs = 2000000000ull;  // limit of every wait on a copy or a product
+
+struct AttendParams {
+  BatchParams batch;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  const int32_t* key_lo;
+  int64_t q_stride;
+  int Hq, group, anchor, page_shift;
+  float scale_log2;    // softmax scale * log2 e
+};
+
+// New tokens [q0, q0 + n) of sequence b that hold kv tokens. Rows outside the
+// tensors are cut off, whatever cu_q says.
+struct SeqSpan {
+  int q0, n, kv;
+};
+__device__ __forceinline__ SeqSpan load_seq(const BatchParams& b, int seq) {
+  SeqSpan s;
+  s.q0 = __ldg(b.cu_q + seq);
+  s.n = min(__ldg(b.cu_q + seq + 1), b.T) - s.q0;
+  s.kv = __ldg(b.kv_len + seq);
+  if (s.q0 < 0 || s.n < 0) s.n = 0;
+  return s;
+}
+
+// The key tiles (kKeys wide) that rows with first keys >= lo and positions <=
+// hi visit: [lo, hi], and before them tile 0 if only the anchor lies there.
+template <int kKeys>
+struct KeyTiles {
+  int first, count, anchor_tile;
+  __device__ __forceinline__ KeyTiles(int lo, int hi, bool anchor) {
+    first = lo / kKeys;
+    const int in = lo <= hi ? hi / kKeys - first + 1 : 0;
+    anchor_tile = (anchor && hi >= 0 && (in == 0 || first > 0)) ? 1 : 0;
+    count = in + anchor_tile;
+  }
+  __device__ __forceinline__ int tile(int i) const { return i < anchor_tile ? 0 : first + i - anchor_tile; }
+};
+
+// Pool row of the page that holds position j of sequence b for head g; a row
+// outside the pool (which a tensor copy fills with zeros) if there is none.
+constexpr int kNoRow = -128;
+__device__ __forceinline__ int pool_row(const BatchParams& b, int seq, int g, int j, int page_shift) {
+  const int w = j >> page_shift;
+  if (w >= b.W) {
+    atomicCAS(b.err, 0, kCacheBadPosition);
+    return kNoRow;
+  }
+  const int page = __ldg(b.table + (int64_t)seq * b.W + w);
+  if (page < 0 || page >= b.num_pages) {
+    atomicCAS(b.err, 0, kCacheBadPage);
+    return kNoRow;
+  }
+  return (int)((((b.layer_page0 + page) * b.Hkv + g) << page_shift) + (j & ((1 << page_shift) - 1)));
+}
+
+// Launchers (arguments already checked).
+// short: at most kShortRows rows (max_q * group) of a sequence and kv head at a time.
+constexpr int kShortRows = 64;
+cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int max_q, cudaStream_t s);
+
+}  // namespace aa

@@ -18,6 +18,9 @@ struct aa_cache_s {
   int device = 0, num_sms = 0;
   void *k_pages = nullptr, *v_pages = nullptr;
   int32_t* err = nullptr;        // device error word (0 = ok)
+  // the pool as [num_layers * num_pages * Hkv * page_size, D] rows, in boxes of
+  // a page's rows (at most 64) by 64 channels
+  CUtensorMap k_map64, v_map64;
   std::vector<aa_cache_seq> seqs;
   std::vector<int32_t> refs;     // [num_pages] sequences holding the page
   std::vector<int32_t> free;     // pages with refs == 0, the lowest last
@@ -38,6 +41,10 @@ struct PagePair {
   int32_t src, dst;
 };
 aa_status launch_copy_pages(const aa_cache_s* c, const std::vector<PagePair>& pairs, cudaStream_t s);
+
+// Tensor map over the pool's rows [rows, D], box {64, box_rows}, 128-byte
+// swizzle (rope.cu).
+aa_status make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int D, int box_rows);
 
 // Checks shared with aa_rope_axes_apply (rope_axes.cu).
 size_t rows_span(int64_t T, int64_t stride, int H, int D);
