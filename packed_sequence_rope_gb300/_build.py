@@ -14,7 +14,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libanchorattn.so")
 SOURCES = ["plan.cpp", "rope.cu", "fwd.cu", "bwd.cu", "bwd_static.cu", "shift_diag.cu", "segments.cu",
            "rope_axes.cu", "cache.cpp", "cache_io.cu", "cache_attend.cu",
-           "cache_attend_short.cu"]
+           "cache_attend_short.cu", "cache_attend_chunk.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -5,66 +5,26 @@
 // "AnchorAttention: The Shared Anchor Design", "Mask construction"):
 //   visible keys: [max(key_lo, 0), p], and key 0 with the anchor (p >= 0)
 //   O_i = sum_j softmax_j(scale * q_i . k_j) v_j, LSE_i = ln sum_j exp(...)
-// in one pass with the running maximum and sum of the softmax.
+// in one pass with the running maximum and sum of the softmax. This file checks the
+// arguments and chooses between cache_attend_short.cu (few rows per sequence: the
+// keys are read once, HBM-bound) and cache_attend_chunk.cu (tcgen05 products).
 #include <algorithm>
 #include <cmath>
 
 #include "cache_attend.cuh"
 
-namespace aa {
-namespace {
-
-// One warp per (row, query head): each lane holds HD / 32 channels, the keys
-// come one after the other.
-template <int HD>
-__global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant__ AttendParams P,
-                                                          const __nv_bfloat16* k_pages, const __nv_bfloat16* v_pages) {
-  constexpr int kPer = HD / 32;
-  const BatchParams& b = P.batch;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(item / P.Hq), h = (int)(item % P.Hq);
-  if (t >= b.T || t < __ldg(b.cu_q) || t >= __ldg(b.cu_q + b.B)) return;
-  const int seq = warp_find_seq(b.cu_q, b.B, t);
-  const int p = __ldg(b.kv_len + seq) - __ldg(b.cu_q + seq + 1) + t;
-  const int lo = P.key_lo ? max(__ldg(P.key_lo + t), 0) : 0;
-  const int g = h / P.group;
-  float q[kPer], acc[kPer] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < kPer; ++e) q[e] = __bfloat162float(P.q[t * P.q_stride + (int64_t)h * HD + lane * kPer + e]);
-  for (int j = P.anchor ? 0 : lo; j <= p; j = j == 0 ? max(lo, 1) : j + 1) {
-    const int w = j >> P.page_shift;
-    if (w >= b.W) {
-      if (lane == 0) atomicCAS(b.err, 0, kCacheBadPosition);
-      break;
-    }
-    const int page = __ldg(b.table + (int64_t)seq * b.W + w);
-    const bool ok = page >= 0 && page < b.num_pages;
-    if (!ok && lane == 0) atomicCAS(b.err, 0, kCacheBadPage);
-    const int64_t row = ((((b.layer_page0 + page) * b.Hkv + g) << P.page_shift) + (j & ((1 << P.page_shift) - 1))) * HD;
-    float s = 0.f;
-    for (int e = 0; e < kPer; ++e) s += ok ? q[e] * __bfloat162float(k_pages[row + lane * kPer + e]) : 0.f;
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= P.scale_log2;
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w_j = exp2f(s - mn);
-    m = mn;
-    l = l * f + w_j;
-    for (int e = 0; e < kPer; ++e)
-      acc[e] = acc[e] * f + (ok ? w_j * __bfloat162float(v_pages[row + lane * kPer + e]) : 0.f);
-  }
-  for (int e = 0; e < kPer; ++e)
-    P.o[((int64_t)t * P.Hq + h) * HD + lane * kPer + e] = __float2bfloat16(l > 0.f ? acc[e] / l : 0.f);
-  if (P.lse && lane == 0) P.lse[(int64_t)h * b.T + t] = (m + log2f(l)) * 0.69314718055994531f;
-}
-
-}  // namespace
-}  // namespace aa
-
 using namespace aa;
+
+// The kernel for single and few tokens as long as its row tile holds them.
+static bool takes_short(int max_q, int group) { return (int64_t)std::max(max_q, 1) * group <= kShortRows; }
 
 extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
                                                   int32_t table_width, int32_t q_heads) {
   if (!c || num_seqs < 1 || total_tokens < 0 || max_q < 0 || table_width < 1 || q_heads < 1) return 0;
-  return 256;
+  const int Hkv = c->cfg.num_kv_heads;
+  if (c->host_only || q_heads % Hkv || q_heads / Hkv > 64) return 0;
+  if (takes_short(max_q, q_heads / Hkv)) return 256;
+  return chunk_workspace_bytes(c, num_seqs, total_tokens, q_heads / Hkv);
 }
 
 extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, const void* q, int64_t q_stride,
@@ -107,17 +67,7 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   P.page_shift = __builtin_ctz((unsigned)c->cfg.page_size);
   P.scale_log2 = (float)((softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((int64_t)std::max(max_q, 1) * P.group <= kShortRows) {
-    cudaError_t e = launch_attend_short(c, P, max_q, s);
-    return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
-  }
-  const unsigned grid = (unsigned)(((int64_t)T * q_heads + 3) / 4);
-  const auto* kp = static_cast<const __nv_bfloat16*>(c->k_pages);
-  const auto* vp = static_cast<const __nv_bfloat16*>(c->v_pages);
-  if (D == 128)
-    attend_rows_kernel<128><<<grid, 128, 0, s>>>(P, kp, vp);
-  else
-    attend_rows_kernel<64><<<grid, 128, 0, s>>>(P, kp, vp);
-  cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_rows_kernel launch");
+  if (!takes_short(max_q, P.group)) return launch_attend_chunk(c, P, workspace, s);
+  cudaError_t e = launch_attend_short(c, P, max_q, s);
+  return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
 }

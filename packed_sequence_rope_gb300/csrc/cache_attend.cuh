@@ -20,16 +20,21 @@ struct AttendParams {
 };
 
 // New tokens [q0, q0 + n) of sequence b that hold kv tokens. Rows outside the
-// tensors are cut off, whatever cu_q says.
+// tensors are cut off, whatever cu_q says; more tokens than the page table has
+// room for are an error, and the rest is not visited.
 struct SeqSpan {
   int q0, n, kv;
 };
-__device__ __forceinline__ SeqSpan load_seq(const BatchParams& b, int seq) {
+__device__ __forceinline__ SeqSpan load_seq(const BatchParams& b, int seq, int page_shift) {
   SeqSpan s;
   s.q0 = __ldg(b.cu_q + seq);
   s.n = min(__ldg(b.cu_q + seq + 1), b.T) - s.q0;
-  s.kv = __ldg(b.kv_len + seq);
+  s.kv = max(__ldg(b.kv_len + seq), 0);
   if (s.q0 < 0 || s.n < 0) s.n = 0;
+  if (s.n > 0 && s.kv > b.W << page_shift) {
+    atomicCAS(b.err, 0, kCacheBadPosition);
+    s.kv = b.W << page_shift;
+  }
   return s;
 }
 
@@ -48,15 +53,11 @@ struct KeyTiles {
 };
 
 // Pool row of the page that holds position j of sequence b for head g; a row
-// outside the pool (which a tensor copy fills with zeros) if there is none.
+// outside the pool (which a tensor copy fills with zeros) if there is none. j lies
+// in [0, the sequence's kv).
 constexpr int kNoRow = -128;
 __device__ __forceinline__ int pool_row(const BatchParams& b, int seq, int g, int j, int page_shift) {
-  const int w = j >> page_shift;
-  if (w >= b.W) {
-    atomicCAS(b.err, 0, kCacheBadPosition);
-    return kNoRow;
-  }
-  const int page = __ldg(b.table + (int64_t)seq * b.W + w);
+  const int page = __ldg(b.table + (int64_t)seq * b.W + (j >> page_shift));  // j < kv <= W * page size
   if (page < 0 || page >= b.num_pages) {
     atomicCAS(b.err, 0, kCacheBadPage);
     return kNoRow;
@@ -68,5 +69,7 @@ __device__ __forceinline__ int pool_row(const BatchParams& b, int seq, int g, in
 // short: at most kShortRows rows (max_q * group) of a sequence and kv head at a time.
 constexpr int kShortRows = 64;
 cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int max_q, cudaStream_t s);
+aa_status launch_attend_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
+size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int group);
 
 }  // namespace aa

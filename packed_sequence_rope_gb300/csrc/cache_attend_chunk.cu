@@ -1,0 +1,678 @@
+// Attention of chunks of new tokens over the paged cache (prompts, and any
+// batch with more rows per sequence than cache_attend_short.cu takes).
+//
+// Rows are packed: row r of a 128-row tile is (token r / group, query head
+// r % group) of one kv head, so a grouped-query layer fills the tensor cores'
+// 128 rows with 128 / group tokens and reads each key once for the group. A unit
+// of work is two such row tiles of one sequence and kv head; its keys come in
+// tiles of 128. Three kernels:
+//   chunk_plan_kernel     one CTA: each unit's key tiles and their running sum,
+//                         from the lengths and key_lo on the device
+//   attend_chunk_kernel   persistent, one CTA per SM. All key tiles of all
+//                         units, laid end to end, are cut into equal shares, one per
+//                         CTA: the SMs finish together whatever the lengths. A
+//                         share's first and last unit may be cut; their partial
+//                         results (fp32, with the rows' maximum and sum) go to the
+//                         workspace
+//   chunk_join_kernel     joins the partial results of each cut unit, in order
+// The second and third are launched as programmatic dependents, so that their
+// start-up overlaps the kernel before them.
+//
+// Roles in attend_chunk_kernel (384 threads), as in the packed forward:
+//   warp 0      finds the CTA's next piece of work and copies its query tiles and
+//               the key tiles' pages (tensor copies, one page piece per lane)
+//   warp 1      owns tensor memory and issues the products
+//   warp 2      clears values that no row sees (a page's unused rows)
+//   warps 4-7   row tile 0: online softmax (thread = row = TMEM lane), epilogue
+//   warps 8-11  the same for row tile 1
+// Tensor memory: S0 [0, 128), S1 [128, 256), O0, O1 (D columns each); P replaces
+// the first half of its S as packed bf16 and feeds P V from there. The issue order
+// S0(j), PV1(j - 1), S1(j), PV0(j) keeps the tensor cores busy with one tile while
+// the other's softmax runs.
+#include <algorithm>
+
+#include "cache_attend.cuh"
+
+namespace aa {
+namespace {
+
+constexpr int kKeys = 128;
+constexpr int kThreads = 384;
+constexpr int kReaders = 10;  // of a published piece: the MMA thread, warp 2, eight softmax warps
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
+constexpr uint64_t kDrainNs = 1000000000ull;
+constexpr int kMinShare = 2;  // key tiles a CTA takes at least
+
+// A unit as chunk_plan_kernel describes it: tokens [i0, i0 + tokens) of a
+// sequence, their positions [p0, p0 + tokens), the first key any of them sees.
+struct Unit {
+  int32_t seq, q_row, tokens, p0, lo;
+};
+
+struct ChunkParams {
+  AttendParams a;
+  int tile_tokens;     // tokens per row tile: 128 / group
+  int slots;           // room for the units of one kv head
+  int64_t* tiles_end;  // [slots + 1] running sum of the units' key tiles; [0] = 0
+  Unit* units;         // [slots]
+  float4* part_o;      // [CTA][2][row tile][D / 4][128]: unnormalised O of a cut unit
+  float2* part_ml;     // [CTA][2][row tile][128]: maximum (log2 units), sum
+};
+
+// ---------------------------------------------------------------- the plan
+// Sequence b's units start at slot cu_q[b] / (2 tile_tokens) + b, which leaves
+// room for a rounded-up count and needs no scan over the sequences before it.
+__global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant__ ChunkParams C) {
+  const AttendParams& P = C.a;
+  const BatchParams& b = P.batch;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int unit_tokens = 2 * C.tile_tokens;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int slot = warp; slot < C.slots; slot += 32) {
+    const int seq = warp_last(b.B, [&](int i) { return __ldg(b.cu_q + i) / unit_tokens + i <= slot; });
+    const SeqSpan s = load_seq(b, seq, P.page_shift);
+    const int64_t i0 = (int64_t)(slot - __ldg(b.cu_q + seq) / unit_tokens - seq) * unit_tokens;
+    Unit u{seq, 0, 0, 0, 0};
+    int count = 0;
+    if (i0 >= 0 && i0 < s.n) {
+      u.q_row = s.q0 + (int)i0;
+      u.tokens = min(unit_tokens, s.n - (int)i0);
+      u.p0 = s.kv - s.n + (int)i0;
+      if (P.key_lo) {
+        int lo = INT_MAX;
+        for (int i = lane; i < u.tokens; i += 32) lo = min(lo, max(__ldg(P.key_lo + u.q_row + i), 0));
+        u.lo = __reduce_min_sync(0xffffffffu, lo);
+      }
+      // rows that see nothing are written too: at least one tile
+      count = max(KeyTiles<kKeys>(u.lo, u.p0 + u.tokens - 1, P.anchor).count, 1);
+    }
+    if (lane == 0) {
+      C.units[slot] = u;
+      C.tiles_end[slot + 1] = count;
+    }
+  }
+  __syncthreads();
+  __shared__ int64_t sums[32];
+  int64_t carry = 0;
+  if (threadIdx.x == 0) C.tiles_end[0] = 0;
+  for (int base = 0; base < C.slots; base += 1024) {
+    const int slot = base + (int)threadIdx.x;
+    int64_t v = slot < C.slots ? C.tiles_end[slot + 1] : 0;
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += up;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      int64_t w = sums[lane];
+      for (int d = 1; d < 32; d *= 2) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, w, d);
+        if (lane >= d) w += up;
+      }
+      sums[lane] = w;
+    }
+    __syncthreads();
+    v += carry + (warp ? sums[warp - 1] : 0);
+    if (slot < C.slots) C.tiles_end[slot + 1] = v;
+    carry += sums[31];
+    __syncthreads();
+  }
+}
+
+// How the key tiles of all heads are shared out, and which unit a tile belongs
+// to: tile numbers run over (kv head, slot, tile of the unit).
+struct Shares {
+  int64_t all, share, per_head;
+  __device__ __forceinline__ Shares(const ChunkParams& C, int ctas) {
+    per_head = C.tiles_end[C.slots];
+    all = per_head * C.a.batch.Hkv;
+    share = max((all + ctas - 1) / ctas, (int64_t)kMinShare);
+  }
+  // kv head, slot and first tile number of the unit that holds tile `at` (whole warp)
+  __device__ __forceinline__ void find(const ChunkParams& C, int64_t at, int* g, int* slot, int64_t* begin, int* count) const {
+    *g = (int)(at / per_head);
+    const int64_t rem = at - *g * per_head;
+    *slot = warp_last(C.slots, [&](int i) { return C.tiles_end[i] <= rem; });
+    const int64_t e0 = C.tiles_end[*slot];
+    *begin = *g * per_head + e0;
+    *count = (int)(C.tiles_end[*slot + 1] - e0);
+  }
+};
+
+// ---------------------------------------------------------------- attention
+// One piece of work: key tiles [first, first + take) of a unit's `count`.
+struct Piece {
+  int valid, g, seq, q_row, tokens, p0, lo;
+  int first, take, whole;  // whole: the unit is not cut
+  int part;                // else: which of the CTA's two partial results
+};
+
+template <int HD>
+struct ChunkSmem {
+  static constexpr int kB = HD / 64;
+  static constexpr int kStages = HD == 128 ? 2 : 4;
+  alignas(1024) uint8_t q[2][kB][16384];
+  alignas(1024) uint8_t k[kStages][kB][16384];
+  alignas(1024) uint8_t v[kStages][kB][16384];
+  uint64_t q_full[2], q_free[2];
+  uint64_t piece_full[2], piece_empty[2];
+  uint64_t kv_full[kStages], v_clean[kStages], kv_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  Piece piece[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort_flag,
+                                              int site) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (ptx::global_timer_ns() - t0 >= kAttendWaitNs) {
+      atomicCAS(err, 0, site);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// The li-th piece of this CTA, or false when there is none left.
+template <class Smem>
+__device__ __forceinline__ bool read_piece(Smem& sm, int li, int32_t* err, volatile int* abort_flag, bool warp_read,
+                                           int site, Piece* out) {
+  bool ok = wait_or_abort(&sm.piece_full[li & 1], (li >> 1) & 1, err, abort_flag, site);
+  if (warp_read) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) return false;
+  *out = sm.piece[li & 1];
+  if (warp_read) __syncwarp();
+  if (!warp_read || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&sm.piece_empty[li & 1]);
+  return out->valid != 0;
+}
+
+// Barrier phases: pieces count the piece ring; the K/V ring counts the CTA's
+// key tiles over all its pieces; s_full / p_full count each row tile's
+// softmax steps; q_full, q_free and o_full the pieces in which the row tile
+// exists. As in the packed forward every wait is bounded and its outcome made
+// uniform in a warp before anything collective.
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ChunkParams C) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  constexpr int kB = HD / 64, kStages = ChunkSmem<HD>::kStages, kTmemCols = 512;
+  constexpr uint32_t kStageBytes = 2 * kKeys * HD * 2;
+  const AttendParams& P = C.a;
+  const BatchParams& b = P.batch;
+  if (ptx::smem_u32(smem_raw) & 1023u) {  // swizzled tiles need a 1 KB aligned base
+    if (threadIdx.x == 0) atomicCAS(b.err, 0, 498);
+    return;
+  }
+  ChunkSmem<HD>& sm = *reinterpret_cast<ChunkSmem<HD>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &sm.abort_flag;
+
+  if (tid == 0) {
+    ptx::tma_prefetch_desc(&tmQ);
+    ptx::tma_prefetch_desc(&tmK);
+    ptx::tma_prefetch_desc(&tmV);
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(&sm.q_full[t], 1);
+      ptx::mbar_init(&sm.q_free[t], 128);
+      ptx::mbar_init(&sm.s_full[t], 1);
+      ptx::mbar_init(&sm.p_full[t], 128);
+      ptx::mbar_init(&sm.o_full[t], 1);
+      ptx::mbar_init(&sm.piece_full[t], 1);
+      ptx::mbar_init(&sm.piece_empty[t], kReaders);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&sm.kv_full[s], 1);
+      ptx::mbar_init(&sm.v_clean[s], 1);
+      ptx::mbar_init(&sm.kv_empty[s], 1);
+    }
+    ptx::mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) ptx::tmem_alloc(&sm.tmem_base, kTmemCols);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan, and everything before it
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const Shares shares(C, gridDim.x);
+    int64_t at = shares.share * blockIdx.x;
+    const int64_t end = min(at + shares.share, shares.all);
+    int nq[2] = {0, 0}, ks = 0;
+    bool ok = true;
+    // a key tile is `pieces` page pieces, each kB column blocks of K and V
+    const int piece_shift = min(P.page_shift, 6), pieces = kKeys >> piece_shift;
+    const int copies = pieces * kB * 2;  // at most 32: one per lane
+    const int part = lane & (pieces - 1), block = (lane / pieces) % kB;
+    const bool is_v = lane >= pieces * kB;
+    for (int li = 0; ok; ++li) {
+      if (li >= 2) ok = __all_sync(0xffffffffu, wait_or_abort(&sm.piece_empty[li & 1], ((li >> 1) - 1) & 1, b.err, abort_flag, 452));
+      if (!ok) break;
+      Piece w{};
+      if (at < end) {
+        int slot, count;
+        int64_t begin;
+        shares.find(C, at, &w.g, &slot, &begin, &count);
+        const Unit u = C.units[slot];
+        w.valid = 1;
+        w.seq = u.seq;
+        w.q_row = u.q_row;
+        w.tokens = u.tokens;
+        w.p0 = u.p0;
+        w.lo = u.lo;
+        w.first = (int)(at - begin);
+        w.take = (int)min((int64_t)(count - w.first), end - at);
+        w.whole = w.take == count;
+        w.part = w.first == 0 ? 1 : 0;  // a cut unit starts in at most one share and ends in at most one
+        at += w.take;
+      }
+      if (lane == 0) {
+        sm.piece[li & 1] = w;
+        ptx::mbar_arrive(&sm.piece_full[li & 1]);
+      }
+      __syncwarp();
+      if (!w.valid) break;
+      const int hi = w.p0 + w.tokens - 1;
+      const KeyTiles<kKeys> keys(w.lo, hi, P.anchor);
+      auto row_of = [&](int i) {
+        const int j = keys.tile(i) * kKeys + (part << piece_shift);
+        // pieces that no row sees are not looked up
+        const bool seen = j <= hi && (j + (1 << piece_shift) > w.lo || (j == 0 && P.anchor));
+        return lane < copies && i < w.first + w.take && i < keys.count && seen ? pool_row(b, w.seq, w.g, j, P.page_shift)
+                                                                               : kNoRow;
+      };
+      int next = row_of(w.first);
+      for (int t = 0; t < (w.tokens > C.tile_tokens ? 2 : 1) && ok; ++t) {
+        // the tile's previous Q has had its last S product
+        if (nq[t] > 0)
+          ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_free[t], (nq[t] - 1) & 1, b.err, abort_flag, 450));
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&sm.q_full[t], (uint32_t)(C.tile_tokens * P.group * HD * 2));
+          for (int c = 0; c < kB; ++c)
+            ptx::tma_load_4d(sm.q[t][c], &tmQ, &sm.q_full[t], c * 64, 0, w.g, w.q_row + t * C.tile_tokens);
+        }
+        __syncwarp();
+        ++nq[t];
+      }
+      for (int i = w.first; i < w.first + w.take && ok; ++i) {
+        const int s = ks % kStages, row = next;
+        next = row_of(i + 1);  // in flight while this stage is waited for
+        if (ks >= kStages)
+          ok = __all_sync(0xffffffffu, wait_or_abort(&sm.kv_empty[s], ((ks / kStages) - 1) & 1, b.err, abort_flag, 451));
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.kv_full[s], kStageBytes);
+        __syncwarp();
+        if (lane < copies) {
+          uint8_t* dst = (is_v ? sm.v[s][block] : sm.k[s][block]) + (part << piece_shift) * 128;
+          ptx::tma_load_2d(dst, is_v ? &tmV : &tmK, &sm.kv_full[s], block * 64, row);
+        }
+        ++ks;
+      }
+    }
+    // every issued copy lands before the CTA exits
+    for (int t = 0; t < 2; ++t)
+      if (nq[t] > 0) ptx::mbar_wait(&sm.q_full[t], (nq[t] - 1) & 1, kDrainNs, b.err, 459);
+    for (int u = max(ks - kStages, 0); u < ks; ++u)
+      ptx::mbar_wait(&sm.kv_full[u % kStages], (u / kStages) & 1, kDrainNs, b.err, 459);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, 0, 1);
+      const uint32_t t_s[2] = {tmem, tmem + 128}, t_o[2] = {tmem + 256, tmem + 256 + HD};
+      uint32_t ph_p[2] = {0, 0};
+      int nq[2] = {0, 0}, ks = 0;
+      bool first_pv[2] = {true, true}, ready[2] = {false, false};
+      auto issue_s = [&](int t, int s) -> bool {
+        if (!ready[t]) {  // this piece's Q tile t has landed (first use only)
+          if (!wait_or_abort(&sm.q_full[t], nq[t] & 1, b.err, abort_flag, 462)) return false;
+          ready[t] = true;
+          ptx::tc_fence_after();
+        }
+        const uint64_t qd = ptx::smem_desc_sw128(ptx::smem_u32(sm.q[t][0]), 16, 1024);
+        const uint64_t kd = ptx::smem_desc_sw128(ptx::smem_u32(sm.k[s][0]), 16, 1024);
+        if constexpr (HD == 128)
+          ptx::mma8_ss_kk(t_s[t], qd, kd, idesc_s, 0);
+        else
+          ptx::mma4_ss_kk(t_s[t], qd, kd, idesc_s, 0);
+        ptx::mma_commit(&sm.s_full[t]);
+        return true;
+      };
+      auto issue_pv = [&](int t, int n) -> bool {
+        const int s = n % kStages;
+        if (!wait_or_abort(&sm.v_clean[s], (n / kStages) & 1, b.err, abort_flag, 464)) return false;
+        if (!wait_or_abort(&sm.p_full[t], ph_p[t], b.err, abort_flag, 461)) return false;
+        ph_p[t] ^= 1;
+        ptx::tc_fence_after();
+        ptx::mma8_ts_seq(t_o[t], t_s[t], ptx::smem_desc_sw128(ptx::smem_u32(sm.v[s][0]), 16384, 1024), idesc_pv,
+                         first_pv[t] ? 0u : 1u);
+        first_pv[t] = false;
+        return true;
+      };
+      bool ok = true;
+      for (int li = 0; ok; ++li) {
+        Piece w;
+        if (!read_piece(sm, li, b.err, abort_flag, false, 460, &w)) break;
+        const bool has1 = w.tokens > C.tile_tokens;
+        first_pv[0] = first_pv[1] = true;
+        ready[0] = false;
+        ready[1] = !has1;
+        for (int i = 0; i < w.take && ok; ++i, ++ks) {
+          const int s = ks % kStages;
+          if (!(ok = wait_or_abort(&sm.kv_full[s], (ks / kStages) & 1, b.err, abort_flag, 463))) break;
+          ptx::tc_fence_after();
+          if (!(ok = issue_s(0, s))) break;
+          if (i > 0) {
+            if (has1 && !(ok = issue_pv(1, ks - 1))) break;
+            ptx::mma_commit(&sm.kv_empty[(ks - 1) % kStages]);
+          }
+          if (has1 && !(ok = issue_s(1, s))) break;
+          if (!(ok = issue_pv(0, ks))) break;
+          if (i == w.take - 1) ptx::mma_commit(&sm.o_full[0]);
+        }
+        if (ok && has1) {
+          ok = issue_pv(1, ks - 1);
+          if (ok) ptx::mma_commit(&sm.o_full[1]);
+        }
+        if (ok) ptx::mma_commit(&sm.kv_empty[(ks - 1) % kStages]);
+        ++nq[0];
+        if (has1) ++nq[1];
+      }
+      // every issued MMA must finish before TMEM is released
+      ptx::mma_commit(&sm.drain);
+      ptx::mbar_wait(&sm.drain, 0, kDrainNs, b.err, 469);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ clearing unseen values
+    // the rows of V that no row of the unit sees have weight 0, but 0 * NaN is not
+    int ks = 0;
+    bool ok = true;
+    for (int li = 0; ok; ++li) {
+      Piece w;
+      if (!read_piece(sm, li, b.err, abort_flag, true, 470, &w)) break;
+      const int hi = w.p0 + w.tokens - 1;
+      const KeyTiles<kKeys> keys(w.lo, hi, P.anchor);
+      for (int i = w.first; i < w.first + w.take; ++i, ++ks) {
+        const int s = ks % kStages;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&sm.kv_full[s], (ks / kStages) & 1, b.err, abort_flag, 471));
+        if (!ok) break;
+        const int j0 = keys.tile(i) * kKeys;
+        if (j0 < w.lo || j0 + kKeys - 1 > hi) {
+          for (int x = lane; x < kKeys * kB * 8; x += 32) {
+            const int key = x / (kB * 8), j = j0 + key;
+            if (!((j >= w.lo && j <= hi) || (j == 0 && P.anchor)))
+              *reinterpret_cast<uint4*>(sm.v[s][(x >> 3) % kB] + key * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) ptx::mbar_arrive(&sm.v_clean[s]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2, r = tid & 127;
+    const float sl2 = P.scale_log2;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + 128 * t + lane_off, t_o = tmem + 256 + HD * t + lane_off;
+    uint32_t ph_s = 0;
+    int nq = 0;
+    bool ok = true;
+    for (int li = 0; ok; ++li) {
+      Piece w;
+      if (!read_piece(sm, li, b.err, abort_flag, true, 480, &w)) break;
+      if (t == 1 && w.tokens <= C.tile_tokens) continue;
+      const KeyTiles<kKeys> keys(w.lo, w.p0 + w.tokens - 1, P.anchor);
+      const int in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
+      const bool row_valid = in_tile < C.tile_tokens && tok < w.tokens;
+      const int lo = row_valid ? (P.key_lo ? max(__ldg(P.key_lo + w.q_row + tok), 0) : 0) : 1;
+      const int hi = row_valid ? w.p0 + tok : 0;
+      const bool anchored = P.anchor && row_valid && hi >= 0;
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < w.take; ++i) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&sm.s_full[t], ph_s, b.err, abort_flag, 482));
+        if (!ok) break;
+        ph_s ^= 1;
+        ptx::tc_fence_after();
+        // the piece's last S product of this tile is done: Q may be replaced
+        if (i == w.take - 1) ptx::mbar_arrive(&sm.q_free[t]);
+        const int j0 = keys.tile(w.first + i) * kKeys;
+        // tiles every row of the warp sees entirely skip the per-element mask
+        const bool full = __all_sync(0xffffffffu, lo <= j0 && j0 + kKeys - 1 <= hi);
+        float sv[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, sv + c * 32);
+        ptx::tmem_wait_ld();
+        if (!full) {
+          const bool a0 = anchored && j0 == 0;
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            sv[e] = (j0 + e >= lo && j0 + e <= hi) || (e == 0 && a0) ? sv[e] : -INFINITY;
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 128; e += 2) mt = fmaxf(mt, fmaxf(sv[e], sv[e + 1]));
+        mt *= sl2;
+        // TMEM access is warp-collective, so a rescale of O is decided per warp
+        const bool need = (mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY);
+        if (__any_sync(0xffffffffu, need)) {
+          const float mn = fmaxf(m, mt);
+          const float f = (m == -INFINITY) ? 0.f : exp2f(m - mn);
+          l *= f;
+          if (i > 0) {  // O holds earlier tiles: S(i) done implies their PV is done
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              float ov[16];
+              ptx::tmem_ld16(t_o + c * 16, ov);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] *= f;
+              ptx::tmem_st16f(t_o + c * 16, ov);
+            }
+          }
+          m = mn;
+        }
+        float rs = 0.f;
+        const float mm = (m == -INFINITY) ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float* sc = sv + c * 32;
+          uint32_t pw[16];
+          const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(-mm, -mm);
+          float2 rs2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(sc[2 * e], sc[2 * e + 1]), sl22, nm2);
+            const float2 pp = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+            rs2 = __fadd2_rn(rs2, pp);
+            pw[e] = ptx::pack_bf16x2(pp.x, pp.y);  // the weights enter the product in bf16, their sum stays fp32
+          }
+          rs += rs2.x + rs2.y;
+          ptx::tmem_st16(t_s + c * 16, pw);
+        }
+        l += rs;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&sm.p_full[t]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&sm.o_full[t], nq & 1, b.err, abort_flag, 483));
+      if (!ok) break;
+      // ---- epilogue. Its TMEM reads complete (tmem_wait_ld) before this
+      // thread's next p_full arrival, which the next piece's first PV of this
+      // tile (overwriting O) waits for.
+      ptx::tc_fence_after();
+      ++nq;
+      if (w.whole) {
+        const int head = w.g * P.group + r - in_tile * P.group;
+        const int64_t row = w.q_row + tok;
+        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        __nv_bfloat16* orow = P.o + (row * P.Hq + head) * HD;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          float ov[32];
+          ptx::tmem_ld32(t_o + c * 32, ov);
+          ptx::tmem_wait_ld();
+          if (row_valid) {
+            uint32_t ow[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              ow[e] = l > 0.f ? ptx::pack_bf16x2(ov[2 * e] * inv_l, ov[2 * e + 1] * inv_l) : 0u;
+            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(ow[4 * e], ow[4 * e + 1], ow[4 * e + 2], ow[4 * e + 3]);
+          }
+        }
+        if (row_valid && P.lse) P.lse[(int64_t)head * b.T + row] = (m + log2f(l)) * 0.69314718055994531f;
+      } else {
+        const int64_t part = ((int64_t)blockIdx.x * 2 + w.part) * 2 + t;
+        float4* po = C.part_o + part * (HD / 4) * 128 + r;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          float ov[32];
+          ptx::tmem_ld32(t_o + c * 32, ov);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            po[(c * 8 + e) * 128] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+        }
+        C.part_ml[part * 128 + r] = make_float2(m, l);
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- joining cut units
+// blockIdx.y = a border between two shares; the block of the first border
+// inside a unit joins that unit's partial results, 256 / (D / 4) rows of it per
+// blockIdx.x.
+template <int HD>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams C, int ctas) {
+  constexpr int kRows = 256 / (HD / 4);
+  const AttendParams& P = C.a;
+  const BatchParams& b = P.batch;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Shares shares(C, ctas);
+  const int64_t border = shares.share * (blockIdx.y + 1);
+  if (border >= shares.all) return;
+  int g, slot, count;
+  int64_t begin;
+  shares.find(C, border, &g, &slot, &begin, &count);
+  const int first = (int)(begin / shares.share);
+  if (begin == border || first != (int)blockIdx.y) return;  // not cut here, or joined at an earlier border
+  const int last = (int)((begin + count - 1) / shares.share);
+  const Unit u = C.units[slot];
+  const int row = blockIdx.x * kRows + threadIdx.x % kRows, c = threadIdx.x / kRows;
+  const int t = row >> 7, r = row & 127, in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
+  if (in_tile >= C.tile_tokens || tok >= u.tokens) return;
+  auto part_of = [&](int cta) { return ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * 2 + t; };
+  float m = -INFINITY;
+  for (int k = first; k <= last; ++k) m = fmaxf(m, C.part_ml[part_of(k) * 128 + r].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int k = first; k <= last; ++k) {
+    const float2 ml = C.part_ml[part_of(k) * 128 + r];
+    if (ml.x == -INFINITY) continue;
+    const float f = exp2f(ml.x - m);
+    const float4 v = C.part_o[(part_of(k) * (HD / 4) + c) * 128 + r];
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+    l += f * ml.y;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int head = g * P.group + r - in_tile * P.group;
+  const int64_t t_row = u.q_row + tok;
+  *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) =
+      make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (c == 0 && P.lse) P.lse[(int64_t)head * b.T + t_row] = (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// ---------------------------------------------------------------- launches
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int slots_for(int tokens, int seqs, int tile_tokens) { return tokens / (2 * tile_tokens) + seqs; }
+
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int HD>
+aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {
+  const BatchParams& b = P.batch;
+  ChunkParams C;
+  C.a = P;
+  C.tile_tokens = 128 / P.group;
+  C.slots = slots_for(b.T, b.B, C.tile_tokens);
+  const int ctas = c->num_sms;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  C.part_o = reinterpret_cast<float4*>(w);
+  w += align256((size_t)ctas * 4 * 128 * HD * 4);
+  C.part_ml = reinterpret_cast<float2*>(w);
+  w += align256((size_t)ctas * 4 * 128 * 8);
+  C.units = reinterpret_cast<Unit*>(w);
+  w += align256((size_t)C.slots * sizeof(Unit));
+  C.tiles_end = reinterpret_cast<int64_t*>(w);
+  CUtensorMap tq;
+  aa_status st = make_query_map(&tq, P.q, b.T, P.q_stride, b.Hkv, P.group, HD, C.tile_tokens);
+  if (st != AA_OK) return st;
+  const size_t smem = sizeof(ChunkSmem<HD>);
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t result[kMaxDevices];
+  cudaError_t e = once_per_device(once, result, c->device, [&] {
+    return cudaFuncSetAttribute(attend_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel smem attribute");
+  chunk_plan_kernel<<<1, 1024, 0, s>>>(C);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "chunk_plan_kernel launch");
+  e = launch_after(attend_chunk_kernel<HD>, dim3((unsigned)ctas), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
+  if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel launch");
+  if (ctas > 1) {
+    constexpr int kRows = 256 / (HD / 4);
+    e = launch_after(chunk_join_kernel<HD>, dim3(256 / kRows, (unsigned)(ctas - 1)), 256, 0, s, C, ctas);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk_join_kernel launch");
+  }
+  return AA_OK;
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int group) {
+  const size_t slots = slots_for(total_tokens, num_seqs, 128 / group), ctas = c->num_sms;
+  return align256(ctas * 4 * 128 * c->cfg.head_dim * 4) + align256(ctas * 4 * 128 * 8) +
+         align256(slots * sizeof(Unit)) + align256((slots + 1) * 8);
+}
+
+aa_status launch_attend_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {
+  return c->cfg.head_dim == 128 ? launch<128>(c, P, workspace, s) : launch<64>(c, P, workspace, s);
+}
+
+}  // namespace aa

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
   const uint32_t ranks = ptx::cluster_size(), rank = ptx::cluster_rank();
   const int unit = (int)(blockIdx.x / ranks);
   const int g = unit % b.Hkv, seq = unit / b.Hkv;
-  const SeqSpan span = load_seq(b, seq);
+  const SeqSpan span = load_seq(b, seq, P.page_shift);
   const int tile_tokens = 16 * RT / P.group;
 
   if (tid == 0) {

@@ -7,21 +7,27 @@
 
 namespace aa {
 
-// The sequence of row t: the last b with cu_q[b] <= t, for cu_q[0] <= t (a
-// whole warp asks for one row; sequences without new tokens are passed over).
-// 33-ary search: one load latency for up to 32 sequences, two for 1056.
-__device__ __forceinline__ int warp_find_seq(const int32_t* __restrict__ cu_q, int num_seqs, int t) {
+// The last i in [0, n) for which `holds` does, where it holds for 0 and, from
+// some i on, no longer. A whole warp asks; 33-ary search: one load latency for
+// up to 33 entries, two for 1089.
+template <class Holds>
+__device__ __forceinline__ int warp_last(int n, Holds holds) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, n = num_seqs;  // the answer lies in [lo, lo + n)
+  int lo = 0;  // the answer lies in [lo, lo + n)
   while (n > 1) {
-    const int step = (n + 32) / 33;  // lanes look at the last entry of 32 of the 33 parts
+    const int step = (n + 32) / 33;  // lanes look at the first entry of all of the 33 parts but one
     const int at = (lane + 1) * step;
-    const bool le = at < n && __ldg(cu_q + lo + at) <= t;
-    const int parts = __popc(__ballot_sync(0xffffffffu, le));  // cu_q does not decrease
+    const bool yes = at < n && holds(lo + at);
+    const int parts = __popc(__ballot_sync(0xffffffffu, yes));
     lo += parts * step;
     n = min(step, n - parts * step);
   }
   return lo;
+}
+
+// The sequence of row t >= cu_q[0] (sequences without new tokens are passed over).
+__device__ __forceinline__ int warp_find_seq(const int32_t* __restrict__ cu_q, int num_seqs, int t) {
+  return warp_last(num_seqs, [&](int i) { return __ldg(cu_q + i) <= t; });
 }
 
 // One batch as the kernels see it.

@@ -46,6 +46,10 @@ aa_status launch_copy_pages(const aa_cache_s* c, const std::vector<PagePair>& pa
 // swizzle (rope.cu).
 aa_status make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int D, int box_rows);
 
+// Tensor map over q [T, Hkv, group, D] with `stride` elements from token to
+// token, box {64, group, 1, tokens} (rope.cu).
+aa_status make_query_map(CUtensorMap* m, const void* q, int T, int64_t stride, int Hkv, int group, int D, int tokens);
+
 // Checks shared with aa_rope_axes_apply (rope_axes.cu).
 size_t rows_span(int64_t T, int64_t stride, int H, int D);
 bool overlap(const void* a, size_t na, const void* b, size_t nb);

@@ -146,6 +146,20 @@ aa_status make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int D, i
   return AA_OK;
 }
 
+aa_status make_query_map(CUtensorMap* m, const void* q, int T, int64_t stride, int Hkv, int group, int D, int tokens) {
+  auto enc = get_encode_fn();
+  if (!enc) return fail(AA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)group, (cuuint64_t)Hkv, (cuuint64_t)T};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)group * D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)tokens};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(AA_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed");
+  return AA_OK;
+}
+
 // One warp waits on a barrier that expects one arrival and never gets it.
 __global__ void bounded_wait_selftest_kernel(int32_t* err, uint64_t limit_ns) {
   __shared__ uint64_t bar;

@@ -74,7 +74,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 aa_status check_rows(const char* what, const void* x, int64_t stride, int H, int D) {
   if (!x || !aligned16(x)) return fail(AA_ERR_INVALID_ARG, std::string(what) + " must be a 16-byte aligned device pointer");
-  if (stride < (int64_t)H * D || stride % 8 || stride >= (1ll << 40))
+  if (stride < (int64_t)H * D || stride % 8 || stride >= (1ll << 38))
     return fail(AA_ERR_INVALID_ARG, std::string(what) + "'s token stride must be a multiple of 8 elements and >= heads * D");
   return AA_OK;
 }
