@@ -20,24 +20,37 @@ import ctypes
 
 import torch
 
-from .binding import AARopeAxes, ROPE_ADJACENT, _check, _stream, lib
+from .binding import AARopeAxes, ROPE_ADJACENT, _check, _stream_ptr, lib
 
 __all__ = ["RopeAxes", "RopeAxesFn", "rope_axes"]
 
 
+# The single-token calls take a few microseconds on the GPU, so their host side is kept lean: plain attribute tests, no
+# context managers or temporary objects on the common path.
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocate on the stream that the kernels will run on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
 
 
-def _check_tensor(name, x, shape, dtype, device=None):
-    """x is a CUDA tensor of `dtype`, `shape` (None: any size) and, if given, `device`."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype:
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
-    if x.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
-        raise ValueError(f"{name} must have shape {tuple('any' if n is None else n for n in shape)}, got {tuple(x.shape)}")
-    if device is not None and x.device != device:
-        raise ValueError(f"{name} is on {x.device}, expected {device}")
+def _check_rows(name, x, T, H, D, device):
+    """x is a bf16 tensor [T, H, D] on `device` (T, H None: any)."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.device != device:
+        raise ValueError(f"{name} must be a bfloat16 tensor on {device}")
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != D or (T is not None and shape[0] != T) or (H is not None and shape[1] != H):
+        want = tuple("any" if n is None else n for n in (T, H, D))
+        raise ValueError(f"{name} must have shape {want}, got {tuple(shape)}")
+
+
+def _check_tensor(name, x, shape, dtype, device):
+    """x is a contiguous tensor of `dtype` and `shape` on `device`."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+    if x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(x.shape)}")
 
 
 def _rows(x):
@@ -54,12 +67,10 @@ def _rows(x):
 
 
 def _out(name, out, like):
-    """The caller's output tensor, checked, or a new one of the shape of `like`."""
+    """The caller's output tensor, checked, or a new contiguous one of the shape of `like`."""
     if out is None:
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     _check_tensor(name, out, like.shape, like.dtype, like.device)
-    if not out.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     return out
 
 
@@ -111,35 +122,41 @@ class RopeAxes:
         self._at = ctypes.addressof(self._c)
 
     def _positions(self, pos, T, device):
-        if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype != torch.int32 or pos.device != device:
+        if not isinstance(pos, torch.Tensor) or pos.dtype is not torch.int32 or pos.device != device:
             raise ValueError(f"pos must be an int32 tensor on {device}")
-        if pos.shape != (self.num_axes, T) and not (self.num_axes == 1 and pos.shape == (T,)):
-            raise ValueError(f"pos must have shape ({self.num_axes}, {T}), got {tuple(pos.shape)}")
+        shape = pos.shape
+        if shape != (self.num_axes, T) and not (self.num_axes == 1 and shape == (T,)):
+            raise ValueError(f"pos must have shape ({self.num_axes}, {T}), got {tuple(shape)}")
         return pos.contiguous()
 
     def apply(self, pos, q, k=None, inverse=False, out_q=None, out_k=None, stream=None):
         """Rotate q [T, Hq, D] (and k [T, Hk, D]) by pos, int32 [axes, T]; inverse=True turns back. Token strides of
         slices are taken as they are; out_q = q works in place on a contiguous q."""
-        _check_tensor("q", q, (None, None, self.head_dim), torch.bfloat16)
-        T, dev = q.shape[0], q.device
-        if dev.index != torch.cuda.current_device():
+        if not isinstance(q, torch.Tensor) or not q.is_cuda:
+            raise ValueError("q must be a CUDA tensor")
+        dev = q.device
+        index = dev.index
+        _check_rows("q", q, None, None, self.head_dim, dev)
+        if index != torch.cuda.current_device():
             raise ValueError(f"q is on {dev}, which is not the current device")
+        T, hq, _ = q.shape
         if k is not None:
-            _check_tensor("k", k, (T, None, self.head_dim), torch.bfloat16, dev)
+            _check_rows("k", k, T, None, self.head_dim, dev)
         elif out_k is not None:
             raise ValueError("out_k goes with k")
         with _on(stream):
             pos = self._positions(pos, T, dev)
             yq = _out("out_q", out_q, q)
-            yk = None if k is None else _out("out_k", out_k, k)
             q, sq = _rows(q)
-            kp, sk, hk = None, 0, 0
+            yk, kp, sk, yp, hk = None, None, 0, None, 0
             if k is not None:
+                yk = _out("out_k", out_k, k)
                 k, sk = _rows(k)
-                kp, hk = k.data_ptr(), k.shape[1]
-            _check(lib().aa_rope_axes_apply(self._at, pos.data_ptr(), T, q.data_ptr(), sq, yq.data_ptr(), q.shape[1], kp,
-                                            sk, None if k is None else yk.data_ptr(), hk, int(bool(inverse)),
-                                            _stream(stream)))
+                kp, yp, hk = k.data_ptr(), yk.data_ptr(), k.shape[1]
+            status = lib().aa_rope_axes_apply(self._at, pos.data_ptr(), T, q.data_ptr(), sq, yq.data_ptr(), hq, kp, sk, yp, hk,
+                                              1 if inverse else 0, _stream_ptr(stream, index))
+            if status:
+                _check(status)
         return yq if k is None else (yq, yk)
 
 

@@ -147,6 +147,22 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_raw_stream = None
+
+
+def _stream_ptr(stream, device_index):
+    """The stream's handle as an integer. For the current one torch's own raw query (0.1 us of host time against 3 us
+    for the Stream object), where this torch has it."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device_index)
+
+
 class Plan:
     """aa_plan for one packing; compute methods wrap aa_rope_apply/aa_fwd/aa_bwd."""
 

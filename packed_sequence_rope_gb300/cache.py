@@ -17,17 +17,23 @@ the binding this marshals arguments: every step runs in the library.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 import torch
 
-from .binding import AACacheBatch, AACacheConfig, _check, _stream, lib
-from .axes import _check_tensor, _on, _out, _rows
+from .axes import _check_rows, _check_tensor, _on, _out, _rows
+from .binding import AACacheConfig, _check, _stream_ptr, lib
 
 __all__ = ["PagedCache"]
 
 
+_BATCH = struct.Struct("@3P4i")  # aa_cache_batch
+
+
 def _host_i32(name, x):
+    if type(x) is np.ndarray and x.dtype == np.int32 and x.ndim == 1 and x.flags.c_contiguous:
+        return x
     a = np.ascontiguousarray(np.asarray(x))
     if a.ndim != 1 or (a.size and a.dtype.kind not in "iu"):
         raise ValueError(f"{name} must be a list of integers")
@@ -70,9 +76,9 @@ class PagedCache:
         elif device is not None:
             raise ValueError("device goes without k_pages and v_pages")
         for name, x in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if not isinstance(x, torch.Tensor) or not x.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
             _check_tensor(name, x, shape, torch.bfloat16, k_pages.device)
-            if not x.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
         self.k_pages, self.v_pages, self.device = k_pages, v_pages, k_pages.device
         with torch.cuda.device(self.device):
             _check(lib().aa_cache_create(ctypes.addressof(self.cfg), k_pages.data_ptr(), v_pages.data_ptr(),
@@ -98,7 +104,7 @@ class PagedCache:
         self.close()
 
     def _stream(self, stream):
-        return None if self.host_only else _stream(stream)
+        return None if self.host_only else _stream_ptr(stream, self.device.index)
 
     # ---- bookkeeping (host)
     def resize(self, seqs, lens, stream=None):
@@ -151,26 +157,29 @@ class PagedCache:
         _check(lib().aa_cache_copy_pages(self._h, a.ctypes.data, b.ctypes.data, a.size, self._stream(stream)))
 
     def check_device_error(self, stream=None):
-        _check(lib().aa_cache_check_error(self._h, _stream(stream)))
+        _check(lib().aa_cache_check_error(self._h, self._stream(stream)))
 
     def _batch(self, page_table, cu_q, kv_len, T, layer):
-        if self.host_only:
+        """aa_cache_batch as bytes."""
+        dev = self.device
+        if dev is None:
             raise ValueError("the cache was created with host_only = True")
-        for name, x, dims in (("page_table", page_table, 2), ("cu_q", cu_q, 1), ("kv_len", kv_len, 1)):
-            if not isinstance(x, torch.Tensor) or x.dtype != torch.int32 or x.device != self.device or x.dim() != dims \
-                    or not x.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous int32 tensor with {dims} dimension(s) on {self.device}")
-        B, W = page_table.shape
-        if cu_q.shape[0] != B + 1 or kv_len.shape[0] != B:
-            raise ValueError(f"page_table has {B} rows: cu_q needs {B + 1} entries and kv_len {B}")
-        return AACacheBatch(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), B, W, T, layer)
+        for x, name in ((page_table, "page_table"), (cu_q, "cu_q"), (kv_len, "kv_len")):
+            if not isinstance(x, torch.Tensor) or x.dtype is not torch.int32 or x.device != dev or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
+        shape = page_table.shape
+        if len(shape) != 2 or cu_q.shape != (shape[0] + 1,) or kv_len.shape != (shape[0],):
+            raise ValueError(f"page_table [B, W], cu_q [B + 1] and kv_len [B] do not fit together: {tuple(shape)}, "
+                             f"{tuple(cu_q.shape)}, {tuple(kv_len.shape)}")
+        return _BATCH.pack(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), shape[0], shape[1], T, layer)
 
     def append(self, k, v, page_table, cu_q, kv_len, layer=0, rope=None, pos=None, q=None, out_q=None, stream=None):
         """Write the new tokens' k (rotated by rope at pos) and v [T, Hkv, D] to their pages; with q [T, Hq, D] the same
         launch rotates q, and the result is returned."""
-        _check_tensor("k", k, (None, self.Hkv, self.D), torch.bfloat16, self.device)
+        dev, D = self.device, self.D
+        _check_rows("k", k, None, self.Hkv, D, dev)
         T = k.shape[0]
-        _check_tensor("v", v, (T, self.Hkv, self.D), torch.bfloat16, self.device)
+        _check_rows("v", v, T, self.Hkv, D, dev)
         batch = self._batch(page_table, cu_q, kv_len, T, layer)
         if (rope is None) != (pos is None):
             raise ValueError("give both rope and pos or neither")
@@ -178,22 +187,25 @@ class PagedCache:
             if out_q is not None:
                 raise ValueError("out_q goes with q")
         else:
-            _check_tensor("q", q, (T, None, self.D), torch.bfloat16, self.device)
+            _check_rows("q", q, T, None, D, dev)
             if rope is None:
                 raise ValueError("q is rotated: it needs rope and pos")
         with _on(stream):
             k, sk = _rows(k)
             v, sv = _rows(v)
-            if pos is not None:
-                pos = rope._positions(pos, T, self.device)
+            rp, pp = None, None
+            if rope is not None:
+                pos = rope._positions(pos, T, dev)
+                rp, pp = rope._at, pos.data_ptr()
             yq, qp, yp, sq, hq = None, None, None, 0, 0
             if q is not None:
                 yq = _out("out_q", out_q, q)
                 q, sq = _rows(q)
                 qp, yp, hq = q.data_ptr(), yq.data_ptr(), q.shape[1]
-            _check(lib().aa_cache_append(self._h, ctypes.addressof(batch), k.data_ptr(), sk, v.data_ptr(), sv,
-                                         None if rope is None else rope._at, None if pos is None else pos.data_ptr(), qp,
-                                         sq, yp, hq, _stream(stream)))
+            status = lib().aa_cache_append(self._h, batch, k.data_ptr(), sk, v.data_ptr(), sv, rp, pp, qp, sq, yp, hq,
+                                           _stream_ptr(stream, dev.index))
+            if status:
+                _check(status)
         return yq
 
     def workspace_bytes(self, num_seqs, total_tokens, max_q, table_width, q_heads):
@@ -209,28 +221,32 @@ class PagedCache:
                lse=None, workspace=None, return_lse=False, stream=None):
         """Attention of the new tokens' rotated q [T, Hq, D] over their sequences' pages: o [T, Hq, D], and with
         return_lse the log-sum-exp [Hq, T] fp32. key_lo: int32 [T], the first key each row sees; anchor: key 0 is seen too."""
-        _check_tensor("q", q, (None, None, self.D), torch.bfloat16, self.device)
+        dev = self.device
+        _check_rows("q", q, None, None, self.D, dev)
         T, hq, _ = q.shape
         batch = self._batch(page_table, cu_q, kv_len, T, layer)
-        if key_lo is not None:
-            _check_tensor("key_lo", key_lo, (T,), torch.int32, self.device)
         with _on(stream):
+            kp = None
             if key_lo is not None:
+                if not isinstance(key_lo, torch.Tensor) or key_lo.dtype is not torch.int32 or key_lo.device != dev \
+                        or key_lo.shape != (T,):
+                    raise ValueError(f"key_lo must be an int32 tensor [{T}] on {dev}")
                 key_lo = key_lo.contiguous()
+                kp = key_lo.data_ptr()
             o = _out("out", out, q)
             if lse is not None:
-                _check_tensor("lse", lse, (hq, T), torch.float32, self.device)
-                if not lse.is_contiguous():
-                    raise ValueError("lse must be contiguous")
+                _check_tensor("lse", lse, (hq, T), torch.float32, dev)
             elif return_lse:
-                lse = torch.empty(hq, T, device=self.device, dtype=torch.float32)
+                lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
             if workspace is None:
-                workspace = self.alloc_workspace(batch.num_seqs, T, max_q, batch.table_width, hq)
-            else:
-                _check_tensor("workspace", workspace, (None,), torch.uint8, self.device)
+                workspace = self.alloc_workspace(page_table.shape[0], T, max_q, page_table.shape[1], hq)
+            elif not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.device != dev \
+                    or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
             q, sq = _rows(q)
-            _check(lib().aa_cache_attend(self._h, ctypes.addressof(batch), q.data_ptr(), sq, hq, int(max_q),
-                                         None if key_lo is None else key_lo.data_ptr(), int(bool(anchor)),
-                                         float(softmax_scale or 0.0), o.data_ptr(), None if lse is None else lse.data_ptr(),
-                                         workspace.data_ptr(), workspace.numel(), _stream(stream)))
+            status = lib().aa_cache_attend(self._h, batch, q.data_ptr(), sq, hq, max_q, kp, 1 if anchor else 0,
+                                           softmax_scale or 0.0, o.data_ptr(), None if lse is None else lse.data_ptr(),
+                                           workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev.index))
+            if status:
+                _check(status)
         return (o, lse) if return_lse else o

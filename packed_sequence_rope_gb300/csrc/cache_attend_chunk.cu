@@ -18,17 +18,19 @@
 // The second and third are launched as programmatic dependents, so that their
 // start-up overlaps the kernel before them.
 //
-// Roles in attend_chunk_kernel (384 threads), as in the packed forward:
+// Roles in attend_chunk_kernel (640 threads):
 //   warp 0      finds the CTA's next piece of work and copies its query tiles and
 //               the key tiles' pages (tensor copies, one page piece per lane)
 //   warp 1      owns tensor memory and issues the products
 //   warp 2      clears values that no row sees (a page's unused rows)
-//   warps 4-7   row tile 0: online softmax (thread = row = TMEM lane), epilogue
-//   warps 8-11  the same for row tile 1
+//   warps 4-11  row tile 0: online softmax and epilogue; lane = row, two warps per
+//               32 rows with half of the columns each, which exchange the rows'
+//               maxima through shared memory
+//   warps 12-19 the same for row tile 1
 // Tensor memory: S0 [0, 128), S1 [128, 256), O0, O1 (D columns each); P replaces
 // the first half of its S as packed bf16 and feeds P V from there. The issue order
-// S0(j), PV1(j - 1), S1(j), PV0(j) keeps the tensor cores busy with one tile while
-// the other's softmax runs.
+// PV0(j), S0(j + 1), PV1(j), S1(j + 1) keeps the tensor cores busy with one tile
+// while the other's softmax runs.
 #include <algorithm>
 
 #include "cache_attend.cuh"
@@ -37,8 +39,9 @@ namespace aa {
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kThreads = 384;
-constexpr int kReaders = 10;  // of a published piece: the MMA thread, warp 2, eight softmax warps
+constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 32 * (4 + kSoftmaxWarps);
+constexpr int kReaders = 2 + kSoftmaxWarps;  // of a published piece: warps 1 and 2, the softmax warps
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
@@ -157,44 +160,48 @@ struct ChunkSmem {
   alignas(1024) uint8_t v[kStages][kB][16384];
   uint64_t q_full[2], q_free[2];
   uint64_t piece_full[2], piece_empty[2];
-  uint64_t kv_full[kStages], v_clean[kStages], kv_empty[kStages];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], drain;
   Piece piece[2];
+  float pair[2][2][2][128];  // [step parity][row tile][column half][row]: maxima, then sums
   uint32_t tmem_base;
   int abort_flag;
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort_flag,
-                                              int site) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::global_timer_ns();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (ptx::mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (ptx::global_timer_ns() - t0 >= kAttendWaitNs) {
-      atomicCAS(err, 0, site);
-      *abort_flag = 1;
-      return false;
+// A converged warp waits, bounded, and gives up with the rest of the CTA. One
+// lane polls: with all lanes of all waiting warps polling, their traffic on
+// shared memory slowed the products' operand reads to half.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort_flag, int site) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0 && !ptx::mbar_try_wait(bar, parity)) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    for (int i = 1;; ++i) {
+      if (ptx::mbar_try_wait(bar, parity)) break;
+      if (i % 64) continue;
+      if (*abort_flag) ok = false;
+      if (ok && ptx::global_timer_ns() - t0 >= kAttendWaitNs) {
+        atomicCAS(err, 0, site);
+        *abort_flag = 1;
+        ok = false;
+      }
+      if (!ok) break;
     }
   }
+  return __all_sync(0xffffffffu, ok);
 }
 
-// The li-th piece of this CTA, or false when there is none left.
+// The li-th piece of this CTA, read by a whole warp; false when there is none left.
 template <class Smem>
-__device__ __forceinline__ bool read_piece(Smem& sm, int li, int32_t* err, volatile int* abort_flag, bool warp_read,
-                                           int site, Piece* out) {
-  bool ok = wait_or_abort(&sm.piece_full[li & 1], (li >> 1) & 1, err, abort_flag, site);
-  if (warp_read) ok = __all_sync(0xffffffffu, ok);
-  if (!ok) return false;
+__device__ __forceinline__ bool read_piece(Smem& sm, int li, int32_t* err, volatile int* abort_flag, int site, Piece* out) {
+  if (!warp_wait(&sm.piece_full[li & 1], (li >> 1) & 1, err, abort_flag, site)) return false;
   *out = sm.piece[li & 1];
-  if (warp_read) __syncwarp();
-  if (!warp_read || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&sm.piece_empty[li & 1]);
-  return out->valid != 0;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&sm.piece_empty[li & 1]);
+  return __all_sync(0xffffffffu, out->valid != 0);
 }
 
-// Barrier phases: pieces count the piece ring; the K/V ring counts the CTA's
-// key tiles over all its pieces; s_full / p_full count each row tile's
+// Barrier phases: pieces count the piece ring; the K and V rings count the
+// CTA's key tiles over all its pieces; s_full / p_full count each row tile's
 // softmax steps; q_full, q_free and o_full the pieces in which the row tile
 // exists. As in the packed forward every wait is bounded and its outcome made
 // uniform in a warp before anything collective.
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ChunkParams C) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   constexpr int kB = HD / 64, kStages = ChunkSmem<HD>::kStages, kTmemCols = 512;
-  constexpr uint32_t kStageBytes = 2 * kKeys * HD * 2;
+  constexpr uint32_t kTileBytes = kKeys * HD * 2;
   const AttendParams& P = C.a;
   const BatchParams& b = P.batch;
   if (ptx::smem_u32(smem_raw) & 1023u) {  // swizzled tiles need a 1 KB aligned base
@@ -212,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   ChunkSmem<HD>& sm = *reinterpret_cast<ChunkSmem<HD>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = (int)__reduce_max_sync(0xffffffffu, (unsigned)tid >> 5), lane = tid & 31;  // uniform
   volatile int* abort_flag = &sm.abort_flag;
 
   if (tid == 0) {
@@ -221,17 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tma_prefetch_desc(&tmV);
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(&sm.q_full[t], 1);
-      ptx::mbar_init(&sm.q_free[t], 128);
+      ptx::mbar_init(&sm.q_free[t], kSoftmaxWarps / 2);
       ptx::mbar_init(&sm.s_full[t], 1);
-      ptx::mbar_init(&sm.p_full[t], 128);
+      ptx::mbar_init(&sm.p_full[t], kSoftmaxWarps / 2);
       ptx::mbar_init(&sm.o_full[t], 1);
       ptx::mbar_init(&sm.piece_full[t], 1);
       ptx::mbar_init(&sm.piece_empty[t], kReaders);
     }
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&sm.kv_full[s], 1);
-      ptx::mbar_init(&sm.v_clean[s], 1);
-      ptx::mbar_init(&sm.kv_empty[s], 1);
+      for (uint64_t* bar : {&sm.k_full[s], &sm.k_empty[s], &sm.v_full[s], &sm.v_clean[s], &sm.v_empty[s]})
+        ptx::mbar_init(bar, 1);
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = __reduce_max_sync(0xffffffffu, sm.tmem_base);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan, and everything before it
 
@@ -250,15 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Shares shares(C, gridDim.x);
     int64_t at = shares.share * blockIdx.x;
     const int64_t end = min(at + shares.share, shares.all);
-    int nq[2] = {0, 0}, ks = 0;
+    int nq[2] = {0, 0}, ks = 0, nk = 0;  // key tiles whose V, whose K has been asked for
     bool ok = true;
-    // a key tile is `pieces` page pieces, each kB column blocks of K and V
+    // a key tile is `pieces` page pieces, each kB column blocks of K, then of V
     const int piece_shift = min(P.page_shift, 6), pieces = kKeys >> piece_shift;
-    const int copies = pieces * kB * 2;  // at most 32: one per lane
+    const int copies = pieces * kB;  // at most 16: one per lane
     const int part = lane & (pieces - 1), block = (lane / pieces) % kB;
-    const bool is_v = lane >= pieces * kB;
     for (int li = 0; ok; ++li) {
-      if (li >= 2) ok = __all_sync(0xffffffffu, wait_or_abort(&sm.piece_empty[li & 1], ((li >> 1) - 1) & 1, b.err, abort_flag, 452));
+      if (li >= 2) ok = warp_wait(&sm.piece_empty[li & 1], ((li >> 1) - 1) & 1, b.err, abort_flag, 452);
       if (!ok) break;
       Piece w{};
       if (at < end) {
@@ -294,10 +299,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                                : kNoRow;
       };
       int next = row_of(w.first);
+      auto load_keys = [&](int i) {
+        const int s = ks % kStages, row = next;
+        next = row_of(i + 1);  // in flight while this stage is waited for
+        // K's buffer is free one product earlier than V's, and V is wanted later
+        for (int v = 0; v < 2; ++v) {
+          uint64_t* full = v ? &sm.v_full[s] : &sm.k_full[s];
+          if (ks >= kStages)
+            ok = warp_wait(v ? &sm.v_empty[s] : &sm.k_empty[s], ((ks / kStages) - 1) & 1, b.err,
+                                                       abort_flag, 451);
+          if (!ok) return;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(full, kTileBytes);
+          __syncwarp();
+          if (lane < copies)
+            ptx::tma_load_2d((v ? sm.v[s][block] : sm.k[s][block]) + (part << piece_shift) * 128, v ? &tmV : &tmK, full,
+                             block * 64, row);
+          if (v == 0) nk = ks + 1;
+        }
+        ++ks;
+      };
+      // the first key tile goes ahead of the queries, whose buffers the piece
+      // before still reads
+      load_keys(w.first);
       for (int t = 0; t < (w.tokens > C.tile_tokens ? 2 : 1) && ok; ++t) {
         // the tile's previous Q has had its last S product
         if (nq[t] > 0)
-          ok = __all_sync(0xffffffffu, wait_or_abort(&sm.q_free[t], (nq[t] - 1) & 1, b.err, abort_flag, 450));
+          ok = warp_wait(&sm.q_free[t], (nq[t] - 1) & 1, b.err, abort_flag, 450);
         if (!ok) break;
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(&sm.q_full[t], (uint32_t)(C.tile_tokens * P.group * HD * 2));
@@ -307,94 +334,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++nq[t];
       }
-      for (int i = w.first; i < w.first + w.take && ok; ++i) {
-        const int s = ks % kStages, row = next;
-        next = row_of(i + 1);  // in flight while this stage is waited for
-        if (ks >= kStages)
-          ok = __all_sync(0xffffffffu, wait_or_abort(&sm.kv_empty[s], ((ks / kStages) - 1) & 1, b.err, abort_flag, 451));
-        if (!ok) break;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.kv_full[s], kStageBytes);
-        __syncwarp();
-        if (lane < copies) {
-          uint8_t* dst = (is_v ? sm.v[s][block] : sm.k[s][block]) + (part << piece_shift) * 128;
-          ptx::tma_load_2d(dst, is_v ? &tmV : &tmK, &sm.kv_full[s], block * 64, row);
-        }
-        ++ks;
-      }
+      for (int i = w.first + 1; i < w.first + w.take && ok; ++i) load_keys(i);
     }
     // every issued copy lands before the CTA exits
     for (int t = 0; t < 2; ++t)
       if (nq[t] > 0) ptx::mbar_wait(&sm.q_full[t], (nq[t] - 1) & 1, kDrainNs, b.err, 459);
+    for (int u = max(nk - kStages, 0); u < nk; ++u)
+      ptx::mbar_wait(&sm.k_full[u % kStages], (u / kStages) & 1, kDrainNs, b.err, 459);
     for (int u = max(ks - kStages, 0); u < ks; ++u)
-      ptx::mbar_wait(&sm.kv_full[u % kStages], (u / kStages) & 1, kDrainNs, b.err, 459);
+      ptx::mbar_wait(&sm.v_full[u % kStages], (u / kStages) & 1, kDrainNs, b.err, 459);
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, 0, 0);
-      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, 0, 1);
-      const uint32_t t_s[2] = {tmem, tmem + 128}, t_o[2] = {tmem + 256, tmem + 256 + HD};
-      uint32_t ph_p[2] = {0, 0};
-      int nq[2] = {0, 0}, ks = 0;
-      bool first_pv[2] = {true, true}, ready[2] = {false, false};
-      auto issue_s = [&](int t, int s) -> bool {
-        if (!ready[t]) {  // this piece's Q tile t has landed (first use only)
-          if (!wait_or_abort(&sm.q_full[t], nq[t] & 1, b.err, abort_flag, 462)) return false;
-          ready[t] = true;
-          ptx::tc_fence_after();
-        }
-        const uint64_t qd = ptx::smem_desc_sw128(ptx::smem_u32(sm.q[t][0]), 16, 1024);
-        const uint64_t kd = ptx::smem_desc_sw128(ptx::smem_u32(sm.k[s][0]), 16, 1024);
-        if constexpr (HD == 128)
-          ptx::mma8_ss_kk(t_s[t], qd, kd, idesc_s, 0);
-        else
-          ptx::mma4_ss_kk(t_s[t], qd, kd, idesc_s, 0);
-        ptx::mma_commit(&sm.s_full[t]);
-        return true;
-      };
-      auto issue_pv = [&](int t, int n) -> bool {
-        const int s = n % kStages;
-        if (!wait_or_abort(&sm.v_clean[s], (n / kStages) & 1, b.err, abort_flag, 464)) return false;
-        if (!wait_or_abort(&sm.p_full[t], ph_p[t], b.err, abort_flag, 461)) return false;
-        ph_p[t] ^= 1;
+    // ------------------------------------------------------------ MMA issuer (the whole warp, converged)
+    constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, 0, 1);
+    uint32_t ph_p[2] = {0, 0}, ph_q[2] = {0, 0};
+    int ks = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity, int site) { return warp_wait(bar, parity, b.err, abort_flag, site); };
+    auto issue_s = [&](int t, int s) {
+      const uint64_t qd = ptx::smem_desc_sw128(ptx::smem_u32(sm.q[t][0]), 16, 1024);
+      const uint64_t kd = ptx::smem_desc_sw128(ptx::smem_u32(sm.k[s][0]), 16, 1024);
+      if constexpr (HD == 128)
+        ptx::mma8_ss_kk_warp(tmem + 128 * t, qd, kd, idesc_s, 0);
+      else
+        ptx::mma4_ss_kk_warp(tmem + 128 * t, qd, kd, idesc_s, 0);
+      ptx::mma_commit_warp(&sm.s_full[t]);
+    };
+    bool ok = true;
+    for (int li = 0; ok; ++li) {
+      Piece w;
+      if (!read_piece(sm, li, b.err, abort_flag, 460, &w)) break;
+      // the reductions make the loops' bounds uniform for the compiler
+      const int take = __reduce_max_sync(0xffffffffu, w.take);
+      const int tiles = __all_sync(0xffffffffu, w.tokens > C.tile_tokens) ? 2 : 1;
+      // the first S products, as the piece's K and Q land
+      if (!(ok = wait(&sm.k_full[ks % kStages], (ks / kStages) & 1, 463))) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t >= tiles) break;
+        if (!(ok = wait(&sm.q_full[t], ph_q[t], 462))) break;
+        ph_q[t] ^= 1;
         ptx::tc_fence_after();
-        ptx::mma8_ts_seq(t_o[t], t_s[t], ptx::smem_desc_sw128(ptx::smem_u32(sm.v[s][0]), 16384, 1024), idesc_pv,
-                         first_pv[t] ? 0u : 1u);
-        first_pv[t] = false;
-        return true;
-      };
-      bool ok = true;
-      for (int li = 0; ok; ++li) {
-        Piece w;
-        if (!read_piece(sm, li, b.err, abort_flag, false, 460, &w)) break;
-        const bool has1 = w.tokens > C.tile_tokens;
-        first_pv[0] = first_pv[1] = true;
-        ready[0] = false;
-        ready[1] = !has1;
-        for (int i = 0; i < w.take && ok; ++i, ++ks) {
-          const int s = ks % kStages;
-          if (!(ok = wait_or_abort(&sm.kv_full[s], (ks / kStages) & 1, b.err, abort_flag, 463))) break;
-          ptx::tc_fence_after();
-          if (!(ok = issue_s(0, s))) break;
-          if (i > 0) {
-            if (has1 && !(ok = issue_pv(1, ks - 1))) break;
-            ptx::mma_commit(&sm.kv_empty[(ks - 1) % kStages]);
-          }
-          if (has1 && !(ok = issue_s(1, s))) break;
-          if (!(ok = issue_pv(0, ks))) break;
-          if (i == w.take - 1) ptx::mma_commit(&sm.o_full[0]);
-        }
-        if (ok && has1) {
-          ok = issue_pv(1, ks - 1);
-          if (ok) ptx::mma_commit(&sm.o_full[1]);
-        }
-        if (ok) ptx::mma_commit(&sm.kv_empty[(ks - 1) % kStages]);
-        ++nq[0];
-        if (has1) ++nq[1];
+        issue_s(t, ks % kStages);
       }
-      // every issued MMA must finish before TMEM is released
-      ptx::mma_commit(&sm.drain);
-      ptx::mbar_wait(&sm.drain, 0, kDrainNs, b.err, 469);
+      if (!ok) break;
+      ptx::mma_commit_warp(&sm.k_empty[ks % kStages]);
+      for (int i = 0; i < take; ++i, ++ks) {
+        // waits for copies first, while the tensor cores are still busy; then
+        // only the softmax's signal stands before P V and the next S of a tile
+        const int s = ks % kStages, s1 = (ks + 1) % kStages;
+        const bool more = i + 1 < take;
+        if (!(ok = wait(&sm.v_clean[s], (ks / kStages) & 1, 464))) break;
+        if (more && !(ok = wait(&sm.k_full[s1], ((ks + 1) / kStages) & 1, 463))) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= tiles) break;
+          if (!(ok = wait(&sm.p_full[t], ph_p[t], 461))) break;
+          ph_p[t] ^= 1;
+          ptx::tc_fence_after();
+          ptx::mma8_ts_seq_warp(tmem + 256 + HD * t, tmem + 128 * t,
+                                ptx::smem_desc_sw128(ptx::smem_u32(sm.v[s][0]), 16384, 1024), idesc_pv, i == 0 ? 0u : 1u);
+          if (more)
+            issue_s(t, s1);
+          else
+            ptx::mma_commit_warp(&sm.o_full[t]);
+        }
+        if (!ok) break;
+        ptx::mma_commit_warp(&sm.v_empty[s]);
+        if (more) ptx::mma_commit_warp(&sm.k_empty[s1]);
+      }
     }
+    // every issued MMA must finish before TMEM is released
+    __syncwarp();
+    ptx::mma_commit_warp(&sm.drain);
+    ptx::mbar_wait(&sm.drain, 0, kDrainNs, b.err, 469);
   } else if (warp == 2) {
     // ------------------------------------------------------------ clearing unseen values
     // the rows of V that no row of the unit sees have weight 0, but 0 * NaN is not
@@ -402,12 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int li = 0; ok; ++li) {
       Piece w;
-      if (!read_piece(sm, li, b.err, abort_flag, true, 470, &w)) break;
+      if (!read_piece(sm, li, b.err, abort_flag, 470, &w)) break;
       const int hi = w.p0 + w.tokens - 1;
       const KeyTiles<kKeys> keys(w.lo, hi, P.anchor);
       for (int i = w.first; i < w.first + w.take; ++i, ++ks) {
         const int s = ks % kStages;
-        ok = __all_sync(0xffffffffu, wait_or_abort(&sm.kv_full[s], (ks / kStages) & 1, b.err, abort_flag, 471));
+        ok = warp_wait(&sm.v_full[s], (ks / kStages) & 1, b.err, abort_flag, 471);
         if (!ok) break;
         const int j0 = keys.tile(i) * kKeys;
         if (j0 < w.lo || j0 + kKeys - 1 > hi) {
@@ -424,49 +436,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
-    const int t = (warp - 4) >> 2, r = tid & 127;
+    const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const int pair_bar = 1 + t * 4 + (warp & 3);  // named barrier of the two warps with the same rows
     const float sl2 = P.scale_log2;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + 128 * t + lane_off, t_o = tmem + 256 + HD * t + lane_off;
+    const uint32_t t_s = tmem + 128 * t + lane_off, t_o = tmem + 256 + HD * t + half * (HD / 2) + lane_off;
     uint32_t ph_s = 0;
     int nq = 0;
-    bool ok = true;
-    for (int li = 0; ok; ++li) {
-      Piece w;
-      if (!read_piece(sm, li, b.err, abort_flag, true, 480, &w)) break;
-      if (t == 1 && w.tokens <= C.tile_tokens) continue;
+    // a warp that gives up still meets its partner: both leave together
+    for (int li = 0;; ++li) {
+      const Piece& w = sm.piece[li & 1];  // released after the epilogue
+      const bool got = warp_wait(&sm.piece_full[li & 1], (li >> 1) & 1, b.err, abort_flag, 480);
+      if (!ptx::bar_and(pair_bar, 64, got) || !w.valid) break;
+      if (t == 1 && w.tokens <= C.tile_tokens) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.piece_empty[li & 1]);
+        continue;
+      }
+      const int in_tile = r / P.group;
+      const bool row_valid = in_tile < C.tile_tokens && t * C.tile_tokens + in_tile < w.tokens;
+      int lo = 1, hi = 0;  // this row's visible keys
+      if (row_valid) {
+        lo = P.key_lo ? max(__ldg(P.key_lo + w.q_row + t * C.tile_tokens + in_tile), 0) : 0;
+        hi = w.p0 + t * C.tile_tokens + in_tile;
+      }
+      const bool anchored = P.anchor && row_valid && hi >= 0 && half == 0;
+      const int take = w.take;
       const KeyTiles<kKeys> keys(w.lo, w.p0 + w.tokens - 1, P.anchor);
-      const int in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
-      const bool row_valid = in_tile < C.tile_tokens && tok < w.tokens;
-      const int lo = row_valid ? (P.key_lo ? max(__ldg(P.key_lo + w.q_row + tok), 0) : 0) : 1;
-      const int hi = row_valid ? w.p0 + tok : 0;
-      const bool anchored = P.anchor && row_valid && hi >= 0;
+      int j0 = keys.tile(w.first) * kKeys + half * 64;  // this warp's first key
+      int next_j0 = keys.tile(w.first + 1) * kKeys + half * 64;
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < w.take; ++i) {
-        ok = __all_sync(0xffffffffu, wait_or_abort(&sm.s_full[t], ph_s, b.err, abort_flag, 482));
-        if (!ok) break;
+      bool ok = true;
+      for (int i = 0; i < take; ++i, j0 = next_j0, next_j0 += kKeys) {
+        ok = warp_wait(&sm.s_full[t], ph_s, b.err, abort_flag, 482);
+        if (!ok) {
+          ptx::bar_and(pair_bar, 64, false);
+          break;
+        }
         ph_s ^= 1;
         ptx::tc_fence_after();
         // the piece's last S product of this tile is done: Q may be replaced
-        if (i == w.take - 1) ptx::mbar_arrive(&sm.q_free[t]);
-        const int j0 = keys.tile(w.first + i) * kKeys;
-        // tiles every row of the warp sees entirely skip the per-element mask
-        const bool full = __all_sync(0xffffffffu, lo <= j0 && j0 + kKeys - 1 <= hi);
-        float sv[128];
+        if (i == take - 1 && lane == 0) ptx::mbar_arrive(&sm.q_free[t]);
+        float sv[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, sv + c * 32);
+        for (int c = 0; c < 2; ++c) ptx::tmem_ld32(t_s + half * 64 + c * 32, sv + c * 32);
+        // columns that every row of the warp sees skip the per-element mask
+        const bool full0 = __all_sync(0xffffffffu, lo <= j0 && j0 + 31 <= hi);
+        const bool full1 = __all_sync(0xffffffffu, lo <= j0 + 32 && j0 + 63 <= hi);
         ptx::tmem_wait_ld();
-        if (!full) {
-          const bool a0 = anchored && j0 == 0;
+        if (!full0) {
+          const float s0 = sv[0];
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            sv[e] = (j0 + e >= lo && j0 + e <= hi) || (e == 0 && a0) ? sv[e] : -INFINITY;
+          for (int e = 0; e < 32; ++e) sv[e] = (j0 + e >= lo && j0 + e <= hi) ? sv[e] : -INFINITY;
+          if (j0 == 0 && anchored) sv[0] = s0;
         }
-        float mt = -INFINITY;
+        if (!full1) {
 #pragma unroll
-        for (int e = 0; e < 128; e += 2) mt = fmaxf(mt, fmaxf(sv[e], sv[e + 1]));
-        mt *= sl2;
-        // TMEM access is warp-collective, so a rescale of O is decided per warp
+          for (int e = 32; e < 64; ++e) sv[e] = (j0 + e >= lo && j0 + e <= hi) ? sv[e] : -INFINITY;
+        }
+        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mq[x] = fmaxf(mq[x], fmaxf(sv[e + 2 * x], sv[e + 2 * x + 1]));
+        float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        sm.pair[i & 1][t][half][r] = mt;
+        // both warps have read their columns of S: P may overwrite them
+        ok = ptx::bar_and(pair_bar, 64, true);
+        if (!ok) break;
+        mt = fmaxf(mt, sm.pair[i & 1][t][half ^ 1][r]) * sl2;
+        // TMEM access is warp-collective, so a rescale of O is decided per warp (alike for both)
         const bool need = (mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY);
         if (__any_sync(0xffffffffu, need)) {
           const float mn = fmaxf(m, mt);
@@ -474,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= f;
           if (i > 0) {  // O holds earlier tiles: S(i) done implies their PV is done
 #pragma unroll 1
-            for (int c = 0; c < HD / 16; ++c) {
+            for (int c = 0; c < HD / 32; ++c) {
               float ov[16];
               ptx::tmem_ld16(t_o + c * 16, ov);
               ptx::tmem_wait_ld();
@@ -485,14 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m = mn;
         }
-        float rs = 0.f;
         const float mm = (m == -INFINITY) ? 0.f : m;
+        const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(-mm, -mm);
+        float2 rs2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           const float* sc = sv + c * 32;
           uint32_t pw[16];
-          const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(-mm, -mm);
-          float2 rs2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 x = __ffma2_rn(make_float2(sc[2 * e], sc[2 * e + 1]), sl22, nm2);
@@ -500,28 +538,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             rs2 = __fadd2_rn(rs2, pp);
             pw[e] = ptx::pack_bf16x2(pp.x, pp.y);  // the weights enter the product in bf16, their sum stays fp32
           }
-          rs += rs2.x + rs2.y;
-          ptx::tmem_st16(t_s + c * 16, pw);
+          ptx::tmem_st16(t_s + half * 32 + c * 16, pw);
         }
-        l += rs;
+        l += rs2.x + rs2.y;
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&sm.p_full[t]);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.p_full[t]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&sm.o_full[t], nq & 1, b.err, abort_flag, 483));
       if (!ok) break;
-      // ---- epilogue. Its TMEM reads complete (tmem_wait_ld) before this
-      // thread's next p_full arrival, which the next piece's first PV of this
-      // tile (overwriting O) waits for.
+      ok = warp_wait(&sm.o_full[t], nq & 1, b.err, abort_flag, 483);
+      sm.pair[take & 1][t][half][r] = l;  // not the buffer of the last step, which the partner may still read
+      if (!ptx::bar_and(pair_bar, 64, ok)) break;
+      l += sm.pair[take & 1][t][half ^ 1][r];
+      // ---- epilogue, half of the channels per warp. Its TMEM reads complete
+      // (tmem_wait_ld) before this thread's next p_full arrival, which the next
+      // piece's first PV of this tile (overwriting O) waits for.
       ptx::tc_fence_after();
       ++nq;
       if (w.whole) {
         const int head = w.g * P.group + r - in_tile * P.group;
-        const int64_t row = w.q_row + tok;
+        const int64_t row = w.q_row + t * C.tile_tokens + in_tile;
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
-        __nv_bfloat16* orow = P.o + (row * P.Hq + head) * HD;
+        __nv_bfloat16* orow = P.o + (row * P.Hq + head) * HD + half * (HD / 2);
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
+        for (int c = 0; c < HD / 64; ++c) {
           float ov[32];
           ptx::tmem_ld32(t_o + c * 32, ov);
           ptx::tmem_wait_ld();
@@ -535,12 +576,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) dst[e] = make_uint4(ow[4 * e], ow[4 * e + 1], ow[4 * e + 2], ow[4 * e + 3]);
           }
         }
-        if (row_valid && P.lse) P.lse[(int64_t)head * b.T + row] = (m + log2f(l)) * 0.69314718055994531f;
+        if (row_valid && P.lse && half == 0) P.lse[(int64_t)head * b.T + row] = (m + log2f(l)) * 0.69314718055994531f;
       } else {
         const int64_t part = ((int64_t)blockIdx.x * 2 + w.part) * 2 + t;
-        float4* po = C.part_o + part * (HD / 4) * 128 + r;
+        float4* po = C.part_o + (part * (HD / 4) + half * (HD / 8)) * 128 + r;
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
+        for (int c = 0; c < HD / 64; ++c) {
           float ov[32];
           ptx::tmem_ld32(t_o + c * 32, ov);
           ptx::tmem_wait_ld();
@@ -548,8 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 8; ++e)
             po[(c * 8 + e) * 128] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
         }
-        C.part_ml[part * 128 + r] = make_float2(m, l);
+        if (half == 0) C.part_ml[part * 128 + r] = make_float2(m, l);
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.piece_empty[li & 1]);
     }
   }
 
@@ -559,12 +602,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining cut units
-// blockIdx.y = a border between two shares; the block of the first border
-// inside a unit joins that unit's partial results, 256 / (D / 4) rows of it per
-// blockIdx.x.
+// blockIdx.y = a border between two shares; the blocks of the first border
+// inside a unit join that unit's partial results, kJoinRows rows each.
+constexpr int kJoinRows = 32;
+
 template <int HD>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams C, int ctas) {
-  constexpr int kRows = 256 / (HD / 4);
+  constexpr int kStep = 256 / (HD / 4);  // rows at a time: consecutive threads read consecutive rows
   const AttendParams& P = C.a;
   const BatchParams& b = P.batch;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -578,31 +622,34 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   if (begin == border || first != (int)blockIdx.y) return;  // not cut here, or joined at an earlier border
   const int last = (int)((begin + count - 1) / shares.share);
   const Unit u = C.units[slot];
-  const int row = blockIdx.x * kRows + threadIdx.x % kRows, c = threadIdx.x / kRows;
-  const int t = row >> 7, r = row & 127, in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
-  if (in_tile >= C.tile_tokens || tok >= u.tokens) return;
-  auto part_of = [&](int cta) { return ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * 2 + t; };
-  float m = -INFINITY;
-  for (int k = first; k <= last; ++k) m = fmaxf(m, C.part_ml[part_of(k) * 128 + r].x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int k = first; k <= last; ++k) {
-    const float2 ml = C.part_ml[part_of(k) * 128 + r];
-    if (ml.x == -INFINITY) continue;
-    const float f = exp2f(ml.x - m);
-    const float4 v = C.part_o[(part_of(k) * (HD / 4) + c) * 128 + r];
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
-    l += f * ml.y;
+  const int c = threadIdx.x / kStep;
+#pragma unroll 2
+  for (int row = blockIdx.x * kJoinRows + threadIdx.x % kStep; row < (int)(blockIdx.x + 1) * kJoinRows; row += kStep) {
+    const int t = row >> 7, r = row & 127, in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
+    if (in_tile >= C.tile_tokens || tok >= u.tokens) continue;
+    auto part_of = [&](int cta) { return ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * 2 + t; };
+    float m = -INFINITY;
+    for (int k = first; k <= last; ++k) m = fmaxf(m, C.part_ml[part_of(k) * 128 + r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int k = first; k <= last; ++k) {
+      const float2 ml = C.part_ml[part_of(k) * 128 + r];
+      if (ml.x == -INFINITY) continue;
+      const float f = exp2f(ml.x - m);
+      const float4 v = C.part_o[(part_of(k) * (HD / 4) + c) * 128 + r];
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+      l += f * ml.y;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int head = g * P.group + r - in_tile * P.group;
+    const int64_t t_row = u.q_row + tok;
+    *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) =
+        make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (c == 0 && P.lse) P.lse[(int64_t)head * b.T + t_row] = (m + log2f(l)) * 0.69314718055994531f;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int head = g * P.group + r - in_tile * P.group;
-  const int64_t t_row = u.q_row + tok;
-  *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) =
-      make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (c == 0 && P.lse) P.lse[(int64_t)head * b.T + t_row] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------- launches
@@ -656,8 +703,7 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   e = launch_after(attend_chunk_kernel<HD>, dim3((unsigned)ctas), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel launch");
   if (ctas > 1) {
-    constexpr int kRows = 256 / (HD / 4);
-    e = launch_after(chunk_join_kernel<HD>, dim3(256 / kRows, (unsigned)(ctas - 1)), 256, 0, s, C, ctas);
+    e = launch_after(chunk_join_kernel<HD>, dim3(256 / kJoinRows, (unsigned)(ctas - 1)), 256, 0, s, C, ctas);
     if (e != cudaSuccess) return cuda_fail(e, "chunk_join_kernel launch");
   }
   return AA_OK;

@@ -46,6 +46,14 @@ struct ShortSmem {
   uint64_t full[kStages], empty[kStages];
 };
 
+// A converged warp waits; one lane polls (the other lanes' polling would take
+// shared-memory cycles from the products).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, int site) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = ptx::mbar_wait(bar, parity, kAttendWaitNs, err, site);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
 template <int HD, int RT>
 __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
     attend_short_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -108,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
         const int row = next;
         next = row_of(i + 1);  // in flight while this stage is waited for
         if (n >= kStages)
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sm.empty[s], (n / kStages - 1) & 1, kAttendWaitNs, b.err, 401));
+          ok = warp_wait(&sm.empty[s], (n / kStages - 1) & 1, b.err, 401);
         if (!ok) break;
         if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.full[s], kStageBytes);
         __syncwarp();
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
       }
       // every copy lands before the stages' memory is used for anything else
       for (int n = max(steps + issued - kStages, steps); n < steps + issued; ++n)
-        ptx::mbar_wait(&sm.full[n % kStages], (n / kStages) & 1, kAttendWaitNs, b.err, 403);
+        warp_wait(&sm.full[n % kStages], (n / kStages) & 1, b.err, 403);
     } else {
       // ---------------------------------------------------------- products and softmax
       const int rg = warp % RT, kg = warp / RT;  // row group, key group
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
 
       for (int i = begin; i < end; ++i) {
         const int n = steps + i - begin, s = n % kStages;
-        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.full[s], (n / kStages) & 1, kAttendWaitNs, b.err, 402))) break;
+        if (!warp_wait(&sm.full[s], (n / kStages) & 1, b.err, 402)) break;
         const int j0 = keys.tile(i) * kTileKeys, jw = j0 + kg * kWarpKeys;  // the tile's, the warp's first key
         float sc[kWarpKeys / 8][4];
 #pragma unroll

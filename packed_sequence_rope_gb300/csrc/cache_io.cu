@@ -13,6 +13,8 @@ namespace aa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 1;         // rows of a thread whose loads are in flight together
+constexpr int kFewTokens = 1024;  // up to here a block takes one token, for latency; above, four
 
 struct AppendParams {
   AxesTable tab;
@@ -24,75 +26,95 @@ struct AppendParams {
   int Hq, page_shift;
 };
 
+// Pool row of token t for kv head 0; -1 if it has none (an error), -2 if the
+// token lies outside the batch (a whole warp asks).
+__device__ __forceinline__ int64_t find_slot(const BatchParams& b, int t, int page_shift) {
+  // the search does not wait for the batch's ends
+  const int begin = __ldg(b.cu_q), end = __ldg(b.cu_q + b.B);
+  const int seq = warp_find_seq(b.cu_q, b.B, t);
+  const int p = __ldg(b.kv_len + seq) - __ldg(b.cu_q + seq + 1) + t, w = p >> page_shift;
+  if (t >= b.T || t < begin || t >= end) return -2;
+  const bool report = (threadIdx.x & 31) == 0;
+  if (p < 0 || w >= b.W) {
+    if (report) atomicCAS(b.err, 0, kCacheBadPosition);
+    return -1;
+  }
+  const int page = __ldg(b.table + (int64_t)seq * b.W + w);
+  if (page < 0 || page >= b.num_pages) {
+    if (report) atomicCAS(b.err, 0, kCacheBadPage);
+    return -1;
+  }
+  return (((b.layer_page0 + page) * b.Hkv) << page_shift) + (p & ((1 << page_shift) - 1));
+}
+
 // L: the pairing (0, 1), or 2 to store the keys as they are. A block takes
 // kTokens rows; as in rope_axes_kernel the angles of a token are computed once
-// for all heads.
+// for all heads, while the first rows are in flight.
 template <int HD, int L, int kTokens>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int kHalf = HD / 2, kChunks = HD / 16, kRows = kThreads / kChunks / kTokens;
   static_assert(kTokens <= kThreads / 32, "a warp looks up each token");
   __shared__ float2 cs[L == 2 ? 1 : kTokens][kHalf];
-  __shared__ int64_t slot[kTokens];  // pool row of head 0; -1: not written, -2: no token
+  __shared__ int64_t slot[kTokens];
   const BatchParams& b = P.batch;
   const int t0 = (int)blockIdx.x * kTokens, warp = threadIdx.x >> 5;
+  const int chunk = threadIdx.x % kChunks, row = threadIdx.x / kChunks;
+  const int tok = row / kRows, heads = P.Hq + 2 * b.Hkv;
+  const int64_t t = t0 + tok;
+  auto load = [&](Pairs8<HD, L == 2 ? 0 : L>& x, int h) {
+    if (t >= b.T || h >= heads) return;
+    const int g = h - P.Hq;
+    x.load(g < 0 ? P.q + t * P.q_stride + (int64_t)h * HD
+                 : g < b.Hkv ? P.k + t * P.k_stride + (int64_t)g * HD : P.v + t * P.v_stride + (int64_t)(g - b.Hkv) * HD,
+           chunk);
+  };
+  Pairs8<HD, L == 2 ? 0 : L> x[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) load(x[i], row % kRows + i * kRows);
   if (warp < kTokens) {
-    const int t = t0 + warp;
-    int64_t at = -2;
-    if (t < b.T && t >= __ldg(b.cu_q) && t < __ldg(b.cu_q + b.B)) {
-      const int seq = warp_find_seq(b.cu_q, b.B, t);
-      const int p = __ldg(b.kv_len + seq) - __ldg(b.cu_q + seq + 1) + t;
-      const int w = p >> P.page_shift;
-      at = -1;
-      if (p < 0 || w >= b.W) {
-        if ((threadIdx.x & 31) == 0) atomicCAS(b.err, 0, kCacheBadPosition);
-      } else {
-        const int page = __ldg(b.table + (int64_t)seq * b.W + w);
-        if (page < 0 || page >= b.num_pages) {
-          if ((threadIdx.x & 31) == 0) atomicCAS(b.err, 0, kCacheBadPage);
-        } else {
-          at = (((b.layer_page0 + page) * b.Hkv) << P.page_shift) + (p & ((1 << P.page_shift) - 1));
-        }
-      }
-    }
+    const int64_t at = find_slot(b, t0 + warp, P.page_shift);
     if ((threadIdx.x & 31) == 0) slot[warp] = at;
   }
   if constexpr (L != 2) {
-    for (int e = threadIdx.x; e < kTokens * kHalf; e += kThreads) {
-      const int tok = e / kHalf, p = e % kHalf;
-      if (t0 + tok < b.T) cs[tok][p] = axes_cs(P.tab, P.pos, b.T, t0 + tok, p);
+    for (int e = kThreads - 1 - (int)threadIdx.x; e < kTokens * kHalf; e += kThreads) {  // the searching warps come last
+      const int at = e / kHalf, p = e % kHalf;
+      if (t0 + at < b.T) cs[at][p] = axes_cs(P.tab, P.pos, b.T, t0 + at, p);
     }
   }
   __syncthreads();
-  const int chunk = threadIdx.x % kChunks, row = threadIdx.x / kChunks;
-  const int tok = row / kRows;
-  const int64_t t = t0 + tok, at = slot[tok];
+  const int64_t at = slot[tok];
   if (at == -2) return;
   float2 mine[8];
   if constexpr (L != 2) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) mine[e] = cs[tok][8 * chunk + e];
   }
-  for (int h = row % kRows; h < P.Hq + 2 * b.Hkv; h += kRows) {
-    Pairs8<HD, L == 2 ? 0 : L> x;
-    if (h < P.Hq) {
-      x.load(P.q + t * P.q_stride + (int64_t)h * HD, chunk);
-      if constexpr (L != 2) x.turn(mine);
-      x.store(P.q_out + (t * P.Hq + h) * HD, chunk);
-    } else if (at >= 0) {
-      const bool is_k = h < P.Hq + b.Hkv;
-      const int g = h - P.Hq - (is_k ? 0 : b.Hkv);
-      x.load(is_k ? P.k + t * P.k_stride + (int64_t)g * HD : P.v + t * P.v_stride + (int64_t)g * HD, chunk);
+  for (int h0 = row % kRows; h0 < heads; h0 += kBatch * kRows) {
+    if (h0 >= kRows) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) load(x[i], h0 + i * kRows);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * kRows, g = h - P.Hq;
+      if (h >= heads) break;
       if constexpr (L != 2)
-        if (is_k) x.turn(mine);
-      x.store((is_k ? P.k_pages : P.v_pages) + (at + ((int64_t)g << P.page_shift)) * HD, chunk);
+        if (g < b.Hkv) x[i].turn(mine);
+      if (g < 0)
+        x[i].store(P.q_out + (t * P.Hq + h) * HD, chunk);
+      else if (at >= 0)
+        x[i].store((g < b.Hkv ? P.k_pages + (at + ((int64_t)g << P.page_shift)) * HD
+                              : P.v_pages + (at + ((int64_t)(g - b.Hkv) << P.page_shift)) * HD), chunk);
     }
   }
 }
 
 template <int HD, int L>
 cudaError_t launch_append(const AppendParams& P, cudaStream_t s) {
-  constexpr int kTokens = 4;
-  cache_append_kernel<HD, L, kTokens><<<(unsigned)((P.batch.T + kTokens - 1) / kTokens), kThreads, 0, s>>>(P);
+  if (P.batch.T <= kFewTokens)
+    cache_append_kernel<HD, L, 1><<<(unsigned)P.batch.T, kThreads, 0, s>>>(P);
+  else
+    cache_append_kernel<HD, L, 4><<<(unsigned)((P.batch.T + 3) / 4), kThreads, 0, s>>>(P);
   return cudaGetLastError();
 }
 

@@ -269,6 +269,52 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                : "memory");
 }
 
+// The same products issued by a whole, converged warp: one elected thread
+// issues them. No branch surrounds them and only the descriptors' low words
+// move, so that the operands can stay in uniform registers.
+#define AA_MMA_WARP_SS_STEP(ao, bo)                                                       \
+  "add.u32 la, al, " #ao ";\n\tadd.u32 lb, bl, " #bo ";\n\t"                          \
+  "mov.b64 ra, {la, ah};\n\tmov.b64 rb, {lb, bh};\n\t"                                \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ra, rb, %3, t;\n\t"
+#define AA_MMA_WARP_TS_STEP(ao, bo)                                                       \
+  "add.u32 la, %1, " #ao ";\n\tadd.u32 lb, bl, " #bo ";\n\tmov.b64 rb, {lb, bh};\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], rb, %3, t;\n\t"
+#define AA_MMA_WARP_PROLOGUE                                                              \
+  "{\n\t.reg .pred p, t, e;\n\t.reg .b64 ra, rb;\n\t.reg .b32 al, ah, bl, bh, la, lb;\n\t" \
+  "elect.sync _|e, 0xffffffff;\n\tmov.b64 {bl, bh}, %2;\n\t"                          \
+  "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+__device__ __forceinline__ void mma8_ss_kk_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(AA_MMA_WARP_PROLOGUE
+               "mov.b64 {al, ah}, %1;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+               AA_MMA_WARP_SS_STEP(2, 2) AA_MMA_WARP_SS_STEP(4, 4) AA_MMA_WARP_SS_STEP(6, 6)
+               AA_MMA_WARP_SS_STEP(1024, 1024) AA_MMA_WARP_SS_STEP(1026, 1026) AA_MMA_WARP_SS_STEP(1028, 1028)
+               AA_MMA_WARP_SS_STEP(1030, 1030) "}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma4_ss_kk_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(AA_MMA_WARP_PROLOGUE
+               "mov.b64 {al, ah}, %1;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+               AA_MMA_WARP_SS_STEP(2, 2) AA_MMA_WARP_SS_STEP(4, 4) AA_MMA_WARP_SS_STEP(6, 6) "}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma8_ts_seq_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(AA_MMA_WARP_PROLOGUE
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+               AA_MMA_WARP_TS_STEP(8, 128) AA_MMA_WARP_TS_STEP(16, 256) AA_MMA_WARP_TS_STEP(24, 384)
+               AA_MMA_WARP_TS_STEP(32, 512) AA_MMA_WARP_TS_STEP(40, 640) AA_MMA_WARP_TS_STEP(48, 768)
+               AA_MMA_WARP_TS_STEP(56, 896) "}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// Arrive once on `bar` when all products that the elected thread has issued finish.
+__device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 // Each thread of the warp reads 32 consecutive fp32 columns of its own lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];

@@ -13,6 +13,8 @@ namespace aa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 1;         // rows of a thread whose loads are in flight together
+constexpr int kFewTokens = 1024;  // up to here a block takes one token, for latency; above, four
 
 struct ApplyParams {
   AxesTable tab;
@@ -28,37 +30,51 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_consta
   constexpr int kHalf = HD / 2, kChunks = HD / 16, kRows = kThreads / kChunks / kTokens;
   __shared__ float2 cs[kTokens][kHalf];
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int chunk = threadIdx.x % kChunks, row = threadIdx.x / kChunks;
+  const int tok = row / kRows, heads = P.Hq + P.Hk;
+  const int64_t t = t0 + tok;
+  auto load = [&](Pairs8<HD, L>& x, int h) {
+    if (t < P.T && h < heads)
+      x.load(h < P.Hq ? P.q + t * P.q_stride + (int64_t)h * HD : P.k + t * P.k_stride + (int64_t)(h - P.Hq) * HD, chunk);
+  };
+  // the first rows are in flight while the angles are computed
+  Pairs8<HD, L> x[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) load(x[i], row % kRows + i * kRows);
   for (int e = threadIdx.x; e < kTokens * kHalf; e += kThreads) {
-    const int tok = e / kHalf, p = e % kHalf;
-    if (t0 + tok < P.T) {
-      float2 v = axes_cs(P.tab, P.pos, P.T, t0 + tok, p);
+    const int at = e / kHalf, p = e % kHalf;
+    if (t0 + at < P.T) {
+      float2 v = axes_cs(P.tab, P.pos, P.T, t0 + at, p);
       if (P.inverse) v.y = -v.y;
-      cs[tok][p] = v;
+      cs[at][p] = v;
     }
   }
   __syncthreads();
-  const int chunk = threadIdx.x % kChunks, row = threadIdx.x / kChunks;
-  const int tok = row / kRows;
-  const int64_t t = t0 + tok;
   if (t >= P.T) return;
   float2 mine[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) mine[e] = cs[tok][8 * chunk + e];
-  for (int h = row % kRows; h < P.Hq + P.Hk; h += kRows) {
-    const bool is_q = h < P.Hq;
-    const __nv_bfloat16* src = is_q ? P.q + t * P.q_stride + (int64_t)h * HD : P.k + t * P.k_stride + (int64_t)(h - P.Hq) * HD;
-    __nv_bfloat16* dst = is_q ? P.q_out + (t * P.Hq + h) * HD : P.k_out + (t * P.Hk + h - P.Hq) * HD;
-    Pairs8<HD, L> x;
-    x.load(src, chunk);
-    x.turn(mine);
-    x.store(dst, chunk);
+  for (int h0 = row % kRows; h0 < heads; h0 += kBatch * kRows) {
+    if (h0 >= kRows) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) load(x[i], h0 + i * kRows);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * kRows;
+      if (h >= heads) break;
+      x[i].turn(mine);
+      x[i].store(h < P.Hq ? P.q_out + (t * P.Hq + h) * HD : P.k_out + (t * P.Hk + h - P.Hq) * HD, chunk);
+    }
   }
 }
 
 template <int HD, int L>
 cudaError_t launch(const ApplyParams& P, cudaStream_t s) {
-  constexpr int kTokens = 4;
-  rope_axes_kernel<HD, L, kTokens><<<(unsigned)((P.T + kTokens - 1) / kTokens), kThreads, 0, s>>>(P);
+  if (P.T <= kFewTokens)
+    rope_axes_kernel<HD, L, 1><<<(unsigned)P.T, kThreads, 0, s>>>(P);
+  else
+    rope_axes_kernel<HD, L, 4><<<(unsigned)((P.T + 3) / 4), kThreads, 0, s>>>(P);
   return cudaGetLastError();
 }
 
