@@ -22,7 +22,7 @@
 //   warp 0      finds the CTA's next piece of work and copies its query tiles and
 //               the key tiles' pages (tensor copies, one page piece per lane)
 //   warp 1      owns tensor memory and issues the products
-//   warp 2      clears values that no row sees (a page's unused rows)
+//   warps 2, 3  clear values that no row sees (a page's unused rows)
 //   warps 4-11  row tile 0: online softmax and epilogue; lane = row, two warps per
 //               32 rows with half of the columns each, which exchange the rows'
 //               maxima through shared memory
@@ -41,7 +41,7 @@ namespace {
 constexpr int kKeys = 128;
 constexpr int kSoftmaxWarps = 16;
 constexpr int kThreads = 32 * (4 + kSoftmaxWarps);
-constexpr int kReaders = 2 + kSoftmaxWarps;  // of a published piece: warps 1 and 2, the softmax warps
+constexpr int kReaders = 3 + kSoftmaxWarps;  // of a published piece: warps 1 to 3, the softmax warps
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
@@ -52,6 +52,12 @@ struct Unit {
   int32_t seq, q_row, tokens, p0, lo;
 };
 
+// A cut unit, as the CTA that begins it describes it to chunk_join_kernel: its
+// parts lie with the CTAs from that one to `last`. last < 0: the CTA begins none.
+struct Cut {
+  int32_t last, g, q_row, tokens;
+};
+
 struct ChunkParams {
   AttendParams a;
   int tile_tokens;     // tokens per row tile: 128 / group
@@ -60,6 +66,7 @@ struct ChunkParams {
   Unit* units;         // [slots]
   float4* part_o;      // [CTA][2][row tile][D / 4][128]: unnormalised O of a cut unit
   float2* part_ml;     // [CTA][2][row tile][128]: maximum (log2 units), sum
+  Cut* cuts;           // [CTA]
 };
 
 // ---------------------------------------------------------------- the plan
@@ -155,36 +162,42 @@ template <int HD>
 struct ChunkSmem {
   static constexpr int kB = HD / 64;
   static constexpr int kStages = HD == 128 ? 2 : 4;
-  alignas(1024) uint8_t q[2][kB][16384];
+  // a piece's two row tiles of Q and one of the next piece: its first S product
+  // does not wait for a copy
+  static constexpr int kQ = 3;
+  alignas(1024) uint8_t q[kQ][kB][16384];
   alignas(1024) uint8_t k[kStages][kB][16384];
   alignas(1024) uint8_t v[kStages][kB][16384];
-  uint64_t q_full[2], q_free[2];
+  uint64_t q_full[kQ], q_free[kQ];
   uint64_t piece_full[2], piece_empty[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], drain;
   Piece piece[2];
-  float pair[2][2][2][128];  // [step parity][row tile][column half][row]: maxima, then sums
+  // between the two warps of 32 rows, [column half][lane]: maxima of a step (by
+  // its parity; rounded to bf16: any bound near the maximum serves), then sums
+  union {
+    __nv_bfloat16 max[2][2][32];
+    float sum[2][32];
+  } pair[2][4];  // [row tile][32 rows]
   uint32_t tmem_base;
   int abort_flag;
 };
 
 // A converged warp waits, bounded, and gives up with the rest of the CTA. One
-// lane polls: with all lanes of all waiting warps polling, their traffic on
-// shared memory slowed the products' operand reads to half.
+// lane asks, and sleeps meanwhile: polling warps take issue slots and
+// shared-memory cycles from the products and the softmax.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort_flag, int site) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0 && !ptx::mbar_try_wait(bar, parity)) {
+  if ((threadIdx.x & 31) == 0 && !ptx::mbar_try_wait_for(bar, parity, kSleepNs)) {
     const uint64_t t0 = ptx::global_timer_ns();
-    for (int i = 1;; ++i) {
-      if (ptx::mbar_try_wait(bar, parity)) break;
-      if (i % 64) continue;
-      if (*abort_flag) ok = false;
-      if (ok && ptx::global_timer_ns() - t0 >= kAttendWaitNs) {
+    while (ok && !ptx::mbar_try_wait_for(bar, parity, kSleepNs)) {
+      if (*abort_flag) {
+        ok = false;
+      } else if (ptx::global_timer_ns() - t0 >= kAttendWaitNs) {
         atomicCAS(err, 0, site);
         *abort_flag = 1;
         ok = false;
       }
-      if (!ok) break;
     }
   }
   return __all_sync(0xffffffffu, ok);
@@ -202,15 +215,15 @@ __device__ __forceinline__ bool read_piece(Smem& sm, int li, int32_t* err, volat
 
 // Barrier phases: pieces count the piece ring; the K and V rings count the
 // CTA's key tiles over all its pieces; s_full / p_full count each row tile's
-// softmax steps; q_full, q_free and o_full the pieces in which the row tile
-// exists. As in the packed forward every wait is bounded and its outcome made
+// softmax steps; q_full and q_free the CTA's row tiles of Q; o_full the pieces
+// in which the row tile exists. As in the packed forward every wait is bounded and its outcome made
 // uniform in a warp before anything collective.
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ChunkParams C) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  constexpr int kB = HD / 64, kStages = ChunkSmem<HD>::kStages, kTmemCols = 512;
+  constexpr int kB = HD / 64, kStages = ChunkSmem<HD>::kStages, kQ = ChunkSmem<HD>::kQ, kTmemCols = 512;
   constexpr uint32_t kTileBytes = kKeys * HD * 2;
   const AttendParams& P = C.a;
   const BatchParams& b = P.batch;
@@ -227,17 +240,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tma_prefetch_desc(&tmK);
     ptx::tma_prefetch_desc(&tmV);
     for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(&sm.q_full[t], 1);
-      ptx::mbar_init(&sm.q_free[t], kSoftmaxWarps / 2);
       ptx::mbar_init(&sm.s_full[t], 1);
       ptx::mbar_init(&sm.p_full[t], kSoftmaxWarps / 2);
       ptx::mbar_init(&sm.o_full[t], 1);
       ptx::mbar_init(&sm.piece_full[t], 1);
       ptx::mbar_init(&sm.piece_empty[t], kReaders);
     }
+    for (int s = 0; s < kQ; ++s) {
+      ptx::mbar_init(&sm.q_full[s], 1);
+      ptx::mbar_init(&sm.q_free[s], 1);
+    }
     for (int s = 0; s < kStages; ++s) {
-      for (uint64_t* bar : {&sm.k_full[s], &sm.k_empty[s], &sm.v_full[s], &sm.v_clean[s], &sm.v_empty[s]})
-        ptx::mbar_init(bar, 1);
+      for (uint64_t* bar : {&sm.k_full[s], &sm.k_empty[s], &sm.v_full[s], &sm.v_empty[s]}) ptx::mbar_init(bar, 1);
+      ptx::mbar_init(&sm.v_clean[s], 2);
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -256,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Shares shares(C, gridDim.x);
     int64_t at = shares.share * blockIdx.x;
     const int64_t end = min(at + shares.share, shares.all);
-    int nq[2] = {0, 0}, ks = 0, nk = 0;  // key tiles whose V, whose K has been asked for
+    Cut cut{-1, 0, 0, 0};
+    int nq = 0, ks = 0, nk = 0;  // row tiles of Q, key tiles whose V, whose K has been asked for
     bool ok = true;
     // a key tile is `pieces` page pieces, each kB column blocks of K, then of V
     const int piece_shift = min(P.page_shift, 6), pieces = kKeys >> piece_shift;
@@ -280,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.first = (int)(at - begin);
         w.take = (int)min((int64_t)(count - w.first), end - at);
         w.whole = w.take == count;
-        w.part = w.first == 0 ? 1 : 0;  // a cut unit starts in at most one share and ends in at most one
+        w.part = w.first == 0 ? 1 : 0;  // the first part of a cut unit, or a later one: at most one of each per CTA
+        if (w.first == 0 && !w.whole) cut = Cut{(int32_t)((begin + count - 1) / shares.share), w.g, w.q_row, w.tokens};
         at += w.take;
       }
       if (lane == 0) {
@@ -319,26 +336,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ks;
       };
       // the first key tile goes ahead of the queries, whose buffers the piece
-      // before still reads
+      // before may still read
       load_keys(w.first);
-      for (int t = 0; t < (w.tokens > C.tile_tokens ? 2 : 1) && ok; ++t) {
-        // the tile's previous Q has had its last S product
-        if (nq[t] > 0)
-          ok = warp_wait(&sm.q_free[t], (nq[t] - 1) & 1, b.err, abort_flag, 450);
+      for (int t = 0; t < (w.tokens > C.tile_tokens ? 2 : 1) && ok; ++t, ++nq) {
+        const int q = nq % kQ;
+        if (nq >= kQ) ok = warp_wait(&sm.q_free[q], (nq / kQ - 1) & 1, b.err, abort_flag, 450);
         if (!ok) break;
         if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&sm.q_full[t], (uint32_t)(C.tile_tokens * P.group * HD * 2));
+          ptx::mbar_arrive_expect_tx(&sm.q_full[q], (uint32_t)(C.tile_tokens * P.group * HD * 2));
           for (int c = 0; c < kB; ++c)
-            ptx::tma_load_4d(sm.q[t][c], &tmQ, &sm.q_full[t], c * 64, 0, w.g, w.q_row + t * C.tile_tokens);
+            ptx::tma_load_4d(sm.q[q][c], &tmQ, &sm.q_full[q], c * 64, 0, w.g, w.q_row + t * C.tile_tokens);
         }
         __syncwarp();
-        ++nq[t];
       }
       for (int i = w.first + 1; i < w.first + w.take && ok; ++i) load_keys(i);
     }
+    if (lane == 0) C.cuts[blockIdx.x] = cut;
     // every issued copy lands before the CTA exits
-    for (int t = 0; t < 2; ++t)
-      if (nq[t] > 0) ptx::mbar_wait(&sm.q_full[t], (nq[t] - 1) & 1, kDrainNs, b.err, 459);
+    for (int u = max(nq - kQ, 0); u < nq; ++u)
+      ptx::mbar_wait(&sm.q_full[u % kQ], (u / kQ) & 1, kDrainNs, b.err, 459);
     for (int u = max(nk - kStages, 0); u < nk; ++u)
       ptx::mbar_wait(&sm.k_full[u % kStages], (u / kStages) & 1, kDrainNs, b.err, 459);
     for (int u = max(ks - kStages, 0); u < ks; ++u)
@@ -347,11 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer (the whole warp, converged)
     constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128, 0, 0);
     constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, 0, 1);
-    uint32_t ph_p[2] = {0, 0}, ph_q[2] = {0, 0};
-    int ks = 0;
+    uint32_t ph_p[2] = {0, 0};
+    int ks = 0, nq = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) { return warp_wait(bar, parity, b.err, abort_flag, site); };
-    auto issue_s = [&](int t, int s) {
-      const uint64_t qd = ptx::smem_desc_sw128(ptx::smem_u32(sm.q[t][0]), 16, 1024);
+    // S of row tile t, its Q in buffer q, and the keys of stage s
+    auto issue_s = [&](int t, int q, int s) {
+      const uint64_t qd = ptx::smem_desc_sw128(ptx::smem_u32(sm.q[q][0]), 16, 1024);
       const uint64_t kd = ptx::smem_desc_sw128(ptx::smem_u32(sm.k[s][0]), 16, 1024);
       if constexpr (HD == 128)
         ptx::mma8_ss_kk_warp(tmem + 128 * t, qd, kd, idesc_s, 0);
@@ -366,15 +383,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the reductions make the loops' bounds uniform for the compiler
       const int take = __reduce_max_sync(0xffffffffu, w.take);
       const int tiles = __all_sync(0xffffffffu, w.tokens > C.tile_tokens) ? 2 : 1;
+      const int q[2] = {nq % kQ, (nq + 1) % kQ};
       // the first S products, as the piece's K and Q land
       if (!(ok = wait(&sm.k_full[ks % kStages], (ks / kStages) & 1, 463))) break;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (t >= tiles) break;
-        if (!(ok = wait(&sm.q_full[t], ph_q[t], 462))) break;
-        ph_q[t] ^= 1;
+        if (!(ok = wait(&sm.q_full[q[t]], ((nq + t) / kQ) & 1, 462))) break;
         ptx::tc_fence_after();
-        issue_s(t, ks % kStages);
+        issue_s(t, q[t], ks % kStages);
+        if (take == 1) ptx::mma_commit_warp(&sm.q_free[q[t]]);
       }
       if (!ok) break;
       ptx::mma_commit_warp(&sm.k_empty[ks % kStages]);
@@ -394,22 +412,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mma8_ts_seq_warp(tmem + 256 + HD * t, tmem + 128 * t,
                                 ptx::smem_desc_sw128(ptx::smem_u32(sm.v[s][0]), 16384, 1024), idesc_pv, i == 0 ? 0u : 1u);
           if (more)
-            issue_s(t, s1);
+            issue_s(t, q[t], s1);
           else
             ptx::mma_commit_warp(&sm.o_full[t]);
+          if (i + 2 == take) ptx::mma_commit_warp(&sm.q_free[q[t]]);
         }
         if (!ok) break;
         ptx::mma_commit_warp(&sm.v_empty[s]);
         if (more) ptx::mma_commit_warp(&sm.k_empty[s1]);
       }
+      nq += tiles;
     }
     // every issued MMA must finish before TMEM is released
     __syncwarp();
     ptx::mma_commit_warp(&sm.drain);
     ptx::mbar_wait(&sm.drain, 0, kDrainNs, b.err, 469);
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ clearing unseen values
-    // the rows of V that no row of the unit sees have weight 0, but 0 * NaN is not
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ clearing unseen values (warps 2 and 3)
+    // The rows of V that no row of the unit sees have weight 0, but 0 * NaN is
+    // not. Pieces that were not looked up hold zeros already, which leaves the
+    // unseen rows of the pieces at the ends of [lo, hi], and behind the anchor.
+    constexpr int kChunks = kB * 8, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row, rows a warp clears at once
+    const int piece = 1 << min(P.page_shift, 6), chunk = lane % kChunks;
+    const int first_row = (warp - 2) * kRowsAtOnce + lane / kChunks;
     int ks = 0;
     bool ok = true;
     for (int li = 0; ok; ++li) {
@@ -419,14 +444,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const KeyTiles<kKeys> keys(w.lo, hi, P.anchor);
       for (int i = w.first; i < w.first + w.take; ++i, ++ks) {
         const int s = ks % kStages;
-        ok = warp_wait(&sm.v_full[s], (ks / kStages) & 1, b.err, abort_flag, 471);
-        if (!ok) break;
+        if (!(ok = warp_wait(&sm.v_full[s], (ks / kStages) & 1, b.err, abort_flag, 471))) break;
         const int j0 = keys.tile(i) * kKeys;
         if (j0 < w.lo || j0 + kKeys - 1 > hi) {
-          for (int x = lane; x < kKeys * kB * 8; x += 32) {
-            const int key = x / (kB * 8), j = j0 + key;
-            if (!((j >= w.lo && j <= hi) || (j == 0 && P.anchor)))
-              *reinterpret_cast<uint4*>(sm.v[s][(x >> 3) % kB] + key * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          auto clear = [&](int from, int to) {  // rows of the tile
+            from = max(from, 0);
+            to = min(to, kKeys);
+#pragma unroll 4
+            for (int row = from + first_row; row < to; row += 2 * kRowsAtOnce)
+              *reinterpret_cast<uint4*>(sm.v[s][chunk >> 3] + row * 128 + (chunk & 7) * 16) = make_uint4(0, 0, 0, 0);
+          };
+          const bool anchored = P.anchor && j0 == 0 && hi >= 0 && w.lo > 0;
+          const int lo_piece = w.lo & ~(piece - 1);  // its copy starts here
+          if (anchored) clear(1, min(piece, w.lo));
+          if (w.lo <= hi) {
+            clear(max(lo_piece - j0, anchored ? 1 : 0), w.lo - j0);
+            clear(hi + 1 - j0, (hi | (piece - 1)) + 1 - j0);
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -434,10 +467,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&sm.v_clean[s]);
       }
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
     const int pair_bar = 1 + t * 4 + (warp & 3);  // named barrier of the two warps with the same rows
+    auto& pair = sm.pair[t][warp & 3];
     const float sl2 = P.scale_log2;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + 128 * t + lane_off, t_o = tmem + 256 + HD * t + half * (HD / 2) + lane_off;
@@ -475,8 +509,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ph_s ^= 1;
         ptx::tc_fence_after();
-        // the piece's last S product of this tile is done: Q may be replaced
-        if (i == take - 1 && lane == 0) ptx::mbar_arrive(&sm.q_free[t]);
+        // The row's maximum over both column halves, and what it changes. Also the
+        // point where both warps have read their columns of S: P may overwrite them.
+        auto agree = [&](float mt) {
+          pair.max[i & 1][half][lane] = __float2bfloat16_ru(mt);
+          if (!ptx::bar_and(pair_bar, 64, true)) return false;
+          mt = __bfloat162float(__hmax(pair.max[i & 1][0][lane], pair.max[i & 1][1][lane])) * sl2;
+          // TMEM access is warp-collective, so a rescale of O is decided per warp (alike for both)
+          const bool need = (mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY);
+          if (__any_sync(0xffffffffu, need)) {
+            const float mn = fmaxf(m, mt);
+            const float f = (m == -INFINITY) ? 0.f : exp2f(m - mn);
+            l *= f;
+            if (i > 0) {  // O holds earlier tiles: S(i) done implies their PV is done
+#pragma unroll 1
+              for (int c = 0; c < HD / 32; ++c) {
+                float ov[16];
+                ptx::tmem_ld16(t_o + c * 16, ov);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ov[e] *= f;
+                ptx::tmem_st16f(t_o + c * 16, ov);
+              }
+            }
+            m = mn;
+          }
+          return true;
+        };
+        const uint32_t t_p = t_s + half * 32;
         float sv[64];
 #pragma unroll
         for (int c = 0; c < 2; ++c) ptx::tmem_ld32(t_s + half * 64 + c * 32, sv + c * 32);
@@ -499,31 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 64; e += 8)
 #pragma unroll
           for (int x = 0; x < 4; ++x) mq[x] = fmaxf(mq[x], fmaxf(sv[e + 2 * x], sv[e + 2 * x + 1]));
-        float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-        sm.pair[i & 1][t][half][r] = mt;
-        // both warps have read their columns of S: P may overwrite them
-        ok = ptx::bar_and(pair_bar, 64, true);
-        if (!ok) break;
-        mt = fmaxf(mt, sm.pair[i & 1][t][half ^ 1][r]) * sl2;
-        // TMEM access is warp-collective, so a rescale of O is decided per warp (alike for both)
-        const bool need = (mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY);
-        if (__any_sync(0xffffffffu, need)) {
-          const float mn = fmaxf(m, mt);
-          const float f = (m == -INFINITY) ? 0.f : exp2f(m - mn);
-          l *= f;
-          if (i > 0) {  // O holds earlier tiles: S(i) done implies their PV is done
-#pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-              float ov[16];
-              ptx::tmem_ld16(t_o + c * 16, ov);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ov[e] *= f;
-              ptx::tmem_st16f(t_o + c * 16, ov);
-            }
-          }
-          m = mn;
-        }
+        if (!(ok = agree(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]))))) break;
         const float mm = (m == -INFINITY) ? 0.f : m;
         const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(-mm, -mm);
         float2 rs2 = make_float2(0.f, 0.f);
@@ -538,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rs2 = __fadd2_rn(rs2, pp);
             pw[e] = ptx::pack_bf16x2(pp.x, pp.y);  // the weights enter the product in bf16, their sum stays fp32
           }
-          ptx::tmem_st16(t_s + half * 32 + c * 16, pw);
+          ptx::tmem_st16(t_p + c * 16, pw);
         }
         l += rs2.x + rs2.y;
         ptx::tmem_wait_st();
@@ -548,9 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       ok = warp_wait(&sm.o_full[t], nq & 1, b.err, abort_flag, 483);
-      sm.pair[take & 1][t][half][r] = l;  // not the buffer of the last step, which the partner may still read
+      pair.sum[half][lane] = l;  // the partner has read the last step's maxima: O is complete
       if (!ptx::bar_and(pair_bar, 64, ok)) break;
-      l += sm.pair[take & 1][t][half ^ 1][r];
+      l += pair.sum[half ^ 1][lane];
       // ---- epilogue, half of the channels per warp. Its TMEM reads complete
       // (tmem_wait_ld) before this thread's next p_full arrival, which the next
       // piece's first PV of this tile (overwriting O) waits for.
@@ -560,23 +596,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int head = w.g * P.group + r - in_tile * P.group;
         const int64_t row = w.q_row + t * C.tile_tokens + in_tile;
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
-        __nv_bfloat16* orow = P.o + (row * P.Hq + head) * HD + half * (HD / 2);
+        if (row_valid && P.lse && half == 0) P.lse[(int64_t)head * b.T + row] = (m + log2f(l)) * 0.69314718055994531f;
+        // four lanes store 64 bytes of one row together: they swap their
+        // 16-byte quarters of 32 channels so that lane q holds quarter q of
+        // the four rows
+        const int at = row_valid ? (int)(row * P.Hq + head) : -1, q = lane & 3;
+        int rows[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rows[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
 #pragma unroll 1
         for (int c = 0; c < HD / 64; ++c) {
           float ov[32];
           ptx::tmem_ld32(t_o + c * 32, ov);
           ptx::tmem_wait_ld();
-          if (row_valid) {
-            uint32_t ow[16];
+          uint32_t ow[4][4];  // [quarter][word]
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              ow[e] = l > 0.f ? ptx::pack_bf16x2(ov[2 * e] * inv_l, ov[2 * e + 1] * inv_l) : 0u;
-            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+          for (int e = 0; e < 16; ++e)
+            ow[e >> 2][e & 3] = l > 0.f ? ptx::pack_bf16x2(ov[2 * e] * inv_l, ov[2 * e + 1] * inv_l) : 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(ow[4 * e], ow[4 * e + 1], ow[4 * e + 2], ow[4 * e + 3]);
+          for (int x = 0; x < 4; ++x) {
+#pragma unroll
+            for (int d = 1; d <= 2; d *= 2)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (k & d) continue;
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, (q & d) ? ow[k][x] : ow[k + d][x], d);
+                if (q & d)
+                  ow[k][x] = other;
+                else
+                  ow[k + d][x] = other;
+              }
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (rows[k] >= 0)
+              *reinterpret_cast<uint4*>(P.o + (int64_t)rows[k] * HD + half * (HD / 2) + c * 32 + q * 8) =
+                  make_uint4(ow[k][0], ow[k][1], ow[k][2], ow[k][3]);
         }
-        if (row_valid && P.lse && half == 0) P.lse[(int64_t)head * b.T + row] = (m + log2f(l)) * 0.69314718055994531f;
       } else {
         const int64_t part = ((int64_t)blockIdx.x * 2 + w.part) * 2 + t;
         float4* po = C.part_o + (part * (HD / 4) + half * (HD / 8)) * 128 + r;
@@ -602,53 +658,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining cut units
-// blockIdx.y = a border between two shares; the blocks of the first border
-// inside a unit join that unit's partial results, kJoinRows rows each.
-constexpr int kJoinRows = 32;
+// blockIdx.y = a CTA of the attention kernel: if it began a cut unit, the
+// unit's partial results are joined here, kJoinRows rows per block.
+constexpr int kJoinRows = 16;
 
 template <int HD>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams C, int ctas) {
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams C) {
   constexpr int kStep = 256 / (HD / 4);  // rows at a time: consecutive threads read consecutive rows
   const AttendParams& P = C.a;
-  const BatchParams& b = P.batch;
+  const int first = (int)blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Shares shares(C, ctas);
-  const int64_t border = shares.share * (blockIdx.y + 1);
-  if (border >= shares.all) return;
-  int g, slot, count;
-  int64_t begin;
-  shares.find(C, border, &g, &slot, &begin, &count);
-  const int first = (int)(begin / shares.share);
-  if (begin == border || first != (int)blockIdx.y) return;  // not cut here, or joined at an earlier border
-  const int last = (int)((begin + count - 1) / shares.share);
-  const Unit u = C.units[slot];
+  const Cut u = C.cuts[first];
+  if (u.last < 0) return;
   const int c = threadIdx.x / kStep;
-#pragma unroll 2
-  for (int row = blockIdx.x * kJoinRows + threadIdx.x % kStep; row < (int)(blockIdx.x + 1) * kJoinRows; row += kStep) {
+#pragma unroll
+  for (int i = 0; i < kJoinRows / kStep; ++i) {
+    const int row = blockIdx.x * kJoinRows + i * kStep + threadIdx.x % kStep;
     const int t = row >> 7, r = row & 127, in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
     if (in_tile >= C.tile_tokens || tok >= u.tokens) continue;
     auto part_of = [&](int cta) { return ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * 2 + t; };
-    float m = -INFINITY;
-    for (int k = first; k <= last; ++k) m = fmaxf(m, C.part_ml[part_of(k) * 128 + r].x);
+    float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int k = first; k <= last; ++k) {
+#pragma unroll 4
+    for (int k = first; k <= u.last; ++k) {
       const float2 ml = C.part_ml[part_of(k) * 128 + r];
-      if (ml.x == -INFINITY) continue;
-      const float f = exp2f(ml.x - m);
       const float4 v = C.part_o[(part_of(k) * (HD / 4) + c) * 128 + r];
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
-      l += f * ml.y;
+      if (ml.x == -INFINITY) continue;
+      const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), fk = exp2f(ml.x - mn);
+      m = mn;
+      acc.x = f * acc.x + fk * v.x;
+      acc.y = f * acc.y + fk * v.y;
+      acc.z = f * acc.z + fk * v.z;
+      acc.w = f * acc.w + fk * v.w;
+      l = f * l + fk * ml.y;
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int head = g * P.group + r - in_tile * P.group;
+    const int head = u.g * P.group + r - in_tile * P.group;
     const int64_t t_row = u.q_row + tok;
     *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) =
         make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (c == 0 && P.lse) P.lse[(int64_t)head * b.T + t_row] = (m + log2f(l)) * 0.69314718055994531f;
+    if (c == 0 && P.lse) P.lse[(int64_t)head * P.batch.T + t_row] = (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -685,6 +734,8 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   w += align256((size_t)ctas * 4 * 128 * HD * 4);
   C.part_ml = reinterpret_cast<float2*>(w);
   w += align256((size_t)ctas * 4 * 128 * 8);
+  C.cuts = reinterpret_cast<Cut*>(w);
+  w += align256((size_t)ctas * sizeof(Cut));
   C.units = reinterpret_cast<Unit*>(w);
   w += align256((size_t)C.slots * sizeof(Unit));
   C.tiles_end = reinterpret_cast<int64_t*>(w);
@@ -703,7 +754,7 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   e = launch_after(attend_chunk_kernel<HD>, dim3((unsigned)ctas), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel launch");
   if (ctas > 1) {
-    e = launch_after(chunk_join_kernel<HD>, dim3(256 / kJoinRows, (unsigned)(ctas - 1)), 256, 0, s, C, ctas);
+    e = launch_after(chunk_join_kernel<HD>, dim3(256 / kJoinRows, (unsigned)(ctas - 1)), 256, 0, s, C);
     if (e != cudaSuccess) return cuda_fail(e, "chunk_join_kernel launch");
   }
   return AA_OK;
@@ -713,7 +764,7 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
 
 size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int group) {
   const size_t slots = slots_for(total_tokens, num_seqs, 128 / group), ctas = c->num_sms;
-  return align256(ctas * 4 * 128 * c->cfg.head_dim * 4) + align256(ctas * 4 * 128 * 8) +
+  return align256(ctas * 4 * 128 * c->cfg.head_dim * 4) + align256(ctas * 4 * 128 * 8) + align256(ctas * sizeof(Cut)) +
          align256(slots * sizeof(Unit)) + align256((slots + 1) * 8);
 }
 
