@@ -15,63 +15,13 @@ leaves alive while capturing.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
-from .binding import AARopeAxes, ROPE_ADJACENT, _check, _stream_ptr, lib
+from .binding import AARopeAxes, ROPE_ADJACENT, _check, lib, native
 
 __all__ = ["RopeAxes", "RopeAxesFn", "rope_axes"]
-
-
-# The single-token calls take a few microseconds on the GPU, so their host side is kept lean: plain attribute tests, no
-# context managers or temporary objects on the common path.
-_NOTHING = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Allocate on the stream that the kernels will run on."""
-    return _NOTHING if stream is None else torch.cuda.stream(stream)
-
-
-def _check_rows(name, x, T, H, D, device):
-    """x is a bf16 tensor [T, H, D] on `device` (T, H None: any)."""
-    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.device != device:
-        raise ValueError(f"{name} must be a bfloat16 tensor on {device}")
-    shape = x.shape
-    if len(shape) != 3 or shape[2] != D or (T is not None and shape[0] != T) or (H is not None and shape[1] != H):
-        want = tuple("any" if n is None else n for n in (T, H, D))
-        raise ValueError(f"{name} must have shape {want}, got {tuple(shape)}")
-
-
-def _check_tensor(name, x, shape, dtype, device):
-    """x is a contiguous tensor of `dtype` and `shape` on `device`."""
-    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
-    if x.shape != shape or not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(x.shape)}")
-
-
-def _rows(x):
-    """(x, token stride) as the kernels read it: a token's heads contiguous, 16-byte aligned rows; copied if it is not."""
-    T, H, D = x.shape
-    a, b, c = x.stride()
-    if c == 1 and (b == D or H == 1) and x.data_ptr() % 16 == 0:
-        if T <= 1:
-            return x, H * D
-        if a >= H * D and a % 8 == 0:
-            return x, a
-    x = x.contiguous()
-    return (x if x.data_ptr() % 16 == 0 else x.clone()), H * D
-
-
-def _out(name, out, like):
-    """The caller's output tensor, checked, or a new contiguous one of the shape of `like`."""
-    if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _check_tensor(name, out, like.shape, like.dtype, like.device)
-    return out
 
 
 class RopeAxes:
@@ -121,43 +71,13 @@ class RopeAxes:
                                        (ctypes.c_double * max(half, 1))(*[float(x) for x in theta])))
         self._at = ctypes.addressof(self._c)
 
-    def _positions(self, pos, T, device):
-        if not isinstance(pos, torch.Tensor) or pos.dtype is not torch.int32 or pos.device != device:
-            raise ValueError(f"pos must be an int32 tensor on {device}")
-        shape = pos.shape
-        if shape != (self.num_axes, T) and not (self.num_axes == 1 and shape == (T,)):
-            raise ValueError(f"pos must have shape ({self.num_axes}, {T}), got {tuple(shape)}")
-        return pos.contiguous()
-
     def apply(self, pos, q, k=None, inverse=False, out_q=None, out_k=None, stream=None):
         """Rotate q [T, Hq, D] (and k [T, Hk, D]) by pos, int32 [axes, T]; inverse=True turns back. Token strides of
         slices are taken as they are; out_q = q works in place on a contiguous q."""
-        if not isinstance(q, torch.Tensor) or not q.is_cuda:
-            raise ValueError("q must be a CUDA tensor")
-        dev = q.device
-        index = dev.index
-        _check_rows("q", q, None, None, self.head_dim, dev)
-        if index != torch.cuda.current_device():
-            raise ValueError(f"q is on {dev}, which is not the current device")
-        T, hq, _ = q.shape
-        if k is not None:
-            _check_rows("k", k, T, None, self.head_dim, dev)
-        elif out_k is not None:
-            raise ValueError("out_k goes with k")
-        with _on(stream):
-            pos = self._positions(pos, T, dev)
-            yq = _out("out_q", out_q, q)
-            q, sq = _rows(q)
-            yk, kp, sk, yp, hk = None, None, 0, None, 0
-            if k is not None:
-                yk = _out("out_k", out_k, k)
-                k, sk = _rows(k)
-                kp, yp, hk = k.data_ptr(), yk.data_ptr(), k.shape[1]
-            status = lib().aa_rope_axes_apply(self._at, pos.data_ptr(), T, q.data_ptr(), sq, yq.data_ptr(), hq, kp, sk, yp, hk,
-                                              1 if inverse else 0, _stream_ptr(stream, index))
-            if status:
-                _check(status)
-        return yq if k is None else (yq, yk)
+        r = native().rope_apply(self._at, self.num_axes, self.head_dim, pos, q, k, inverse, out_q, out_k, stream)
+        if type(r) is int:
+            _check(r)
+        return r
 
 
 class RopeAxesFn(torch.autograd.Function):

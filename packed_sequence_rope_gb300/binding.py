@@ -147,20 +147,20 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-_raw_stream = None
+_native = None
 
 
-def _stream_ptr(stream, device_index):
-    """The stream's handle as an integer. For the current one torch's own raw query (0.1 us of host time against 3 us
-    for the Stream object), where this torch has it."""
-    global _raw_stream
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is None:
-        import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _raw_stream(device_index)
+def native():
+    """_calls.so: the serving operators' per-step calls (csrc/torch_calls.cpp), built with the library."""
+    global _native
+    if _native is None:
+        lib()
+        try:
+            from . import _calls
+        except ImportError as e:
+            raise RuntimeError("_calls.so is missing or does not fit this torch: run __graft_entry__.build()") from e
+        _native = _calls
+    return _native
 
 
 class Plan:

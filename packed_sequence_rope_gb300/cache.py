@@ -17,18 +17,13 @@ the binding this marshals arguments: every step runs in the library.
 from __future__ import annotations
 
 import ctypes
-import struct
 
 import numpy as np
 import torch
 
-from .axes import _check_rows, _check_tensor, _on, _out, _rows
-from .binding import AACacheConfig, _check, _stream_ptr, lib
+from .binding import AACacheConfig, _check, _stream, lib, native
 
 __all__ = ["PagedCache"]
-
-
-_BATCH = struct.Struct("@3P4i")  # aa_cache_batch
 
 
 def _host_i32(name, x):
@@ -53,16 +48,16 @@ class PagedCache:
 
     def __init__(self, num_pages, page_size, num_kv_heads, head_dim, num_layers=1, max_seqs=0, k_pages=None, v_pages=None,
                  device=None, host_only=False):
+        self._h, self._dev = None, -1
         self.cfg = AACacheConfig(int(num_layers), int(num_pages), int(page_size), int(num_kv_heads), int(head_dim),
                                  int(max_seqs), int(bool(host_only)))
         self.L, self.P, self.ps = int(num_layers), int(num_pages), int(page_size)
         self.Hkv, self.D, self.host_only = int(num_kv_heads), int(head_dim), bool(host_only)
-        self._h = None
         h = ctypes.c_void_p()
         if host_only:
             _check(lib().aa_cache_create(ctypes.addressof(self.cfg), None, None, ctypes.byref(h)))
             self.k_pages = self.v_pages = self.device = None
-            self._h = h
+            self._h, self._dev = h, -1
             return
         shape = (self.L, self.P, self.Hkv, self.ps, self.D)
         if (k_pages is None) != (v_pages is None):
@@ -76,14 +71,15 @@ class PagedCache:
         elif device is not None:
             raise ValueError("device goes without k_pages and v_pages")
         for name, x in (("k_pages", k_pages), ("v_pages", v_pages)):
-            if not isinstance(x, torch.Tensor) or not x.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            _check_tensor(name, x, shape, torch.bfloat16, k_pages.device)
+            if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16 or x.device != k_pages.device:
+                raise ValueError(f"{name} must be a bfloat16 CUDA tensor, both on one device")
+            if x.shape != shape or not x.is_contiguous():
+                raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(x.shape)}")
         self.k_pages, self.v_pages, self.device = k_pages, v_pages, k_pages.device
         with torch.cuda.device(self.device):
             _check(lib().aa_cache_create(ctypes.addressof(self.cfg), k_pages.data_ptr(), v_pages.data_ptr(),
                                          ctypes.byref(h)))
-        self._h = h
+        self._h, self._dev = h, self.device.index
 
     # ---- lifetime
     def close(self):
@@ -104,7 +100,7 @@ class PagedCache:
         self.close()
 
     def _stream(self, stream):
-        return None if self.host_only else _stream_ptr(stream, self.device.index)
+        return None if self.host_only else _stream(stream)
 
     # ---- bookkeeping (host)
     def resize(self, seqs, lens, stream=None):
@@ -159,54 +155,21 @@ class PagedCache:
     def check_device_error(self, stream=None):
         _check(lib().aa_cache_check_error(self._h, self._stream(stream)))
 
-    def _batch(self, page_table, cu_q, kv_len, T, layer):
-        """aa_cache_batch as bytes."""
-        dev = self.device
-        if dev is None:
-            raise ValueError("the cache was created with host_only = True")
-        for x, name in ((page_table, "page_table"), (cu_q, "cu_q"), (kv_len, "kv_len")):
-            if not isinstance(x, torch.Tensor) or x.dtype is not torch.int32 or x.device != dev or not x.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
-        shape = page_table.shape
-        if len(shape) != 2 or cu_q.shape != (shape[0] + 1,) or kv_len.shape != (shape[0],):
-            raise ValueError(f"page_table [B, W], cu_q [B + 1] and kv_len [B] do not fit together: {tuple(shape)}, "
-                             f"{tuple(cu_q.shape)}, {tuple(kv_len.shape)}")
-        return _BATCH.pack(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), shape[0], shape[1], T, layer)
+    def _device_handle(self):
+        """The handle's address, for the native calls."""
+        if self._dev < 0 or self._h is None:
+            raise ValueError("the cache is closed or was created with host_only = True")
+        return self._h.value
 
     def append(self, k, v, page_table, cu_q, kv_len, layer=0, rope=None, pos=None, q=None, out_q=None, stream=None):
         """Write the new tokens' k (rotated by rope at pos) and v [T, Hkv, D] to their pages; with q [T, Hq, D] the same
         launch rotates q, and the result is returned."""
-        dev, D = self.device, self.D
-        _check_rows("k", k, None, self.Hkv, D, dev)
-        T = k.shape[0]
-        _check_rows("v", v, T, self.Hkv, D, dev)
-        batch = self._batch(page_table, cu_q, kv_len, T, layer)
-        if (rope is None) != (pos is None):
-            raise ValueError("give both rope and pos or neither")
-        if q is None:
-            if out_q is not None:
-                raise ValueError("out_q goes with q")
-        else:
-            _check_rows("q", q, T, None, D, dev)
-            if rope is None:
-                raise ValueError("q is rotated: it needs rope and pos")
-        with _on(stream):
-            k, sk = _rows(k)
-            v, sv = _rows(v)
-            rp, pp = None, None
-            if rope is not None:
-                pos = rope._positions(pos, T, dev)
-                rp, pp = rope._at, pos.data_ptr()
-            yq, qp, yp, sq, hq = None, None, None, 0, 0
-            if q is not None:
-                yq = _out("out_q", out_q, q)
-                q, sq = _rows(q)
-                qp, yp, hq = q.data_ptr(), yq.data_ptr(), q.shape[1]
-            status = lib().aa_cache_append(self._h, batch, k.data_ptr(), sk, v.data_ptr(), sv, rp, pp, qp, sq, yp, hq,
-                                           _stream_ptr(stream, dev.index))
-            if status:
-                _check(status)
-        return yq
+        r = native().cache_append(self._device_handle(), self._dev, self.Hkv, self.D, k, v, page_table, cu_q, kv_len, layer,
+                                  None if rope is None else rope._at, 0 if rope is None else rope.num_axes, pos, q, out_q,
+                                  stream)
+        if type(r) is int:
+            _check(r)
+        return r
 
     def workspace_bytes(self, num_seqs, total_tokens, max_q, table_width, q_heads):
         return int(lib().aa_cache_attend_workspace_bytes(self._h, int(num_seqs), int(total_tokens), int(max_q),
@@ -221,32 +184,8 @@ class PagedCache:
                lse=None, workspace=None, return_lse=False, stream=None):
         """Attention of the new tokens' rotated q [T, Hq, D] over their sequences' pages: o [T, Hq, D], and with
         return_lse the log-sum-exp [Hq, T] fp32. key_lo: int32 [T], the first key each row sees; anchor: key 0 is seen too."""
-        dev = self.device
-        _check_rows("q", q, None, None, self.D, dev)
-        T, hq, _ = q.shape
-        batch = self._batch(page_table, cu_q, kv_len, T, layer)
-        with _on(stream):
-            kp = None
-            if key_lo is not None:
-                if not isinstance(key_lo, torch.Tensor) or key_lo.dtype is not torch.int32 or key_lo.device != dev \
-                        or key_lo.shape != (T,):
-                    raise ValueError(f"key_lo must be an int32 tensor [{T}] on {dev}")
-                key_lo = key_lo.contiguous()
-                kp = key_lo.data_ptr()
-            o = _out("out", out, q)
-            if lse is not None:
-                _check_tensor("lse", lse, (hq, T), torch.float32, dev)
-            elif return_lse:
-                lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
-            if workspace is None:
-                workspace = self.alloc_workspace(page_table.shape[0], T, max_q, page_table.shape[1], hq)
-            elif not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.device != dev \
-                    or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-            q, sq = _rows(q)
-            status = lib().aa_cache_attend(self._h, batch, q.data_ptr(), sq, hq, max_q, kp, 1 if anchor else 0,
-                                           softmax_scale or 0.0, o.data_ptr(), None if lse is None else lse.data_ptr(),
-                                           workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev.index))
-            if status:
-                _check(status)
-        return (o, lse) if return_lse else o
+        r = native().cache_attend(self._device_handle(), self._dev, self.D, q, page_table, cu_q, kv_len, max_q, layer, key_lo,
+                                  anchor, softmax_scale or 0.0, out, lse, workspace, return_lse, stream)
+        if type(r) is int:
+            _check(r)
+        return r
