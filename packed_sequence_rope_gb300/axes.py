@@ -17,11 +17,9 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 from .binding import AARopeAxes, ROPE_ADJACENT, _check, lib, native
 
-__all__ = ["RopeAxes", "RopeAxesFn", "rope_axes"]
+__all__ = ["RopeAxes", "rope_axes"]
 
 
 class RopeAxes:
@@ -74,34 +72,12 @@ class RopeAxes:
     def apply(self, pos, q, k=None, inverse=False, out_q=None, out_k=None, stream=None):
         """Rotate q [T, Hq, D] (and k [T, Hk, D]) by pos, int32 [axes, T]; inverse=True turns back. Token strides of
         slices are taken as they are; out_q = q works in place on a contiguous q."""
-        r = native().rope_apply(self._at, self.num_axes, self.head_dim, pos, q, k, inverse, out_q, out_k, stream)
+        r = native().rope_apply(self._at, pos, q, k, inverse, out_q, out_k, stream)
         if type(r) is int:
             _check(r)
         return r
 
 
-class RopeAxesFn(torch.autograd.Function):
-    """The rotation is orthogonal: its gradient is the rotation back."""
-
-    @staticmethod
-    def forward(ctx, rope, pos, inverse, q, k):
-        ctx.rope, ctx.inverse = rope, inverse
-        ctx.save_for_backward(pos)
-        out = rope.apply(pos, q, k, inverse=inverse)
-        return (out, None) if k is None else out
-
-    @staticmethod
-    def backward(ctx, gq, gk):
-        (pos,) = ctx.saved_tensors
-        need_q, need_k = ctx.needs_input_grad[3:]
-        if need_q:
-            gq, gk = RopeAxesFn.apply(ctx.rope, pos, not ctx.inverse, gq, gk if need_k else None)
-        elif need_k:
-            gq, gk = None, RopeAxesFn.apply(ctx.rope, pos, not ctx.inverse, gk, None)[0]
-        return None, None, None, gq if need_q else None, gk if need_k else None
-
-
 def rope_axes(rope, pos, q, k=None):
-    """RopeAxes.apply as a differentiable op: q, or (q, k), rotated."""
-    yq, yk = RopeAxesFn.apply(rope, pos, False, q, k)
-    return yq if k is None else (yq, yk)
+    """RopeAxes.apply as a differentiable op: q, or (q, k), rotated. The gradient is the rotation back."""
+    return native().rope_autograd(rope._at, pos, q, k)

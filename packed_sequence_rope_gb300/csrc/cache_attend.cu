@@ -23,7 +23,9 @@ extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs
   if (!c || num_seqs < 1 || total_tokens < 0 || max_q < 0 || table_width < 1 || q_heads < 1) return 0;
   const int Hkv = c->cfg.num_kv_heads;
   if (c->host_only || q_heads % Hkv || q_heads / Hkv > 64) return 0;
-  if (takes_short(max_q, q_heads / Hkv)) return 256;
+  if (total_tokens >= (1 << 30) || num_seqs > (1 << 20) || (int64_t)table_width * c->cfg.page_size >= (1ll << 30)) return 0;
+  if (takes_short(max_q, q_heads / Hkv))
+    return short_workspace_bytes(c, num_seqs, total_tokens, max_q, table_width, q_heads / Hkv);
   return chunk_workspace_bytes(c, num_seqs, total_tokens, q_heads / Hkv);
 }
 
@@ -68,6 +70,6 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   P.scale_log2 = (float)((softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!takes_short(max_q, P.group)) return launch_attend_chunk(c, P, workspace, s);
-  cudaError_t e = launch_attend_short(c, P, max_q, s);
+  cudaError_t e = launch_attend_short(c, P, max_q, workspace, s);
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
 }

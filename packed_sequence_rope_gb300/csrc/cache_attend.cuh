@@ -66,10 +66,30 @@ __device__ __forceinline__ int pool_row(const BatchParams& b, int seq, int g, in
   return (int)((((b.layer_page0 + page) * b.Hkv + g) << page_shift) + (j & ((1 << page_shift) - 1)));
 }
 
-// Launchers (arguments already checked).
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Launch a kernel whose start-up may overlap the kernel before it (it waits with
+// griddepcontrol.wait before it reads anything).
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Launchers (arguments already checked) and the workspaces they need.
 // short: at most kShortRows rows (max_q * group) of a sequence and kv head at a time.
 constexpr int kShortRows = 64;
-cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int max_q, cudaStream_t s);
+cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int max_q, void* workspace, cudaStream_t s);
+size_t short_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int max_q, int table_width, int group);
 aa_status launch_attend_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
 size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int group);
 

@@ -702,24 +702,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- launches
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 int slots_for(int tokens, int seqs, int tile_tokens) { return tokens / (2 * tile_tokens) + seqs; }
-
-template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 template <int HD>
 aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {

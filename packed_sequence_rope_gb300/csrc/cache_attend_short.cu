@@ -15,7 +15,9 @@
 //             in the critical path), online softmax in registers
 // and at the end the warps' partial results are joined in shared memory, the
 // CTAs' through distributed shared memory: one launch, no workspace, and the
-// same order of additions in every run.
+// same order of additions in every run. Where the units times a cluster's CTAs do
+// not fill the GPU (one user with a long context), each unit gets several
+// clusters; their results go to the workspace and a second kernel joins them.
 #include "cache_attend.cuh"
 
 namespace aa {
@@ -25,6 +27,16 @@ constexpr int kTileKeys = 64;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
+
+constexpr int kSplitRanks = 4, kSplitTiles = 8;
+
+// Results of the clusters of a unit: [split][row][query head], unnormalised O and
+// (maximum in log2 units, sum).
+struct ShortParts {
+  int splits;
+  float4* o;
+  float2* ml;
+};
 
 template <int HD>
 struct ShortSmem {
@@ -64,7 +76,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
 template <int HD, int RT>
 __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
     attend_short_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const __grid_constant__ AttendParams P) {
+                        const __grid_constant__ AttendParams P, const ShortParts S) {
   constexpr int kB = HD / 64, kStages = ShortSmem<HD>::kStages;
   constexpr int kKeyGroups = kWarps / RT, kWarpKeys = kTileKeys / kKeyGroups;
   constexpr uint32_t kStageBytes = 2 * kTileKeys * HD * 2;
@@ -73,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
   const BatchParams& b = P.batch;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ranks = ptx::cluster_size(), rank = ptx::cluster_rank();
+  const int64_t shares = (int64_t)ranks * S.splits, share = (int64_t)ranks * blockIdx.y + rank;  // of a unit's tiles
   const int unit = (int)(blockIdx.x / ranks);
   const int g = unit % b.Hkv, seq = unit / b.Hkv;
   const SeqSpan span = load_seq(b, seq, P.page_shift);
@@ -101,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
       lo = __reduce_min_sync(0xffffffffu, lo);
     }
     const KeyTiles<kTileKeys> keys(lo, hi, P.anchor);
-    const int begin = (int)((int64_t)keys.count * rank / ranks), end = (int)((int64_t)keys.count * (rank + 1) / ranks);
+    const int begin = (int)(keys.count * share / shares), end = (int)(keys.count * (share + 1) / shares);
 
     if (warp == kWarps) {
       // ---------------------------------------------------------- producer
@@ -327,9 +340,15 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
         acc.w += f * v.w;
         sum += f * ptx::cluster_ld(ptx::cluster_map(ptx::smem_u32(&sm.cta_l[row]), k));
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const int tok = row / P.group, h = g * P.group + row - tok * P.group;
       const int64_t t = span.q0 + i0 + tok;
+      if (S.splits > 1) {
+        const int64_t at = ((int64_t)blockIdx.y * b.T + t) * P.Hq + h;
+        S.o[at * (HD / 4) + (c >> 2)] = acc;
+        if (c == 0) S.ml[at] = make_float2(mx, sum);
+        continue;
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
       *reinterpret_cast<uint2*>(P.o + (t * P.Hq + h) * HD + c) =
           make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
       if (c == 0 && P.lse) P.lse[(int64_t)h * b.T + t] = (mx + log2f(sum)) * 0.69314718055994531f;
@@ -342,46 +361,108 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
   }
 }
 
+// One thread per four channels of a (row, query head): the clusters' results in
+// order. Rows outside the batch have none.
+template <int HD>
+__global__ void __launch_bounds__(256) short_join_kernel(const __grid_constant__ AttendParams P, const ShortParts S) {
+  const BatchParams& b = P.batch;
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, row = x / (HD / 4);
+  const int c = (int)(x % (HD / 4)), t = (int)(row / P.Hq), h = (int)(row % P.Hq);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t >= b.T || t < max(__ldg(b.cu_q), 0) || t >= __ldg(b.cu_q + b.B)) return;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t step = (int64_t)b.T * P.Hq;
+#pragma unroll 8
+  for (int i = 0; i < S.splits; ++i) {
+    const float2 ml = S.ml[row + i * step];
+    const float4 v = S.o[(row + i * step) * (HD / 4) + c];
+    if (ml.x == -INFINITY) continue;
+    const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), fk = exp2f(ml.x - mn);
+    m = mn;
+    acc.x = f * acc.x + fk * v.x;
+    acc.y = f * acc.y + fk * v.y;
+    acc.z = f * acc.z + fk * v.z;
+    acc.w = f * acc.w + fk * v.w;
+    l = f * l + fk * ml.y;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<uint2*>(P.o + row * HD + c * 4) =
+      make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (c == 0 && P.lse) P.lse[(int64_t)h * b.T + t] = (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// How a call is cut: rows per tile / 16, CTAs per cluster, clusters per unit.
+struct ShortShape {
+  int rt, ranks, splits;
+};
+
+ShortShape shape_of(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
+  const int rows = std::max(max_q, 1) * group;
+  const int64_t units = (int64_t)num_seqs * c->cfg.num_kv_heads;
+  const int64_t tiles = ((int64_t)table_width * c->cfg.page_size + kTileKeys - 1) / kTileKeys;
+  ShortShape f{rows <= 16 ? 1 : rows <= 32 ? 2 : 4, 1, 1};
+  // CTAs of a unit: enough to fill the SMs a few times over (ragged sequences
+  // then even out), as long as each has a few tiles. Measured on 256 units of
+  // up to 8K keys, 64 channels: 4 per SM 70 us, 2 per SM 72 us, 8 per SM 80 us;
+  // 512 units of up to 32K keys, 128 channels: 774, 818 and 771 us.
+  while (f.ranks < 8 && units * f.ranks < 4 * c->num_sms && tiles >= 4 * f.ranks) f.ranks *= 2;
+  // Two CTAs fit on an SM. Where clusters of 8 do not come to that many, several
+  // smaller clusters per unit do, if each CTA keeps kSplitTiles tiles: the
+  // second launch costs some 2 us.
+  const int64_t room = 2 * c->num_sms;
+  if (units * 8 < room) {
+    const int64_t splits = std::min(room / (units * kSplitRanks), tiles / (kSplitRanks * kSplitTiles));
+    if (splits * kSplitRanks > f.ranks) {
+      f.ranks = kSplitRanks;
+      f.splits = (int)splits;
+    }
+  }
+  return f;
+}
+
 template <int HD, int RT>
-cudaError_t launch(const aa_cache_s* c, const AttendParams& P, int ranks, cudaStream_t s) {
+cudaError_t launch(const aa_cache_s* c, const AttendParams& P, const ShortShape& f, const ShortParts& S, cudaStream_t s) {
   const auto kernel = attend_short_kernel<HD, RT>;
   const size_t smem = sizeof(ShortSmem<HD>);
   static std::once_flag once[kMaxDevices];
   static cudaError_t result[kMaxDevices];
   cudaError_t e = once_per_device(once, result, c->device, [&] {
-    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return r;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((int64_t)P.batch.B * P.batch.Hkv * ranks));
+  cfg.gridDim = dim3((unsigned)((int64_t)P.batch.B * P.batch.Hkv * f.ranks), (unsigned)f.splits);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)ranks;
+  attr.val.clusterDim.x = (unsigned)f.ranks;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, c->k_map64, c->v_map64, P);
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, c->k_map64, c->v_map64, P, S)) != cudaSuccess || f.splits == 1) return e;
+  const int64_t threads = (int64_t)P.batch.T * P.Hq * (HD / 4);
+  return launch_after(short_join_kernel<HD>, dim3((unsigned)((threads + 255) / 256)), 256, 0, s, P, S);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int max_q, cudaStream_t s) {
-  const int rows = std::max(max_q, 1) * P.group;
-  const int rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  // CTAs of a unit: enough to fill the SMs several times over (ragged
-  // sequences then even out), as long as each has a few tiles
-  const int64_t units = (int64_t)P.batch.B * P.batch.Hkv;
-  const int64_t tiles = (((int64_t)P.batch.W << P.page_shift) + kTileKeys - 1) / kTileKeys;
-  int ranks = 1;
-  while (ranks < 16 && units * ranks < 8 * c->num_sms && tiles >= 4 * ranks) ranks *= 2;
+size_t short_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int max_q, int table_width, int group) {
+  const ShortShape f = shape_of(c, num_seqs, max_q, table_width, group);
+  const size_t rows = (size_t)total_tokens * c->cfg.num_kv_heads * group;
+  return f.splits == 1 ? 256 : align256(f.splits * rows * c->cfg.head_dim * 4) + align256(f.splits * rows * 8);
+}
+
+cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int max_q, void* workspace, cudaStream_t s) {
+  const ShortShape f = shape_of(c, P.batch.B, max_q, P.batch.W, P.group);
+  ShortParts S{f.splits, static_cast<float4*>(workspace), nullptr};
+  S.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) +
+                                   align256((size_t)f.splits * P.batch.T * P.Hq * c->cfg.head_dim * 4));
   if (c->cfg.head_dim == 128)
-    return rt == 1 ? launch<128, 1>(c, P, ranks, s) : rt == 2 ? launch<128, 2>(c, P, ranks, s) : launch<128, 4>(c, P, ranks, s);
-  return rt == 1 ? launch<64, 1>(c, P, ranks, s) : rt == 2 ? launch<64, 2>(c, P, ranks, s) : launch<64, 4>(c, P, ranks, s);
+    return f.rt == 1 ? launch<128, 1>(c, P, f, S, s) : f.rt == 2 ? launch<128, 2>(c, P, f, S, s) : launch<128, 4>(c, P, f, S, s);
+  return f.rt == 1 ? launch<64, 1>(c, P, f, S, s) : f.rt == 2 ? launch<64, 2>(c, P, f, S, s) : launch<64, 4>(c, P, f, S, s);
 }
 
 }  // namespace aa

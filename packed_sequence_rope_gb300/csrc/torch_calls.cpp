@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -185,48 +186,115 @@ void check_count(const char* name, Py_ssize_t got, Py_ssize_t want) {
   TORCH_CHECK_TYPE(got == want, name, " takes ", want, " arguments, got ", got);
 }
 
-// rope_apply(rope, axes, head_dim, pos, q, k, inverse, out_q, out_k, stream)
-PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  check_count("rope_apply", n, 10);
-  const auto* rope = as_handle<const aa_rope_axes*>(a[0]);
-  const int64_t axes = as_int(a[1]), D = as_int(a[2]);
-  const Tensor& q = need(a[4], "q");
+// ---------------------------------------------------------------- rotation
+struct Rotated {
+  int status;
+  Tensor q, k;
+};
+
+Rotated rotate(const aa_rope_axes* rope, const Tensor& pos, const Tensor& q, const Tensor* k, bool inverse,
+               const Tensor* out_q, const Tensor* out_k, PyObject* stream) {
   TORCH_CHECK_VALUE(q.is_cuda(), "q must be a CUDA tensor");
   const at::Device dev = q.device();
-  check_rows(q, "q", -1, -1, D, dev);
+  check_rows(q, "q", -1, -1, rope->head_dim, dev);
   TORCH_CHECK_VALUE(dev.index() == c10::cuda::current_device(), "q is on ", dev, ", which is not the current device");
   const int64_t T = q.size(0);
-  const Tensor *k = given(a[5], "k"), *out_q = given(a[7], "out_q"), *out_k = given(a[8], "out_k");
   TORCH_CHECK_VALUE(k || !out_k, "out_k goes with k");
-  if (k) check_rows(*k, "k", T, -1, D, dev);
+  if (k) check_rows(*k, "k", T, -1, rope->head_dim, dev);
   TORCH_CHECK_VALUE(T <= INT32_MAX && q.size(1) <= INT32_MAX && (!k || k->size(1) <= INT32_MAX), "q or k is too large");
-  const bool inverse = as_bool(a[6]);
-  const OnStream on(a[9], dev);
-  Tensor keep, yk;
-  const int32_t* pos = positions(need(a[3], "pos"), axes, T, dev, &keep);
-  Tensor yq = out_or_new(out_q, "out_q", q.sizes(), at::kBFloat16, dev);
+  const OnStream on(stream, dev);
+  Tensor keep;
+  Rotated r;
+  const int32_t* p = positions(pos, rope->num_axes, T, dev, &keep);
+  r.q = out_or_new(out_q, "out_q", q.sizes(), at::kBFloat16, dev);
   const Rows rq(q);
   std::optional<Rows> rk;
   if (k) {
-    yk = out_or_new(out_k, "out_k", k->sizes(), at::kBFloat16, dev);
+    r.k = out_or_new(out_k, "out_k", k->sizes(), at::kBFloat16, dev);
     rk.emplace(*k);
   }
-  const int status = without_gil([&] {
-    return aa_rope_axes_apply(rope, pos, (int32_t)T, rq.ptr, rq.stride, yq.mutable_data_ptr(), (int32_t)q.size(1),
-                              k ? rk->ptr : nullptr, k ? rk->stride : 0, k ? yk.mutable_data_ptr() : nullptr,
-                              k ? (int32_t)k->size(1) : 0, inverse, on.s);
-  });
-  if (status) return PyLong_FromLong(status);
-  if (!k) return THPVariable_Wrap(std::move(yq));
-  PyObject *pq = THPVariable_Wrap(std::move(yq)), *pk = THPVariable_Wrap(std::move(yk));
+  r.status = aa_rope_axes_apply(rope, p, (int32_t)T, rq.ptr, rq.stride, r.q.mutable_data_ptr(), (int32_t)q.size(1),
+                                k ? rk->ptr : nullptr, k ? rk->stride : 0, k ? r.k.mutable_data_ptr() : nullptr,
+                                k ? (int32_t)k->size(1) : 0, inverse, on.s);
+  return r;
+}
+
+PyObject* wrap(Tensor q, Tensor k) {
+  PyObject* pq = THPVariable_Wrap(std::move(q));
+  if (!k.defined()) return pq;
+  PyObject* pk = THPVariable_Wrap(std::move(k));
   PyObject* r = PyTuple_Pack(2, pq, pk);
   Py_XDECREF(pq);
   Py_XDECREF(pk);
   return r;
+}
+
+// rope_apply(rope, pos, q, k, inverse, out_q, out_k, stream)
+PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count("rope_apply", n, 8);
+  Rotated r = rotate(as_handle<const aa_rope_axes*>(a[0]), need(a[1], "pos"), need(a[2], "q"), given(a[3], "k"), as_bool(a[4]),
+                     given(a[5], "out_q"), given(a[6], "out_k"), a[7]);
+  if (r.status) return PyLong_FromLong(r.status);
+  return wrap(std::move(r.q), std::move(r.k));
   END_HANDLE_TH_ERRORS
 }
 
+// The rotation is orthogonal: its gradient is the rotation back, and so on.
+struct RopeHold : torch::CustomClassHolder {
+  aa_rope_axes rope;
+  explicit RopeHold(const aa_rope_axes& r) : rope(r) {}
+};
+using RopePtr = c10::intrusive_ptr<RopeHold>;
+
+struct RopeFn : torch::autograd::Function<RopeFn> {
+  using List = torch::autograd::variable_list;
+  static List turn(const RopePtr& rope, bool inverse, const Tensor& pos, const Tensor& q, const std::optional<Tensor>& k) {
+    Rotated r = rotate(&rope->rope, pos, q, k ? &*k : nullptr, inverse, nullptr, nullptr, Py_None);
+    TORCH_CHECK(r.status == 0, aa_status_string((aa_status)r.status), ": ", aa_last_error());
+    return r.k.defined() ? List{r.q, r.k} : List{r.q};
+  }
+  static List forward(torch::autograd::AutogradContext* ctx, RopePtr rope, bool inverse, Tensor pos, Tensor q,
+                      std::optional<Tensor> k) {
+    ctx->save_for_backward({pos});
+    ctx->saved_data["rope"] = c10::IValue::make_capsule(rope);
+    ctx->saved_data["inverse"] = inverse;
+    return turn(rope, inverse, pos, q, k);
+  }
+  static List backward(torch::autograd::AutogradContext* ctx, List g) {
+    const Tensor pos = ctx->get_saved_variables()[0];
+    const RopePtr rope = c10::static_intrusive_pointer_cast<RopeHold>(ctx->saved_data["rope"].toCapsule());
+    const bool inverse = !ctx->saved_data["inverse"].toBool();
+    // edges: pos, q, k
+    const bool need_q = ctx->needs_input_grad(1), need_k = g.size() > 1 && ctx->needs_input_grad(2);
+    auto both = [&](const Tensor& q, const std::optional<Tensor>& k) {
+      return at::GradMode::is_enabled() ? apply(rope, inverse, pos, q, k) : turn(rope, inverse, pos, q, k);
+    };
+    Tensor gq, gk;
+    if (need_q) {
+      List r = both(g[0], need_k ? std::optional<Tensor>(g[1]) : std::nullopt);
+      gq = r[0];
+      if (need_k) gk = r[1];
+    } else if (need_k) {
+      gk = both(g[1], std::nullopt)[0];
+    }
+    return {Tensor(), Tensor(), Tensor(), gq, gk};
+  }
+};
+
+// rope_autograd(rope, pos, q, k)
+PyObject* rope_autograd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count("rope_autograd", n, 4);
+  const Tensor& q = need(a[2], "q");
+  const Tensor* k = given(a[3], "k");
+  const auto rope = c10::make_intrusive<RopeHold>(*as_handle<const aa_rope_axes*>(a[0]));
+  RopeFn::List r = RopeFn::apply(rope, false, need(a[1], "pos"), q, k ? std::optional<Tensor>(*k) : std::nullopt);
+  return wrap(r[0], r.size() > 1 ? r[1] : Tensor());
+  END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------- cache
 // cache_append(cache, device, Hkv, head_dim, k, v, table, cu_q, kv_len, layer, rope, axes, pos, q, out_q, stream)
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -311,17 +379,13 @@ PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            (size_t)work.numel(), on.s);
   });
   if (status) return PyLong_FromLong(status);
-  if (!return_lse) return THPVariable_Wrap(std::move(o));
-  PyObject *po = THPVariable_Wrap(std::move(o)), *pl = THPVariable_Wrap(std::move(lse));
-  PyObject* r = PyTuple_Pack(2, po, pl);
-  Py_XDECREF(po);
-  Py_XDECREF(pl);
-  return r;
+  return wrap(std::move(o), return_lse ? std::move(lse) : Tensor());
   END_HANDLE_TH_ERRORS
 }
 
 PyMethodDef methods[] = {
     {"rope_apply", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_apply)), METH_FASTCALL, nullptr},
+    {"rope_autograd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_autograd)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"cache_attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_attend)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
