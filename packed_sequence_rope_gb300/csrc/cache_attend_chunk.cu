@@ -16,7 +16,8 @@
 //                         workspace
 //   chunk_join_kernel     joins the partial results of each cut unit, in order
 // The second and third are launched as programmatic dependents, so that their
-// start-up overlaps the kernel before them.
+// start-up overlaps the kernel before them. Where the page tables hold few keys
+// a unit is short, and the second kernel alone takes whole units.
 //
 // Roles in attend_chunk_kernel (640 threads):
 //   warp 0      finds the CTA's next piece of work and copies its query tiles and
@@ -45,6 +46,11 @@ constexpr int kReaders = 3 + kSoftmaxWarps;  // of a published piece: warps 1 to
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
+// Up to so many keys per page table no unit is cut. Measured, 32 / 8 heads of 128:
+// 8 sequences of 32 new tokens over 700 keys 18.5 us whole and 21.2 us cut, 42 of
+// 128 over 500 71 and 88 us; over 1000 keys 22.5 and 23.1 us, 105 and 119 us, but
+// 8 of 128 41 and 39 us: beyond, long units end unevenly.
+constexpr int kWholeKeys = 768;
 
 // A unit as chunk_plan_kernel describes it: tokens [i0, i0 + tokens) of a
 // sequence, their positions [p0, p0 + tokens), the first key any of them sees.
@@ -62,6 +68,7 @@ struct ChunkParams {
   AttendParams a;
   int tile_tokens;     // tokens per row tile: 128 / group
   int slots;           // room for the units of one kv head
+  int whole_units;     // short contexts: CTAs take whole units, there is no plan and nothing to join
   int64_t* tiles_end;  // [slots + 1] running sum of the units' key tiles; [0] = 0
   Unit* units;         // [slots]
   float4* part_o;      // [CTA][2][row tile][D / 4][128]: unnormalised O of a cut unit
@@ -70,32 +77,40 @@ struct ChunkParams {
 };
 
 // ---------------------------------------------------------------- the plan
-// Sequence b's units start at slot cu_q[b] / (2 tile_tokens) + b, which leaves
-// room for a rounded-up count and needs no scan over the sequences before it.
-__global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant__ ChunkParams C) {
+// The unit of a slot and its number of key tiles; no tokens and 0 if the slot is
+// empty (a whole warp asks). Sequence b's units start at slot
+// cu_q[b] / (2 tile_tokens) + b, which leaves room for a rounded-up count and
+// needs no scan over the sequences before it.
+__device__ __forceinline__ Unit load_unit(const ChunkParams& C, int slot, int* count) {
   const AttendParams& P = C.a;
   const BatchParams& b = P.batch;
+  const int lane = threadIdx.x & 31, unit_tokens = 2 * C.tile_tokens;
+  const int seq = warp_last(b.B, [&](int i) { return __ldg(b.cu_q + i) / unit_tokens + i <= slot; });
+  const SeqSpan s = load_seq(b, seq, P.page_shift);
+  const int64_t i0 = (int64_t)(slot - __ldg(b.cu_q + seq) / unit_tokens - seq) * unit_tokens;
+  Unit u{seq, 0, 0, 0, 0};
+  *count = 0;
+  if (i0 >= 0 && i0 < s.n) {
+    u.q_row = s.q0 + (int)i0;
+    u.tokens = min(unit_tokens, s.n - (int)i0);
+    u.p0 = s.kv - s.n + (int)i0;
+    if (P.key_lo) {
+      int lo = INT_MAX;
+      for (int i = lane; i < u.tokens; i += 32) lo = min(lo, max(__ldg(P.key_lo + u.q_row + i), 0));
+      u.lo = __reduce_min_sync(0xffffffffu, lo);
+    }
+    // rows that see nothing are written too: at least one tile
+    *count = max(KeyTiles<kKeys>(u.lo, u.p0 + u.tokens - 1, P.anchor).count, 1);
+  }
+  return u;
+}
+
+__global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant__ ChunkParams C) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int unit_tokens = 2 * C.tile_tokens;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int slot = warp; slot < C.slots; slot += 32) {
-    const int seq = warp_last(b.B, [&](int i) { return __ldg(b.cu_q + i) / unit_tokens + i <= slot; });
-    const SeqSpan s = load_seq(b, seq, P.page_shift);
-    const int64_t i0 = (int64_t)(slot - __ldg(b.cu_q + seq) / unit_tokens - seq) * unit_tokens;
-    Unit u{seq, 0, 0, 0, 0};
-    int count = 0;
-    if (i0 >= 0 && i0 < s.n) {
-      u.q_row = s.q0 + (int)i0;
-      u.tokens = min(unit_tokens, s.n - (int)i0);
-      u.p0 = s.kv - s.n + (int)i0;
-      if (P.key_lo) {
-        int lo = INT_MAX;
-        for (int i = lane; i < u.tokens; i += 32) lo = min(lo, max(__ldg(P.key_lo + u.q_row + i), 0));
-        u.lo = __reduce_min_sync(0xffffffffu, lo);
-      }
-      // rows that see nothing are written too: at least one tile
-      count = max(KeyTiles<kKeys>(u.lo, u.p0 + u.tokens - 1, P.anchor).count, 1);
-    }
+    int count;
+    const Unit u = load_unit(C, slot, &count);
     if (lane == 0) {
       C.units[slot] = u;
       C.tiles_end[slot + 1] = count;
@@ -134,6 +149,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
 // to: tile numbers run over (kv head, slot, tile of the unit).
 struct Shares {
   int64_t all, share, per_head;
+  Shares() = default;
   __device__ __forceinline__ Shares(const ChunkParams& C, int ctas) {
     per_head = C.tiles_end[C.slots];
     all = per_head * C.a.batch.Hkv;
@@ -268,9 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const Shares shares(C, gridDim.x);
-    int64_t at = shares.share * blockIdx.x;
-    const int64_t end = min(at + shares.share, shares.all);
+    Shares shares{};
+    int64_t at = blockIdx.x, end = (int64_t)C.slots * b.Hkv;  // whole units: numbers over (kv head, slot)
+    if (!C.whole_units) {
+      shares = Shares(C, gridDim.x);
+      at = shares.share * blockIdx.x;
+      end = min(at + shares.share, shares.all);
+    }
     Cut cut{-1, 0, 0, 0};
     int nq = 0, ks = 0, nk = 0;  // row tiles of Q, key tiles whose V, whose K has been asked for
     bool ok = true;
@@ -282,8 +302,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (li >= 2) ok = warp_wait(&sm.piece_empty[li & 1], ((li >> 1) - 1) & 1, b.err, abort_flag, 452);
       if (!ok) break;
       Piece w{};
-      if (at < end) {
-        int slot, count;
+      int count = 0;
+      if (C.whole_units) {
+        for (; at < end && count == 0; at += gridDim.x) {
+          w.g = (int)(at / C.slots);
+          const Unit u = load_unit(C, (int)(at % C.slots), &count);
+          w.seq = u.seq;
+          w.q_row = u.q_row;
+          w.tokens = u.tokens;
+          w.p0 = u.p0;
+          w.lo = u.lo;
+        }
+        w.valid = count > 0;
+        w.take = count;
+        w.whole = 1;
+      } else if (at < end) {
+        int slot;
         int64_t begin;
         shares.find(C, at, &w.g, &slot, &begin, &count);
         const Unit u = C.units[slot];
@@ -351,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int i = w.first + 1; i < w.first + w.take && ok; ++i) load_keys(i);
     }
-    if (lane == 0) C.cuts[blockIdx.x] = cut;
+    if (lane == 0 && !C.whole_units) C.cuts[blockIdx.x] = cut;
     // every issued copy lands before the CTA exits
     for (int u = max(nq - kQ, 0); u < nq; ++u)
       ptx::mbar_wait(&sm.q_full[u % kQ], (u / kQ) & 1, kDrainNs, b.err, 459);
@@ -711,6 +745,7 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   C.a = P;
   C.tile_tokens = 128 / P.group;
   C.slots = slots_for(b.T, b.B, C.tile_tokens);
+  C.whole_units = ((int64_t)b.W << P.page_shift) <= kWholeKeys;
   const int ctas = c->num_sms;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   C.part_o = reinterpret_cast<float4*>(w);
@@ -732,6 +767,11 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
     return cudaFuncSetAttribute(attend_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel smem attribute");
+  if (C.whole_units) {
+    const unsigned grid = (unsigned)std::min<int64_t>((int64_t)C.slots * b.Hkv, ctas);
+    e = launch_after(attend_chunk_kernel<HD>, dim3(grid), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
+    return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_chunk_kernel launch");
+  }
   chunk_plan_kernel<<<1, 1024, 0, s>>>(C);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "chunk_plan_kernel launch");
   e = launch_after(attend_chunk_kernel<HD>, dim3((unsigned)ctas), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
