@@ -39,6 +39,11 @@ __device__ __forceinline__ SeqSpan load_seq(const BatchParams& b, int seq, int p
   return s;
 }
 
+// The first key that row t of the batch sees (positions stay below 2^30).
+__device__ __forceinline__ int first_key(const AttendParams& P, int t) {
+  return P.key_lo ? min(max(__ldg(P.key_lo + t), 0), 1 << 30) : 0;
+}
+
 // The key tiles (kKeys wide) that rows with first keys >= lo and positions <=
 // hi visit: [lo, hi], and before them tile 0 if only the anchor lies there.
 template <int kKeys>

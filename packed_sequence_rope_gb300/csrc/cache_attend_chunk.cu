@@ -96,7 +96,7 @@ __device__ __forceinline__ Unit load_unit(const ChunkParams& C, int slot, int* c
     u.p0 = s.kv - s.n + (int)i0;
     if (P.key_lo) {
       int lo = INT_MAX;
-      for (int i = lane; i < u.tokens; i += 32) lo = min(lo, max(__ldg(P.key_lo + u.q_row + i), 0));
+      for (int i = lane; i < u.tokens; i += 32) lo = min(lo, first_key(P, u.q_row + i));
       u.lo = __reduce_min_sync(0xffffffffu, lo);
     }
     // rows that see nothing are written too: at least one tile
@@ -227,6 +227,13 @@ __device__ __forceinline__ bool read_piece(Smem& sm, int li, int32_t* err, volat
   __syncwarp();
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&sm.piece_empty[li & 1]);
   return __all_sync(0xffffffffu, out->valid != 0);
+}
+
+// Bit e: key j + e lies in [lo, hi].
+__device__ __forceinline__ uint32_t visible_bits(int j, int lo, int hi) {
+  const int last = hi - j, first = lo - j;
+  const uint32_t upto = last < 0 ? 0u : last >= 31 ? ~0u : (2u << last) - 1u;
+  return first <= 0 ? upto : first > 31 ? 0u : upto & (~0u << first);
 }
 
 // Barrier phases: pieces count the piece ring; the K and V rings count the
@@ -525,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_valid = in_tile < C.tile_tokens && t * C.tile_tokens + in_tile < w.tokens;
       int lo = 1, hi = 0;  // this row's visible keys
       if (row_valid) {
-        lo = P.key_lo ? max(__ldg(P.key_lo + w.q_row + t * C.tile_tokens + in_tile), 0) : 0;
+        lo = first_key(P, w.q_row + t * C.tile_tokens + in_tile);
         hi = w.p0 + t * C.tile_tokens + in_tile;
       }
       const bool anchored = P.anchor && row_valid && hi >= 0 && half == 0;
@@ -579,14 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool full1 = __all_sync(0xffffffffu, lo <= j0 + 32 && j0 + 63 <= hi);
         ptx::tmem_wait_ld();
         if (!full0) {
-          const float s0 = sv[0];
+          const uint32_t bits = visible_bits(j0, lo, hi) | (j0 == 0 && anchored ? 1u : 0u);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[e] = (j0 + e >= lo && j0 + e <= hi) ? sv[e] : -INFINITY;
-          if (j0 == 0 && anchored) sv[0] = s0;
+          for (int e = 0; e < 32; ++e) sv[e] = (bits >> e) & 1u ? sv[e] : -INFINITY;
         }
         if (!full1) {
+          const uint32_t bits = visible_bits(j0 + 32, lo, hi);
 #pragma unroll
-          for (int e = 32; e < 64; ++e) sv[e] = (j0 + e >= lo && j0 + e <= hi) ? sv[e] : -INFINITY;
+          for (int e = 0; e < 32; ++e) sv[32 + e] = (bits >> e) & 1u ? sv[32 + e] : -INFINITY;
         }
         float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
