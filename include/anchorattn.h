@@ -528,8 +528,10 @@ aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const v
  * (the mask of [ARCH §3.4 Anchor]: key_lo is the first token of the query's
  * document; or p - W + 1 for a sliding window):
  *   O_i = sum_j softmax_j(scale * q_i . k_j) v_j,  LSE_i = ln sum_j exp(...).
- * A row that sees no key gives O = 0 and LSE = -inf. Keys that no row of the
- * call sees do not reach the result, whatever their values (NaN, infinities).
+ * A row that sees no key gives O = 0 and LSE = -inf. Keys that no new token of
+ * their sequence sees do not reach the result, whatever they hold (NaN,
+ * infinities); what a row sees makes it NaN as the formula does, and a value that
+ * is not finite may reach the other rows of its sequence in the call too.
  *  - q [T, q_heads, D] bf16, ROTATED (q_stride elements from token to token);
  *    q_heads % Hkv == 0, at most 64 query heads per kv head.
  *  - max_q: the most new tokens of a sequence. It chooses the kernel; a
@@ -538,14 +540,16 @@ aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const v
  *  - softmax_scale <= 0 selects 1/sqrt(D).
  *  - o [T, q_heads, D] bf16; lse [q_heads, T] fp32 or NULL.
  *  - workspace: aa_cache_attend_workspace_bytes() bytes, 256-byte aligned,
- *    contents ignored; calls that may overlap need one each. */
+ *    contents ignored; calls that may overlap need one each.
+ *  - num_seqs * Hkv < 2^27; q_heads * total_tokens < 2^31. */
 aa_status aa_cache_attend(aa_cache_t cache, const aa_cache_batch* batch, const void* q, int64_t q_stride, int32_t q_heads,
                           int32_t max_q, const int32_t* key_lo, int32_t anchor, float softmax_scale, void* o, float* lse,
                           void* workspace, size_t workspace_bytes, aa_stream_t stream);
 
 /* Bytes of device scratch aa_cache_attend needs for a batch of these sizes
- * (partial results of keys split among CTAs; it grows with no argument but
- * total_tokens and q_heads beyond a few hundred rows). 0 for invalid ones. */
+ * (partial results of keys that are split among CTAs): some 20 to 80 MB, nearly
+ * independent of the batch, or 256 bytes where nothing is split. 0 for invalid
+ * sizes. */
 size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
                                        int32_t table_width, int32_t q_heads);
 

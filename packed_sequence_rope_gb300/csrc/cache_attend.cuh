@@ -44,6 +44,14 @@ __device__ __forceinline__ int first_key(const AttendParams& P, int t) {
   return P.key_lo ? min(max(__ldg(P.key_lo + t), 0), 1 << 30) : 0;
 }
 
+// Four channels of a row divided by its sum, in bf16; 0 for a row that saw
+// nothing (a NaN among its logits makes the sum NaN, and the row).
+__device__ __forceinline__ uint2 normalised(const float4& o, float sum) {
+  if (sum == 0.f) return make_uint2(0u, 0u);
+  const float inv = 1.f / sum;
+  return make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+}
+
 // The key tiles (kKeys wide) that rows with first keys >= lo and positions <=
 // hi visit: [lo, hi], and before them tile 0 if only the anchor lies there.
 template <int kKeys>

@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.whole) {
         const int head = w.g * P.group + r - in_tile * P.group;
         const int64_t row = w.q_row + t * C.tile_tokens + in_tile;
-        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        const float inv_l = 1.f / l;
         if (row_valid && P.lse && half == 0) P.lse[(int64_t)head * b.T + row] = (m + log2f(l)) * 0.69314718055994531f;
         // four lanes store 64 bytes of one row together: they swap their
         // 16-byte quarters of 32 channels so that lane q holds quarter q of
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t ow[4][4];  // [quarter][word]
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            ow[e >> 2][e & 3] = l > 0.f ? ptx::pack_bf16x2(ov[2 * e] * inv_l, ov[2 * e + 1] * inv_l) : 0u;
+            ow[e >> 2][e & 3] = l != 0.f ? ptx::pack_bf16x2(ov[2 * e] * inv_l, ov[2 * e + 1] * inv_l) : 0u;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
 #pragma unroll
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     for (int k = first; k <= u.last; ++k) {
       const float2 ml = C.part_ml[part_of(k) * 128 + r];
       const float4 v = C.part_o[(part_of(k) * (HD / 4) + c) * 128 + r];
-      if (ml.x == -INFINITY) continue;
+      if (ml.y == 0.f) continue;
       const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), fk = exp2f(ml.x - mn);
       m = mn;
       acc.x = f * acc.x + fk * v.x;
@@ -733,11 +733,9 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
       acc.w = f * acc.w + fk * v.w;
       l = f * l + fk * ml.y;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
     const int head = u.g * P.group + r - in_tile * P.group;
     const int64_t t_row = u.q_row + tok;
-    *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) =
-        make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) = normalised(acc, l);
     if (c == 0 && P.lse) P.lse[(int64_t)head * P.batch.T + t_row] = (m + log2f(l)) * 0.69314718055994531f;
   }
 }

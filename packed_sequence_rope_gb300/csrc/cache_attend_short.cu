@@ -81,6 +81,10 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
   constexpr int kKeyGroups = kWarps / RT, kWarpKeys = kTileKeys / kKeyGroups;
   constexpr uint32_t kStageBytes = 2 * kTileKeys * HD * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (ptx::smem_u32(smem_raw) & 1023u) {  // swizzled tiles need a 1 KB aligned base
+    if (threadIdx.x == 0) atomicCAS(P.batch.err, 0, 498);
+    return;
+  }
   ShortSmem<HD>& sm = *reinterpret_cast<ShortSmem<HD>*>(smem_raw);
   const BatchParams& b = P.batch;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -348,9 +352,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
         if (c == 0) S.ml[at] = make_float2(mx, sum);
         continue;
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      *reinterpret_cast<uint2*>(P.o + (t * P.Hq + h) * HD + c) =
-          make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(P.o + (t * P.Hq + h) * HD + c) = normalised(acc, sum);
       if (c == 0 && P.lse) P.lse[(int64_t)h * b.T + t] = (mx + log2f(sum)) * 0.69314718055994531f;
     }
     // nobody leaves (or writes its partial results again) while another reads
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(256) short_join_kernel(const __grid_constant__
   for (int i = 0; i < S.splits; ++i) {
     const float2 ml = S.ml[row + i * step];
     const float4 v = S.o[(row + i * step) * (HD / 4) + c];
-    if (ml.x == -INFINITY) continue;
+    if (ml.y == 0.f) continue;
     const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), fk = exp2f(ml.x - mn);
     m = mn;
     acc.x = f * acc.x + fk * v.x;
@@ -386,9 +388,7 @@ __global__ void __launch_bounds__(256) short_join_kernel(const __grid_constant__
     acc.w = f * acc.w + fk * v.w;
     l = f * l + fk * ml.y;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(P.o + row * HD + c * 4) =
-      make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2*>(P.o + row * HD + c * 4) = normalised(acc, l);
   if (c == 0 && P.lse) P.lse[(int64_t)h * b.T + t] = (m + log2f(l)) * 0.69314718055994531f;
 }
 

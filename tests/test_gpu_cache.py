@@ -183,6 +183,42 @@ def test_values_far_apart(aa):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("new,kv", [(1, 500), (1, 20000), (4, 300), (100, 300), (100, 3000)])
+def test_nan_in_a_visible_key_shows(aa, new, kv):
+    """A NaN in a key makes every row that sees it NaN (never 0), and no row of another sequence."""
+    d = ref.make_batch(3, [kv, kv], [new, new], 4, 2, 64, 64, device="cuda")
+    at = kv - new // 2 - 1  # seen by the later half of the new tokens
+    d["k_pages"][0, int(d["table"][1, at // 64]), 1, at % 64, 3] = math.nan
+    with _cache(aa, d, 64, 2, 64) as c:
+        o, lse = c.attend(d["q"], d["table"], d["cu"], d["kv"], new, return_lse=True)
+        c.check_device_error()
+    sees = torch.zeros(2 * new, 4, dtype=torch.bool)
+    sees[new + at - (kv - new):, 2:] = True
+    assert torch.isnan(lse.T.cpu()).equal(sees)
+    assert torch.isnan(o.cpu()).all(-1).equal(sees) and torch.isnan(o.cpu()).any(-1).equal(sees)
+
+
+@pytest.mark.parametrize("page_tokens", [16, 128])
+def test_mixed_batch_of_many_sequences(aa, page_tokens):
+    """Hundreds of sequences, most idle or with one token, some with chunks: the kernel for chunks, whole units and cut ones."""
+    g = torch.Generator().manual_seed(8)
+    pick = torch.randint(0, 10, (300,), generator=g).tolist()
+    new = [0 if x < 4 else 1 if x < 9 else 50 + i % 97 for i, x in enumerate(pick)]
+    kv = [n + int(x) for n, x in zip(new, torch.randint(0, 90, (300,), generator=g))]
+    d = ref.make_batch(8, kv, new, 4, 1, 64, page_tokens, device="cuda")
+    _attend(aa, d, page_tokens, 1, 64)
+    kv[7] += 2500  # one long context: wide tables, units are cut
+    d = ref.make_batch(8, kv, new, 4, 1, 64, page_tokens, device="cuda")
+    _attend(aa, d, page_tokens, 1, 64)
+
+
+@pytest.mark.parametrize("group", [1, 4, 16])
+def test_chunks_with_wide_tables(aa, group):
+    """Short and long contexts in one batch under tables of 4096 keys: pieces of units on many SMs."""
+    d = ref.make_batch(group, [3900, 64, 5, 1000], [80, 64, 5, 300], 2 * group, 2, 128, 32, device="cuda", extra_width=6)
+    _attend(aa, d, 32, 2, 128)
+
+
 def test_strides_layers_and_rows_behind_the_batch(aa):
     for new in (1, 90):
         T, pad, Hq, Hkv, D, ps = 2 * new, 5, 4, 2, 128, 64
