@@ -407,10 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph_p[2] = {0, 0};
     int ks = 0, nq = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) { return warp_wait(bar, parity, b.err, abort_flag, site); };
-    // S of row tile t, its Q in buffer q, and the keys of stage s
-    auto issue_s = [&](int t, int q, int s) {
-      const uint64_t qd = ptx::smem_desc_sw128(ptx::smem_u32(sm.q[q][0]), 16, 1024);
-      const uint64_t kd = ptx::smem_desc_sw128(ptx::smem_u32(sm.k[s][0]), 16, 1024);
+    // Descriptors of the first buffers; the others follow at kTileBytes. They are
+    // made before the waits, so that nothing stands between a signal and its
+    // products.
+    const uint64_t q0 = ptx::smem_desc_sw128(ptx::smem_u32(sm.q[0][0]), 16, 1024);
+    const uint64_t k0 = ptx::smem_desc_sw128(ptx::smem_u32(sm.k[0][0]), 16, 1024);
+    const uint64_t v0 = ptx::smem_desc_sw128(ptx::smem_u32(sm.v[0][0]), 16384, 1024);
+    auto issue_s = [&](int t, uint64_t qd, uint64_t kd) {
       if constexpr (HD == 128)
         ptx::mma8_ss_kk_warp(tmem + 128 * t, qd, kd, idesc_s, 0);
       else
@@ -425,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int take = __reduce_max_sync(0xffffffffu, w.take);
       const int tiles = __all_sync(0xffffffffu, w.tokens > C.tile_tokens) ? 2 : 1;
       const int q[2] = {nq % kQ, (nq + 1) % kQ};
+      const uint64_t qd[2] = {q0 + q[0] * (kTileBytes >> 4), q0 + q[1] * (kTileBytes >> 4)};
       // the first S products, as the piece's K and Q land
       if (!(ok = wait(&sm.k_full[ks % kStages], (ks / kStages) & 1, 463))) break;
 #pragma unroll
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t >= tiles) break;
         if (!(ok = wait(&sm.q_full[q[t]], ((nq + t) / kQ) & 1, 462))) break;
         ptx::tc_fence_after();
-        issue_s(t, q[t], ks % kStages);
+        issue_s(t, qd[t], k0 + (ks % kStages) * (kTileBytes >> 4));
         if (take == 1) ptx::mma_commit_warp(&sm.q_free[q[t]]);
       }
       if (!ok) break;
@@ -442,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // only the softmax's signal stands before P V and the next S of a tile
         const int s = ks % kStages, s1 = (ks + 1) % kStages;
         const bool more = i + 1 < take;
+        const uint64_t vd = v0 + s * (kTileBytes >> 4), kd = k0 + s1 * (kTileBytes >> 4);
         if (!(ok = wait(&sm.v_clean[s], (ks / kStages) & 1, 464))) break;
         if (more && !(ok = wait(&sm.k_full[s1], ((ks + 1) / kStages) & 1, 463))) break;
 #pragma unroll
@@ -450,10 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait(&sm.p_full[t], ph_p[t], 461))) break;
           ph_p[t] ^= 1;
           ptx::tc_fence_after();
-          ptx::mma8_ts_seq_warp(tmem + 256 + HD * t, tmem + 128 * t,
-                                ptx::smem_desc_sw128(ptx::smem_u32(sm.v[s][0]), 16384, 1024), idesc_pv, i == 0 ? 0u : 1u);
+          ptx::mma8_ts_seq_warp(tmem + 256 + HD * t, tmem + 128 * t, vd, idesc_pv, i == 0 ? 0u : 1u);
           if (more)
-            issue_s(t, q[t], s1);
+            issue_s(t, qd[t], kd);
           else
             ptx::mma_commit_warp(&sm.o_full[t]);
           if (i + 2 == take) ptx::mma_commit_warp(&sm.q_free[q[t]]);
