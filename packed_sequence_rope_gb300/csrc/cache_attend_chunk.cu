@@ -704,43 +704,82 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- joining cut units
 // blockIdx.y = a CTA of the attention kernel: if it began a cut unit, the
-// unit's partial results are joined here, kJoinRows rows per block.
-constexpr int kJoinRows = 16;
+// unit's partial results are joined here, kJoinRows rows per block. A thread
+// keeps the loads of kAtOnce parts of its rows in flight: with long contexts and
+// few new tokens a unit has some twenty parts, and there are few rows to hide
+// their latency behind.
+constexpr int kJoinRows = 16, kAtOnce = 4;
 
 template <int HD>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams C) {
   constexpr int kStep = 256 / (HD / 4);  // rows at a time: consecutive threads read consecutive rows
+  constexpr int kMine = kJoinRows / kStep;
   const AttendParams& P = C.a;
   const int first = (int)blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut u = C.cuts[first];
   if (u.last < 0) return;
-  const int c = threadIdx.x / kStep;
+  const int c = threadIdx.x / kStep, row0 = blockIdx.x * kJoinRows + threadIdx.x % kStep;
+  const int t = (int)(blockIdx.x * kJoinRows) >> 7;  // row tile
+  auto token = [&](int i) {  // of the i-th of this thread's rows; < 0: none
+    const int in_tile = ((row0 + i * kStep) & 127) / P.group, tok = t * C.tile_tokens + in_tile;
+    return in_tile < C.tile_tokens && tok < u.tokens ? tok : -1;
+  };
+  float m[kMine], l[kMine];
+  float4 acc[kMine];
 #pragma unroll
-  for (int i = 0; i < kJoinRows / kStep; ++i) {
-    const int row = blockIdx.x * kJoinRows + i * kStep + threadIdx.x % kStep;
-    const int t = row >> 7, r = row & 127, in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
-    if (in_tile >= C.tile_tokens || tok >= u.tokens) continue;
-    auto part_of = [&](int cta) { return ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * 2 + t; };
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = first; k <= u.last; ++k) {
-      const float2 ml = C.part_ml[part_of(k) * 128 + r];
-      const float4 v = C.part_o[(part_of(k) * (HD / 4) + c) * 128 + r];
-      if (ml.y == 0.f) continue;
-      const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), fk = exp2f(ml.x - mn);
-      m = mn;
-      acc.x = f * acc.x + fk * v.x;
-      acc.y = f * acc.y + fk * v.y;
-      acc.z = f * acc.z + fk * v.z;
-      acc.w = f * acc.w + fk * v.w;
-      l = f * l + fk * ml.y;
+  for (int i = 0; i < kMine; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int k0 = first; k0 <= u.last; k0 += kAtOnce) {
+    float2 ml[kMine][kAtOnce];
+    float4 v[kMine][kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int k = min(k0 + x, u.last), r = (row0 + i * kStep) & 127;
+        const int64_t part = ((int64_t)k * 2 + (k == first ? 1 : 0)) * 2 + t;
+        ml[i][x] = C.part_ml[part * 128 + r];
+        v[i][x] = C.part_o[(part * (HD / 4) + c) * 128 + r];
+      }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      float mn = m[i];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        if (k0 + x > u.last) ml[i][x] = make_float2(-INFINITY, 0.f);
+        mn = fmaxf(mn, ml[i][x].x);
+      }
+      const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
+      m[i] = mn;
+      l[i] *= f;
+      acc[i].x *= f;
+      acc[i].y *= f;
+      acc[i].z *= f;
+      acc[i].w *= f;
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        if (ml[i][x].y == 0.f) continue;  // the part saw nothing of this row
+        const float fk = exp2f(ml[i][x].x - mn);
+        acc[i].x += fk * v[i][x].x;
+        acc[i].y += fk * v[i][x].y;
+        acc[i].z += fk * v[i][x].z;
+        acc[i].w += fk * v[i][x].w;
+        l[i] += fk * ml[i][x].y;
+      }
     }
-    const int head = u.g * P.group + r - in_tile * P.group;
+  }
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int tok = token(i), r = (row0 + i * kStep) & 127;
+    if (tok < 0) continue;
+    const int head = u.g * P.group + r % P.group;
     const int64_t t_row = u.q_row + tok;
-    *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) = normalised(acc, l);
-    if (c == 0 && P.lse) P.lse[(int64_t)head * P.batch.T + t_row] = (m + log2f(l)) * 0.69314718055994531f;
+    *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) = normalised(acc[i], l[i]);
+    if (c == 0 && P.lse) P.lse[(int64_t)head * P.batch.T + t_row] = (m[i] + log2f(l[i])) * 0.69314718055994531f;
   }
 }
 
