@@ -7,7 +7,6 @@
 namespace aa {
 
 constexpr uint64_t kAttendWaitNs = 2000000000ull;  // limit of every wait on a copy or a product
-constexpr uint32_t kSleepNs = 20000;               // how long a waiting thread may be suspended at a time
 
 struct AttendParams {
   BatchParams batch;

@@ -58,18 +58,10 @@ struct ShortSmem {
   uint64_t full[kStages], empty[kStages];
 };
 
-// A converged warp waits, bounded; one lane asks, and sleeps meanwhile.
+// A converged warp waits, bounded; one lane asks for all.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, int site) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0 && !ptx::mbar_try_wait_for(bar, parity, kSleepNs)) {
-    const uint64_t t0 = ptx::global_timer_ns();
-    while (ok && !ptx::mbar_try_wait_for(bar, parity, kSleepNs)) {
-      if (ptx::global_timer_ns() - t0 >= kAttendWaitNs) {
-        atomicCAS(err, 0, site);
-        ok = false;
-      }
-    }
-  }
+  if ((threadIdx.x & 31) == 0) ok = ptx::mbar_wait(bar, parity, kAttendWaitNs, err, site);
   return __all_sync(0xffffffffu, ok);
 }
 
