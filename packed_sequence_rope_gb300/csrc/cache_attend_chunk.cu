@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int in_tile = r / P.group;
       const bool row_valid = in_tile < C.tile_tokens && t * C.tile_tokens + in_tile < w.tokens;
-      int lo = 1, hi = 0;  // this row's visible keys
+      // this row's visible keys; rows that are none see all, which needs no mask
+      int lo = 0, hi = INT_MAX;
       if (row_valid) {
         lo = first_key(P, w.q_row + t * C.tile_tokens + in_tile);
         hi = w.p0 + t * C.tile_tokens + in_tile;
