@@ -15,8 +15,24 @@
 
 using namespace aa;
 
-// The kernel for single and few tokens as long as its row tile holds them.
-static bool takes_short(int max_q, int group) { return (int64_t)std::max(max_q, 1) * group <= kShortRows; }
+// Few rows: the kernel for them, whose row tile holds kShortRows. Its warps share a
+// 16-row tile's keys at 16 rows, but at 33 to 64 take 16 rows each and all keys,
+// which at D = 128 costs more than HBM does; there the other kernel takes the calls
+// with work for every SM, and those of short contexts. Measured, microseconds of
+// this one / the other, 8 kv heads of 128, group 4:
+//   rows, sequences   300 keys     2048        16384
+//   32, 1             10.1 / 10.6  9.7 / 16.5  20.6 / 33.8
+//   32, 42            31.7 / 27.4  80.9 / 95.4 461 / 537
+//   64, 1             15.1 / 10.6  14.2 / 16.9 29.4 / 34.3
+//   64, 8             15.1 / 11.5  33.9 / 32.2 131 / 121
+//   64, 42            49.1 / 27.8  117 / 96.0  621 / 538
+// With D = 64: 64 rows of 42 sequences 24.7 / 24.9, 56.9 / 79.0 and 313 / 472.
+static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
+  const int64_t rows = (int64_t)std::max(max_q, 1) * group;
+  if (rows <= 32 || c->cfg.head_dim == 64) return rows <= kShortRows;
+  return rows <= kShortRows && (int64_t)table_width * c->cfg.page_size > kWholeKeys &&
+         (int64_t)num_seqs * c->cfg.num_kv_heads < 64;
+}
 
 extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
                                                   int32_t table_width, int32_t q_heads) {
@@ -24,7 +40,7 @@ extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs
   const int Hkv = c->cfg.num_kv_heads;
   if (c->host_only || q_heads % Hkv || q_heads / Hkv > 64) return 0;
   if (total_tokens >= (1 << 30) || num_seqs > (1 << 20) || (int64_t)table_width * c->cfg.page_size >= (1ll << 30)) return 0;
-  if (takes_short(max_q, q_heads / Hkv))
+  if (takes_short(c, num_seqs, max_q, table_width, q_heads / Hkv))
     return short_workspace_bytes(c, num_seqs, total_tokens, max_q, table_width, q_heads / Hkv);
   return chunk_workspace_bytes(c, num_seqs, total_tokens, q_heads / Hkv);
 }
@@ -69,7 +85,7 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   P.page_shift = __builtin_ctz((unsigned)c->cfg.page_size);
   P.scale_log2 = (float)((softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!takes_short(max_q, P.group)) return launch_attend_chunk(c, P, workspace, s);
+  if (!takes_short(c, batch->num_seqs, max_q, batch->table_width, P.group)) return launch_attend_chunk(c, P, workspace, s);
   cudaError_t e = launch_attend_short(c, P, max_q, workspace, s);
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
 }

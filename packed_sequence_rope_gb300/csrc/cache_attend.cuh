@@ -97,6 +97,12 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Up to so many keys per page table the chunk kernel takes whole units. Measured,
+// 32 / 8 heads of 128, microseconds whole / cut: 8 sequences of 32 new tokens over
+// 700 keys 17.5 / 21.5, 42 of 128 over 500 65.6 / 85.4; over 1000 keys 21.0 / 22.9
+// and 99.7 / 118, but one of 32 20.0 / 15.6; over 2000 20 of 32 69.1 / 62.1.
+constexpr int kWholeKeys = 768;
+
 // Launchers (arguments already checked) and the workspaces they need.
 // short: at most kShortRows rows (max_q * group) of a sequence and kv head at a time.
 constexpr int kShortRows = 64;

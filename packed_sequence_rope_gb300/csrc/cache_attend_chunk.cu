@@ -46,11 +46,6 @@ constexpr int kReaders = 3 + kSoftmaxWarps;  // of a published piece: warps 1 to
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
-// Up to so many keys per page table no unit is cut. Measured, 32 / 8 heads of 128:
-// 8 sequences of 32 new tokens over 700 keys 18.5 us whole and 21.2 us cut, 42 of
-// 128 over 500 71 and 88 us; over 1000 keys 22.5 and 23.1 us, 105 and 119 us, but
-// 8 of 128 41 and 39 us: beyond, long units end unevenly.
-constexpr int kWholeKeys = 768;
 
 // A unit as chunk_plan_kernel describes it: tokens [i0, i0 + tokens) of a
 // sequence, their positions [p0, p0 + tokens), the first key any of them sees.

@@ -93,6 +93,17 @@ def test_chunks(aa, chunk, ps, Hq, Hkv, D):
     _attend(aa, d, ps, Hkv, D)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B", [2, 40])
+@pytest.mark.parametrize("most", [500, 1500])
+def test_up_to_64_rows(aa, D, B, most):
+    """Rows where the choice of kernel depends on the head size, the batch and the contexts."""
+    for new in (8, 9, 13, 16):
+        kv = [max(new, most - 37 * b % most) for b in range(B)]
+        d = ref.make_batch(new + B, kv, [new - b % 3 for b in range(B)], 8, 2, D, 32, device="cuda")
+        _attend(aa, d, 32, 2, D)
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(64, 1), (45, 1), (33, 1), (10, 2)])
 @pytest.mark.parametrize("ps", [32, 64])
 def test_chunks_many_heads_per_group(aa, Hq, Hkv, ps):
