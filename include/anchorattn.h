@@ -515,8 +515,8 @@ typedef struct {
 /* Write the new tokens' keys and values (k, v [T, Hkv, D]) to their pages, the
  * keys rotated by `rope` at pos (device int32 [num_axes, T]; both NULL: stored
  * as they are). With q != NULL the same launch rotates q [T, q_heads, D] into
- * q_out (contiguous; may be q if that is contiguous), which is what
- * aa_cache_attend takes; it needs `rope`. */
+ * q_out (contiguous; may be q if that is contiguous; not in the pool), which is
+ * what aa_cache_attend takes; it needs `rope`. */
 aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const void* k, int64_t k_stride, const void* v,
                           int64_t v_stride, const aa_rope_axes* rope, const int32_t* pos, const void* q,
                           int64_t q_stride, void* q_out, int32_t q_heads, aa_stream_t stream);
@@ -538,7 +538,7 @@ aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const v
  *    sequence with more is still computed, only slower.
  *  - key_lo: device int32 [T] or NULL (0 for every row).
  *  - softmax_scale <= 0 selects 1/sqrt(D).
- *  - o [T, q_heads, D] bf16; lse [q_heads, T] fp32 or NULL.
+ *  - o [T, q_heads, D] bf16; lse [q_heads, T] fp32 or NULL; neither in the pool.
  *  - workspace: aa_cache_attend_workspace_bytes() bytes, 256-byte aligned,
  *    contents ignored; calls that may overlap need one each.
  *  - num_seqs * Hkv < 2^27; q_heads * total_tokens < 2^31. */
@@ -548,8 +548,8 @@ aa_status aa_cache_attend(aa_cache_t cache, const aa_cache_batch* batch, const v
 
 /* Bytes of device scratch aa_cache_attend needs for a batch of these sizes
  * (partial results of keys that are split among CTAs): some 20 to 80 MB, nearly
- * independent of the batch, or 256 bytes where nothing is split. 0 for invalid
- * sizes. */
+ * independent of the batch, or 256 bytes where nothing is split. A smaller batch
+ * may need more. 0 for invalid sizes. */
 size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
                                        int32_t table_width, int32_t q_heads);
 

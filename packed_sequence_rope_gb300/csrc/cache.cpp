@@ -41,6 +41,13 @@ aa_status check_batch(const aa_cache_s* c, const aa_cache_batch* b) {
   return AA_OK;
 }
 
+aa_status check_outside_pool(const aa_cache_s* c, const char* what, const void* out, size_t bytes) {
+  const size_t pool = (size_t)c->cfg.num_layers * c->cfg.num_pages * c->page_elems() * 2;
+  if (overlap(out, bytes, c->k_pages, pool) || overlap(out, bytes, c->v_pages, pool))
+    return fail(AA_ERR_INVALID_ARG, std::string(what) + " overlaps the cache's pages");
+  return AA_OK;
+}
+
 namespace {
 
 aa_status check_seq(const aa_cache_s* c, int32_t s) {

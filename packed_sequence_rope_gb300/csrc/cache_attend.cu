@@ -67,6 +67,9 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
     return fail(AA_ERR_INVALID_ARG, "lse and key_lo must be 4-byte aligned device pointers");
   if (overlap(o, (size_t)T * q_heads * D * 2, q, rows_span(T, q_stride, q_heads, D)))
     return fail(AA_ERR_INVALID_ARG, "o overlaps q");
+  if ((st = check_outside_pool(c, "o", o, (size_t)T * q_heads * D * 2)) != AA_OK ||
+      (lse && (st = check_outside_pool(c, "lse", lse, (size_t)T * q_heads * 4)) != AA_OK))
+    return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(AA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   if (workspace_bytes <

@@ -35,6 +35,8 @@ constexpr int32_t kCacheBadPage = 1, kCacheBadPosition = 2;
 // Refuses NULL, host-only handles and a current device that is not the handle's.
 aa_status check_compute_cache(const aa_cache_s* c);
 aa_status check_batch(const aa_cache_s* c, const aa_cache_batch* b);
+// Refuses an output that lies in the pool.
+aa_status check_outside_pool(const aa_cache_s* c, const char* what, const void* out, size_t bytes);
 
 // One (source, target) pair of a page copy.
 struct PagePair {

@@ -203,6 +203,7 @@ extern "C" aa_status aa_cache_append(aa_cache_t c, const aa_cache_batch* batch, 
     const size_t nq = (size_t)T * q_heads * D * 2;
     if (overlap(q_out, nq, k, rows_span(T, k_stride, Hkv, D)) || overlap(q_out, nq, v, rows_span(T, v_stride, Hkv, D)))
       return fail(AA_ERR_INVALID_ARG, "q_out overlaps k or v");
+    if ((st = check_outside_pool(c, "q_out", q_out, nq)) != AA_OK) return st;
   }
   AppendParams P;
   P.tab = rope ? axes_table(rope) : AxesTable{};

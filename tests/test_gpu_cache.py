@@ -501,6 +501,25 @@ def test_refusals(aa):
         assert (out == 7).all()
 
 
+def test_results_in_the_pool_are_refused(aa):
+    d = ref.make_batch(2, [20, 30], [2, 1], 4, 2, 64, 16, device="cuda")
+    rope, pos = aa.RopeAxes(64, (32,)), torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    with _cache(aa, d, 16, 2, 64) as c:
+        good = dict(q=d["q"], page_table=d["table"], cu_q=d["cu"], kv_len=d["kv"], max_q=2)
+        for pool in (c.k_pages, c.v_pages):
+            before = pool.clone()
+            inside = pool.reshape(-1)[-3 * 4 * 64:].view(3, 4, 64)
+            lse = pool.reshape(-1)[:24].view(torch.float32).view(4, 3)
+            for change in (dict(out=inside), dict(lse=lse)):
+                with pytest.raises(aa.AAError, match="pages"):
+                    c.attend(**(good | change))
+            with pytest.raises(aa.AAError, match="pages"):
+                c.append(d["k"], d["v"], d["table"], d["cu"], d["kv"], rope=rope, pos=pos, q=d["q"], out_q=inside)
+            torch.cuda.synchronize()
+            assert torch.equal(pool, before)
+        c.check_device_error()
+
+
 # ------------------------------------------------------------------ the run of them together
 def test_serving_run_against_the_packed_forward(aa):
     """A packed sequence of documents is prefilled in chunks and then continued token by token through the cache, with
