@@ -149,9 +149,9 @@ class PagedCache:
     def copy_pages(self, src, dst, stream=None):
         """Copy page src[i] to dst[i] (host integers), all layers, keys and values."""
         a, b = _host_i32("src", src), _host_i32("dst", dst)
-        if a.size != b.size:
-            raise ValueError("src and dst must have the same number of entries")
-        _check(lib().aa_cache_copy_pages(self._h, a.ctypes.data, b.ctypes.data, a.size, self._stream(stream)))
+        r = native().cache_copy_pages(self._h.value if self._h else 0, self._dev, a, b, stream)
+        if r:
+            _check(r)
 
     def check_device_error(self, stream=None):
         _check(lib().aa_cache_check_error(self._h, self._stream(stream)))

@@ -383,11 +383,43 @@ PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Page numbers: a buffer of contiguous 32-bit integers (an int32 array).
+struct HostInts {
+  Py_buffer b;
+  HostInts(PyObject* o, const char* name) {
+    if (PyObject_GetBuffer(o, &b, PyBUF_FORMAT | PyBUF_C_CONTIGUOUS)) throw python_error();
+    const bool fits = b.ndim == 1 && b.itemsize == 4 && b.format && (b.format[0] == 'i' || b.format[0] == 'l') && !b.format[1];
+    if (!fits) PyBuffer_Release(&b);
+    TORCH_CHECK_VALUE(fits, name, " must be an int32 array");
+  }
+  ~HostInts() { PyBuffer_Release(&b); }
+  HostInts(const HostInts&) = delete;
+  const int32_t* data() const { return static_cast<const int32_t*>(b.buf); }
+  Py_ssize_t size() const { return b.len / 4; }
+};
+
+// cache_copy_pages(cache, device, src, dst, stream)
+PyObject* cache_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count("cache_copy_pages", n, 5);
+  const auto cache = as_handle<aa_cache_t>(a[0]);
+  const int64_t dev = as_int(a[1]);  // -1: no device, which the library refuses
+  const HostInts src(a[2], "src"), dst(a[3], "dst");
+  TORCH_CHECK_VALUE(src.size() == dst.size(), "src and dst must have the same number of entries");
+  TORCH_CHECK_VALUE(src.size() <= INT32_MAX, "src and dst are too long");
+  std::optional<OnStream> on;
+  if (dev >= 0) on.emplace(a[4], at::Device(at::kCUDA, (c10::DeviceIndex)dev));
+  const aa_stream_t s = on ? on->s : nullptr;
+  return PyLong_FromLong(without_gil([&] { return aa_cache_copy_pages(cache, src.data(), dst.data(), (int32_t)src.size(), s); }));
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"rope_apply", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_apply)), METH_FASTCALL, nullptr},
     {"rope_autograd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_autograd)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"cache_attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_attend)), METH_FASTCALL, nullptr},
+    {"cache_copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_copy_pages)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
