@@ -60,7 +60,7 @@ struct Unit {
 
 // A cut unit, as the CTA that begins it describes it to chunk_join_kernel: its
 // parts lie with the CTAs from that one to `last`. last < 0: the CTA begins none.
-struct Cut {
+struct alignas(16) Cut {
   int32_t last, g, q_row, tokens;
 };
 
@@ -68,6 +68,7 @@ struct ChunkParams {
   AttendParams a;
   int tile_tokens;     // tokens per row tile: 128 / group
   int slots;           // room for the units of one kv head
+  int ctas;            // of the attention kernel, unless it takes whole units
   int whole_units;     // short contexts: CTAs take whole units, there is no plan and nothing to join
   int64_t* tiles_end;  // [slots + 1] running sum of the units' costs in key tiles; [0] = 0
   Unit* units;         // [slots]
@@ -252,7 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const AttendParams& P = C.a;
   const BatchParams& b = P.batch;
   if (ptx::smem_u32(smem_raw) & 1023u) {  // swizzled tiles need a 1 KB aligned base
-    if (threadIdx.x == 0) atomicCAS(b.err, 0, 498);
+    if (threadIdx.x == 0) {
+      atomicCAS(b.err, 0, 498);
+      if (!C.whole_units) C.cuts[blockIdx.x] = Cut{-1, 0, 0, 0};
+    }
     return;
   }
   ChunkSmem<HD>& sm = *reinterpret_cast<ChunkSmem<HD>*>(smem_raw);
@@ -693,10 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_ld32(t_o + c * 32, ov);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            po[(c * 8 + e) * 128] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          for (int e = 0; e < 8; ++e)  // hi: rows that are none leave nothing
+            if (hi != INT_MAX) po[(c * 8 + e) * 128] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
         }
-        if (half == 0) C.part_ml[part * 128 + r] = make_float2(m, l);
+        if (hi != INT_MAX && half == 0) C.part_ml[part * 128 + r] = make_float2(m, l);
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.piece_empty[li & 1]);
@@ -709,87 +713,150 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining cut units
-// blockIdx.y = a CTA of the attention kernel: if it began a cut unit, the
-// unit's partial results are joined here, kJoinRows rows per block. A thread
-// keeps the loads of kAtOnce parts of its rows in flight: with long contexts and
-// few new tokens a unit has some twenty parts, and there are few rows to hide
-// their latency behind.
-constexpr int kJoinRows = 16, kAtOnce = 4;
+// kJoinRows rows of a cut unit at a time. With kHelp false blockIdx.y is a CTA of the
+// attention kernel, and the block joins the unit that it began, if any. Contexts that
+// are long for their few new tokens give few units many parts, and few rows to hide
+// their latency behind: a thread keeps the loads of kAtOnce parts of its rows in
+// flight, and with kHelp every block lists the cut units, up to kMaxHelp blocks take a
+// share of the channels of the same rows, and the threads that this frees a share of
+// the parts. Measured without / with, D = 128: 17 tokens of one sequence and kv head
+// over 52K keys 66 / 26 us (138 parts), over 8K 26 / 18, over 1000 15.7 / 16.6; 64
+// tokens of 8 sequences, 8 kv heads, over 1000 keys 27.0 / 30.0.
+constexpr int kJoinRows = 16, kJoinThreads = 256, kAtOnce = 4, kMaxHelp = 8;
+constexpr int kMaxCtas = kJoinThreads;  // a thread looks at each CTA's cut
+constexpr int kJoinBlocks = 3;          // per SM
+constexpr int kHelpKeys = 2048;         // blocks help with contexts above
+constexpr int kHelpParts = 8;           // and where units can have so many parts
 
-template <int HD>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams C) {
-  constexpr int kStep = 256 / (HD / 4);  // rows at a time: consecutive threads read consecutive rows
-  constexpr int kMine = kJoinRows / kStep;
-  const AttendParams& P = C.a;
-  const int first = (int)blockIdx.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Cut u = C.cuts[first];
-  if (u.last < 0) return;
-  const int c = threadIdx.x / kStep, row0 = blockIdx.x * kJoinRows + threadIdx.x % kStep;
-  const int t = (int)(blockIdx.x * kJoinRows) >> 7;  // row tile
-  auto token = [&](int i) {  // of the i-th of this thread's rows; < 0: none
-    const int in_tile = ((row0 + i * kStep) & 127) / P.group, tok = t * C.tile_tokens + in_tile;
-    return in_tile < C.tile_tokens && tok < u.tokens ? tok : -1;
-  };
-  float m[kMine], l[kMine];
-  float4 acc[kMine];
+// Rows' running maximum (log2 units), sum and unnormalised O.
+struct JoinState {
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the next N results of the row; ml.y == 0: one that saw nothing of it
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N]) {
+    float mn = m;
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < N; ++x) mn = fmaxf(mn, ml[x].x);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
+    m = mn;
+    l *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      if (ml[x].y == 0.f) continue;
+      const float fk = exp2f(ml[x].x - mn);
+      acc.x += fk * v[x].x;
+      acc.y += fk * v[x].y;
+      acc.z += fk * v[x].z;
+      acc.w += fk * v[x].w;
+      l += fk * ml[x].y;
+    }
   }
-  for (int k0 = first; k0 <= u.last; k0 += kAtOnce) {
+};
+
+template <int HD, bool kHelp>
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) chunk_join_kernel(const __grid_constant__ ChunkParams C) {
+  constexpr int kStep = kJoinThreads / (HD / 4);  // rows at a time: consecutive threads read consecutive rows
+  constexpr int kMine = kJoinRows / kStep, kPieces = 256 / kJoinRows;
+  const AttendParams& P = C.a;
+  const int tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Cut u;
+  int first, rows0, most = 1, share_of = 0;  // most: blocks that may share a unit's rows
+  if constexpr (kHelp) {
+    __shared__ Cut cuts[kMaxCtas];
+    __shared__ int begins[kMaxCtas], found[kJoinThreads / 32];
+    const Cut cut = tid < C.ctas ? C.cuts[tid] : Cut{-1, 0, 0, 0};
+    const uint32_t here = __ballot_sync(0xffffffffu, cut.last >= 0);
+    if ((tid & 31) == 0) found[tid >> 5] = __popc(here);
+    __syncthreads();
+    int units = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w == tid >> 5) before = units;
+      units += found[w];
+    }
+    if (cut.last >= 0) {
+      before += __popc(here & ((1u << (tid & 31)) - 1u));
+      cuts[before] = cut;
+      begins[before] = tid;
+    }
+    __syncthreads();
+    while (most < kMaxHelp && units * kPieces * most * 2 <= (int)gridDim.x) most *= 2;
+    const int unit = (int)blockIdx.x / (kPieces * most);
+    if (unit >= units) return;
+    u = cuts[unit];
+    first = begins[unit];
+    share_of = (int)blockIdx.x / kPieces % most;
+    rows0 = (int)blockIdx.x % kPieces * kJoinRows;
+  } else {
+    first = (int)blockIdx.y;
+    u = C.cuts[first];
+    if (u.last < 0) return;
+    rows0 = (int)blockIdx.x * kJoinRows;
+  }
+  const int t = rows0 >> 7, parts = u.last - first + 1;  // row tile
+  if (t * C.tile_tokens + (rows0 & 127) / P.group >= u.tokens) return;  // the rows hold no token
+  int help = 1;
+  while (help < most && parts >= 2 * help * kAtOnce) help *= 2;
+  if (share_of >= help) return;
+  const int columns = HD / 4 / help, group = tid / (kStep * columns);  // columns of four channels
+  const int c = share_of * columns + tid / kStep % columns;
+  auto row = [&](int i) { return (rows0 + tid % kStep + i * kStep) & 127; };
+  JoinState mine[kMine];
+  const int share = (parts + help - 1) / help, begin = first + group * share, end = min(begin + share, u.last + 1);
+  for (int k0 = begin; k0 < end; k0 += kAtOnce) {
     float2 ml[kMine][kAtOnce];
     float4 v[kMine][kAtOnce];
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
 #pragma unroll
       for (int x = 0; x < kAtOnce; ++x) {
-        const int k = min(k0 + x, u.last), r = (row0 + i * kStep) & 127;
+        const int k = k0 + x;
         const int64_t part = ((int64_t)k * 2 + (k == first ? 1 : 0)) * 2 + t;
-        ml[i][x] = C.part_ml[part * 128 + r];
-        v[i][x] = C.part_o[(part * (HD / 4) + c) * 128 + r];
+        ml[i][x] = k < end ? C.part_ml[part * 128 + row(i)] : make_float2(-INFINITY, 0.f);
+        v[i][x] = k < end ? C.part_o[(part * (HD / 4) + c) * 128 + row(i)] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      float mn = m[i];
+    for (int i = 0; i < kMine; ++i) mine[i].add(ml[i], v[i]);
+  }
+  if constexpr (kHelp) {
+    if (help > 1) {  // the first group's threads take the other groups' results, in order
+      __shared__ float4 group_o[kMine][kJoinThreads];
+      __shared__ float2 group_ml[kMine][kJoinThreads];
 #pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        if (k0 + x > u.last) ml[i][x] = make_float2(-INFINITY, 0.f);
-        mn = fmaxf(mn, ml[i][x].x);
+      for (int i = 0; i < kMine; ++i) {
+        group_o[i][tid] = mine[i].acc;
+        group_ml[i][tid] = make_float2(mine[i].m, mine[i].l);
       }
-      const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
-      m[i] = mn;
-      l[i] *= f;
-      acc[i].x *= f;
-      acc[i].y *= f;
-      acc[i].z *= f;
-      acc[i].w *= f;
+      __syncthreads();
+      if (group > 0) return;
+      for (int g = 1; g < help; ++g)
 #pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        if (ml[i][x].y == 0.f) continue;  // the part saw nothing of this row
-        const float fk = exp2f(ml[i][x].x - mn);
-        acc[i].x += fk * v[i][x].x;
-        acc[i].y += fk * v[i][x].y;
-        acc[i].z += fk * v[i][x].z;
-        acc[i].w += fk * v[i][x].w;
-        l[i] += fk * ml[i][x].y;
-      }
+        for (int i = 0; i < kMine; ++i) {
+          const float2 ml[1] = {group_ml[i][tid + g * kStep * columns]};
+          const float4 v[1] = {group_o[i][tid + g * kStep * columns]};
+          mine[i].add(ml, v);
+        }
     }
   }
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int tok = token(i), r = (row0 + i * kStep) & 127;
-    if (tok < 0) continue;
-    const int head = u.g * P.group + r % P.group;
+    const int r = row(i), in_tile = r / P.group, tok = t * C.tile_tokens + in_tile;
+    if (in_tile >= C.tile_tokens || tok >= u.tokens) continue;  // the row holds no token
+    const int head = u.g * P.group + r - in_tile * P.group;
     const int64_t t_row = u.q_row + tok;
-    *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) = normalised(acc[i], l[i]);
-    if (c == 0 && P.lse) P.lse[(int64_t)head * P.batch.T + t_row] = (m[i] + log2f(l[i])) * 0.69314718055994531f;
+    *reinterpret_cast<uint2*>(P.o + (t_row * P.Hq + head) * HD + c * 4) = normalised(mine[i].acc, mine[i].l);
+    if (c == 0 && P.lse) P.lse[(int64_t)head * P.batch.T + t_row] = (mine[i].m + log2f(mine[i].l)) * 0.69314718055994531f;
   }
 }
 
 // ---------------------------------------------------------------- launches
+int ctas_for(const aa_cache_s* c) { return std::min(c->num_sms, kMaxCtas); }
 int slots_for(int tokens, int seqs, int tile_tokens) { return tokens / (2 * tile_tokens) + seqs; }
 
 template <int HD>
@@ -800,7 +867,8 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   C.tile_tokens = 128 / P.group;
   C.slots = slots_for(b.T, b.B, C.tile_tokens);
   C.whole_units = ((int64_t)b.W << P.page_shift) <= kWholeKeys;
-  const int ctas = c->num_sms;
+  const int ctas = ctas_for(c);
+  C.ctas = ctas;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   C.part_o = reinterpret_cast<float4*>(w);
   w += align256((size_t)ctas * 4 * 128 * HD * 4);
@@ -830,17 +898,18 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "chunk_plan_kernel launch");
   e = launch_after(attend_chunk_kernel<HD>, dim3((unsigned)ctas), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel launch");
-  if (ctas > 1) {
-    e = launch_after(chunk_join_kernel<HD>, dim3(256 / kJoinRows, (unsigned)(ctas - 1)), 256, 0, s, C);
-    if (e != cudaSuccess) return cuda_fail(e, "chunk_join_kernel launch");
-  }
+  const bool few = (int64_t)C.slots * b.Hkv * kHelpParts <= ctas && ((int64_t)b.W << P.page_shift) > kHelpKeys;
+  static_assert(256 / kJoinRows <= kHelpParts * kJoinBlocks, "a block for each piece of the few units");
+  e = few ? launch_after(chunk_join_kernel<HD, true>, dim3((unsigned)(kJoinBlocks * ctas)), kJoinThreads, 0, s, C)
+          : launch_after(chunk_join_kernel<HD, false>, dim3(256 / kJoinRows, (unsigned)ctas), kJoinThreads, 0, s, C);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk_join_kernel launch");
   return AA_OK;
 }
 
 }  // namespace
 
 size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int group) {
-  const size_t slots = slots_for(total_tokens, num_seqs, 128 / group), ctas = c->num_sms;
+  const size_t slots = slots_for(total_tokens, num_seqs, 128 / group), ctas = ctas_for(c);
   return align256(ctas * 4 * 128 * c->cfg.head_dim * 4) + align256(ctas * 4 * 128 * 8) + align256(ctas * sizeof(Cut)) +
          align256(slots * sizeof(Unit)) + align256((slots + 1) * 8);
 }

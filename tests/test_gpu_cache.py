@@ -149,6 +149,19 @@ def test_long_chunk_over_long_context(aa):
 
 
 # ------------------------------------------------------------------ attend: values, layouts, streams
+@pytest.mark.parametrize("new,kv,Hq,Hkv,D", [(17, 52000, 8, 1, 128), (5, 70000, 16, 1, 64), (40, 20000, 8, 1, 64),
+                                              (33, 2200, 8, 2, 128), (130, 9000, 16, 2, 128), (300, 5000, 4, 4, 64)])
+def test_few_units_with_many_parts(aa, new, kv, Hq, Hkv, D):
+    """Long contexts of one or two sequences: a unit's keys are split among many CTAs."""
+    for lens, n in (([kv], [new]), ([kv, kv // 3], [new, new // 2])):
+        d = ref.make_batch(new, lens, n, Hq, Hkv, D, 64, device="cuda")
+        _attend(aa, d, 64, Hkv, D)
+        lo = torch.full((sum(n),), kv // 5, dtype=torch.int32, device="cuda")
+        lo[::7] = kv  # rows that see nothing but the anchor
+        for anchor in (False, True):
+            _attend(aa, d, 64, Hkv, D, key_lo=lo, anchor=anchor)
+
+
 @pytest.mark.parametrize("new", [1, 4, 200])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_what_no_row_sees_does_not_reach_the_result(aa, new, bad):
