@@ -21,12 +21,12 @@ using namespace aa;
 // with work for every SM, and those of short contexts. Measured, microseconds of
 // this one / the other, 8 kv heads of 128, group 4:
 //   rows, sequences   300 keys     2048        16384
-//   32, 1             10.1 / 10.6  9.7 / 16.5  20.6 / 33.8
-//   32, 42            31.7 / 27.4  80.9 / 95.4 461 / 537
-//   64, 1             15.1 / 10.6  14.2 / 16.9 29.4 / 34.3
-//   64, 8             15.1 / 11.5  33.9 / 32.2 131 / 121
-//   64, 42            49.1 / 27.8  117 / 96.0  621 / 538
-// With D = 64: 64 rows of 42 sequences 24.7 / 24.9, 56.9 / 79.0 and 313 / 472.
+//   32, 1             10.1 / 10.5  9.6 / 16.7  20.6 / 27.1
+//   32, 42            31.8 / 27.2  81.1 / 89.1 457 / 534
+//   64, 1             15.1 / 10.7  14.2 / 17.3 29.2 / 28.8
+//   64, 8             15.1 / 11.6  33.9 / 29.6 131 / 118
+//   64, 42            49.1 / 27.7  117 / 92.0  621 / 537
+// With D = 64: 64 rows of 42 sequences 24.4 / 25.0, 56.9 / 76.2 and 314 / 469.
 static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
   const int64_t rows = (int64_t)std::max(max_q, 1) * group;
   if (rows <= 32 || c->cfg.head_dim == 64) return rows <= kShortRows;

@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) chunk_join_kernel(c
     rows0 = (int)blockIdx.x * kJoinRows;
   }
   const int t = rows0 >> 7, parts = u.last - first + 1;  // row tile
-  if (t * C.tile_tokens + (rows0 & 127) / P.group >= u.tokens) return;  // the rows hold no token
+  if ((rows0 & 127) >= (u.tokens - t * C.tile_tokens) * P.group) return;  // the rows hold no token
   int help = 1;
   while (help < most && parts >= 2 * help * kAtOnce) help *= 2;
   if (share_of >= help) return;
