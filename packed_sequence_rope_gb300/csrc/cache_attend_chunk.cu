@@ -190,12 +190,12 @@ struct ChunkSmem {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], drain;
   Piece piece[2];
-  // between the two warps of 32 rows, [column half][lane]: maxima of a step (by
-  // its parity; rounded to bf16: any bound near the maximum serves), then sums
-  union {
-    __nv_bfloat16 max[2][2][32];
-    float sum[2][32];
-  } pair[2][4];  // [row tile][32 rows]
+  // Between the two warps of 32 rows, [row tile][32 rows][column half][lane]: the
+  // maxima of a step, then the sums. One buffer serves all steps: a step's S is
+  // issued only after both warps have handed over the last step's weights, and so
+  // have read its maxima. In fp32: a base that is off by a fraction of a large
+  // maximum leaves weights that underflow to 0.
+  float pair[2][4][2][32];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -567,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The row's maximum over both column halves, and what it changes. Also the
         // point where both warps have read their columns of S: P may overwrite them.
         auto agree = [&](float mt) {
-          pair.max[i & 1][half][lane] = __float2bfloat16_ru(mt);
+          pair[half][lane] = mt;
           if (!ptx::bar_and(pair_bar, 64, true)) return false;
-          mt = __bfloat162float(__hmax(pair.max[i & 1][0][lane], pair.max[i & 1][1][lane])) * sl2;
+          mt = fmaxf(pair[0][lane], pair[1][lane]) * sl2;
           // TMEM access is warp-collective, so a rescale of O is decided per warp (alike for both)
           const bool need = (mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY);
           if (__any_sync(0xffffffffu, need)) {
@@ -639,9 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       ok = warp_wait(&sm.o_full[t], nq & 1, b.err, abort_flag, 483);
-      pair.sum[half][lane] = l;  // the partner has read the last step's maxima: O is complete
+      pair[half][lane] = l;  // the partner has read the last step's maxima: O is complete
       if (!ptx::bar_and(pair_bar, 64, ok)) break;
-      l += pair.sum[half ^ 1][lane];
+      l += pair[half ^ 1][lane];
       // ---- epilogue, half of the channels per warp. Its TMEM reads complete
       // (tmem_wait_ld) before this thread's next p_full arrival, which the next
       // piece's first PV of this tile (overwriting O) waits for.

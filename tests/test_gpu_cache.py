@@ -187,6 +187,22 @@ def test_large_logits_and_scales(aa):
             _attend(aa, d, 64, 2, 64, softmax_scale=scale)
 
 
+@pytest.mark.parametrize("logit", [2e4, 5e4, -2e4, -5e4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,kv", [(1, 500), (1, 20000), (120, 500), (120, 3500)])
+def test_logits_of_tens_of_thousands(aa, logit, D, new, kv):
+    """Maxima far from 0 on both sides: a row's base has to be within a few units of its maximum, whatever its size.
+    Both kernels, with whole and with cut units; the rows' logits differ by some tens."""
+    d = ref.make_batch(kv, [kv], [new], 4, 2, D, 64, device="cuda")
+    a = math.sqrt(abs(logit) / math.sqrt(D))
+    g = torch.Generator().manual_seed(7)
+    rows = a * (1.0 + 0.2 * torch.rand(d["q"].shape[:2] + (1,), generator=g)).cuda()
+    d["q"].copy_(rows + 0.1 * d["q"])
+    d["k_pages"].copy_(math.copysign(a, logit) + 0.3 * d["k_pages"])
+    o, lse = _attend(aa, d, 64, 2, D)
+    assert torch.isfinite(lse).all() and (o.float().abs().amax(-1) > 0).all()
+
+
 def test_values_far_apart(aa):
     """One key far above the others, first, in the middle or last; and logits of -inf from infinite keys."""
     for new in (1, 130):
