@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const KeyTiles<kKeys> keys(w.lo, hi, P.anchor);
       auto row_of = [&](int i) {
         const int j = keys.tile(i) * kKeys + (part << piece_shift);
-        // pieces that no row sees are not looked up
-        const bool seen = j <= hi && (j + (1 << piece_shift) > w.lo || (j == 0 && P.anchor));
+        // pieces that no row sees are not looked up (lo > hi: the rows see the anchor at most)
+        const bool seen = j <= hi && ((w.lo <= hi && j + (1 << piece_shift) > w.lo) || (j == 0 && P.anchor));
         return lane < copies && i < w.first + w.take && i < keys.count && seen ? pool_row(b, w.seq, w.g, j, P.page_shift)
                                                                                : kNoRow;
       };
@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ clearing unseen values (warps 2 and 3)
     // The rows of V that no row of the unit sees have weight 0, but 0 * NaN is
     // not. Pieces that were not looked up hold zeros already, which leaves the
-    // unseen rows of the pieces at the ends of [lo, hi], and behind the anchor.
+    // unseen rows of the pieces at the ends of [lo, hi], and behind the anchor (all
+    // of its piece's, where no row sees another key: lo > hi).
     constexpr int kChunks = kB * 8, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row, rows a warp clears at once
     const int piece = 1 << min(P.page_shift, 6), chunk = lane % kChunks;
     const int first_row = (warp - 2) * kRowsAtOnce + lane / kChunks;
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           const bool anchored = P.anchor && j0 == 0 && hi >= 0 && w.lo > 0;
           const int lo_piece = w.lo & ~(piece - 1);  // its copy starts here
-          if (anchored) clear(1, min(piece, w.lo));
+          if (anchored) clear(1, w.lo <= hi ? min(piece, w.lo) : piece);
           if (w.lo <= hi) {
             clear(max(lo_piece - j0, anchored ? 1 : 0), w.lo - j0);
             clear(hi + 1 - j0, (hi | (piece - 1)) + 1 - j0);

@@ -180,6 +180,25 @@ def test_what_no_row_sees_does_not_reach_the_result(aa, new, bad):
     assert torch.isfinite(o.float()).all()
 
 
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+@pytest.mark.parametrize("wide", [1, 90])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_chunks_that_see_only_the_anchor(aa, ps, wide, bad):
+    """Every row's first key lies behind its position, in the page of the last one: of that page, and of the anchor's, no
+    row sees anything but key 0."""
+    for kv, new, Hq, D in ((6, 6, 16, 128), (100, 40, 4, 128), (100, 90, 2, 64), (127, 40, 4, 64), (300, 40, 4, 128)):
+        d = ref.make_batch(kv, [kv], [new], Hq, 1, D, ps, device="cuda", extra_width=wide)
+        for pages in (d["k_pages"], d["v_pages"]):
+            first = pages[0, d["table"][0, 0], 0, 0].clone()
+            pages.fill_(bad)
+            pages[0, d["table"][0, 0], 0, 0] = first
+        for lo in {kv, -(-(kv + 1) // ps) * ps - 1, kv + 1000}:
+            key_lo = torch.full((new,), lo, dtype=torch.int32, device="cuda")
+            o, _ = _attend(aa, d, ps, 1, D, key_lo=key_lo, anchor=True)
+            # one key of weight 1
+            assert torch.equal(o, d["v_pages"][0, d["table"][0, 0], 0, 0].expand_as(o))
+
+
 def test_large_logits_and_scales(aa):
     for new in (1, 150):
         for scale in (0.5, 4.0):
