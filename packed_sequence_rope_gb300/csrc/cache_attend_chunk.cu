@@ -571,8 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           pair[half][lane] = mt;
           if (!ptx::bar_and(pair_bar, 64, true)) return false;
           mt = fmaxf(pair[0][lane], pair[1][lane]) * sl2;
-          // TMEM access is warp-collective, so a rescale of O is decided per warp (alike for both)
-          const bool need = (mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY);
+          // TMEM access is warp-collective, so a rescale of O is decided per warp (alike
+          // for both), and by rows that hold a token alone: what lies in the others
+          // (the next sequence's queries, old shared memory) must not change a bit
+          const bool need = row_valid && ((mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY));
           if (__any_sync(0xffffffffu, need)) {
             const float mn = fmaxf(m, mt);
             const float f = (m == -INFINITY) ? 0.f : exp2f(m - mn);

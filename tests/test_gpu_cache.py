@@ -323,6 +323,44 @@ def test_runs_agree_bit_for_bit_and_across_streams(aa):
             assert all(torch.equal(x, want) for x in got)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(6, 2, 128), (14, 2, 128), (5, 1, 64), (7, 1, 64)])
+def test_rows_that_hold_no_token_change_nothing(aa, Hq, Hkv, D):
+    """Groups that do not divide 128 leave rows of a tile without a token, over whatever shared memory holds: the same
+    call after calls with other queries, which leave small and large values there, gives the same bits."""
+    ps = 64
+    for kv in (700, 2600):  # whole units; cut ones
+        d = ref.make_batch(Hq, [kv] * 12, [80] * 12, Hq, Hkv, D, ps, device="cuda", extra_width=0)
+        n = 160 * 256
+        q = torch.randn(n, Hkv, D, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+        table = d["table"][:1].expand(160, -1).contiguous()
+        cu = torch.arange(0, n + 1, 256, dtype=torch.int32, device="cuda")
+        length = torch.full((160,), 256, dtype=torch.int32, device="cuda")
+        with _cache(aa, d, ps, Hkv, D) as c:
+            got = []
+            for times in (0.0, 1.0, 30.0, 1000.0):
+                c.attend(q * times, table, cu, length, 256)
+                got.append(c.attend(d["q"], d["table"], d["cu"], d["kv"], 80, return_lse=True))
+            torch.cuda.synchronize()
+            c.check_device_error()
+        assert all(torch.equal(x[0], got[0][0]) and torch.equal(x[1], got[0][1]) for x in got)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (6, 2, 128), (4, 4, 64)])
+def test_a_sequence_does_not_depend_on_the_next_ones_queries(aa, Hq, Hkv, D):
+    """The rows behind a sequence's last token hold the next sequence's queries: the first one's bits are the same
+    whatever those are, and without them."""
+    ps, new = 64, 300 // (Hq // Hkv) - 7
+    d = ref.make_batch(Hq, [700, 700], [new, new], Hq, Hkv, D, ps, device="cuda", extra_width=0)
+    with _cache(aa, d, ps, Hkv, D) as c:
+        want = c.attend(d["q"][:new], d["table"][:1], d["cu"][:2], d["kv"][:1], new, return_lse=True)
+        for times in (1.0, 30.0, 1000.0):
+            q = d["q"].clone()
+            q[new:] *= times
+            o, lse = c.attend(q, d["table"], d["cu"], d["kv"], new, return_lse=True)
+            assert torch.equal(o[:new], want[0]) and torch.equal(lse[:, :new], want[1])
+        c.check_device_error()
+
+
 def test_graph_replay_follows_lengths_and_tables(aa):
     for new in (1, 100):
         Hq, Hkv, D, ps = 8, 2, 128, 32
