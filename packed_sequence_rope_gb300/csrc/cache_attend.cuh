@@ -43,6 +43,21 @@ __device__ __forceinline__ int first_key(const AttendParams& P, int t) {
   return P.key_lo ? min(max(__ldg(P.key_lo + t), 0), 1 << 30) : 0;
 }
 
+// Bit x: some of the tokens q_row + i (i < tokens, at positions p0 + i) sees key
+// j + x, x < 64 (a whole warp asks). Together they see every key from the smallest
+// first key to the last position, unless some of them see nothing.
+__device__ __forceinline__ uint64_t seen_keys(const AttendParams& P, int q_row, int p0, int tokens, int j) {
+  const int a = j + (threadIdx.x & 31), b = a + 32;
+  bool sees_a = P.anchor && a == 0 && p0 + tokens > 0, sees_b = false;
+#pragma unroll 1
+  for (int i = max(j - p0, 0); i < tokens; ++i) {
+    const int lo = first_key(P, q_row + i), hi = p0 + i;
+    sees_a |= lo <= a && a <= hi;
+    sees_b |= lo <= b && b <= hi;
+  }
+  return __ballot_sync(0xffffffffu, sees_a) | (uint64_t)__ballot_sync(0xffffffffu, sees_b) << 32;
+}
+
 // Four channels of a row divided by its sum, in bf16; 0 for a row that saw
 // nothing (a NaN among its logits makes the sum NaN, and the row).
 __device__ __forceinline__ uint2 normalised(const float4& o, float sum) {

@@ -53,9 +53,10 @@ constexpr int kMinShare = 2;  // key tiles a CTA takes at least
 constexpr int kUnitCost = 2;
 
 // A unit as chunk_plan_kernel describes it: tokens [i0, i0 + tokens) of a
-// sequence, their positions [p0, p0 + tokens), the first key any of them sees.
+// sequence, their positions [p0, p0 + tokens), the smallest of their first keys;
+// gaps: some of them see nothing, so that keys between seen ones may be unseen.
 struct Unit {
-  int32_t seq, q_row, tokens, p0, lo;
+  int32_t seq, q_row, tokens, p0, lo, gaps;
 };
 
 // A cut unit, as the CTA that begins it describes it to chunk_join_kernel: its
@@ -89,7 +90,7 @@ __device__ __forceinline__ Unit load_unit(const ChunkParams& C, int slot, int* c
   const int seq = warp_last(b.B, [&](int i) { return __ldg(b.cu_q + i) / unit_tokens + i <= slot; });
   const SeqSpan s = load_seq(b, seq, P.page_shift);
   const int64_t i0 = (int64_t)(slot - __ldg(b.cu_q + seq) / unit_tokens - seq) * unit_tokens;
-  Unit u{seq, 0, 0, 0, 0};
+  Unit u{seq, 0, 0, 0, 0, 0};
   *count = 0;
   if (i0 >= 0 && i0 < s.n) {
     u.q_row = s.q0 + (int)i0;
@@ -97,8 +98,14 @@ __device__ __forceinline__ Unit load_unit(const ChunkParams& C, int slot, int* c
     u.p0 = s.kv - s.n + (int)i0;
     if (P.key_lo) {
       int lo = INT_MAX;
-      for (int i = lane; i < u.tokens; i += 32) lo = min(lo, first_key(P, u.q_row + i));
+      bool gaps = false;
+      for (int i = lane; i < u.tokens; i += 32) {
+        const int first = first_key(P, u.q_row + i);
+        lo = min(lo, first);
+        gaps |= first > u.p0 + i;
+      }
       u.lo = __reduce_min_sync(0xffffffffu, lo);
+      u.gaps = __any_sync(0xffffffffu, gaps);
     }
     // rows that see nothing are written too: at least one tile
     *count = max(KeyTiles<kKeys>(u.lo, u.p0 + u.tokens - 1, P.anchor).count, 1);
@@ -170,7 +177,7 @@ struct Shares {
 // ---------------------------------------------------------------- attention
 // One piece of work: key tiles [first, first + take) of a unit's `count`.
 struct Piece {
-  int valid, g, seq, q_row, tokens, p0, lo;
+  int valid, g, seq, q_row, tokens, p0, lo, gaps;
   int first, take, whole;  // whole: the unit is not cut
   int part;                // else: which of the CTA's two partial results
 };
@@ -324,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.tokens = u.tokens;
           w.p0 = u.p0;
           w.lo = u.lo;
+          w.gaps = u.gaps;
         }
         w.valid = count > 0;
         w.take = count;
@@ -339,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.tokens = u.tokens;
           w.p0 = u.p0;
           w.lo = u.lo;
+          w.gaps = u.gaps;
           const int64_t until = min(begin + count, end);
           w.first = (int)max(at - begin - kUnitCost, (int64_t)0);
           w.take = (int)max(until - begin - kUnitCost, (int64_t)0) - w.first;
@@ -486,7 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The rows of V that no row of the unit sees have weight 0, but 0 * NaN is
     // not. Pieces that were not looked up hold zeros already, which leaves the
     // unseen rows of the pieces at the ends of [lo, hi], and behind the anchor (all
-    // of its piece's, where no row sees another key: lo > hi).
+    // of its piece's, where no row sees another key: lo > hi). Where rows of the unit
+    // see nothing, the keys at the new tokens' positions are looked at one by one.
     constexpr int kChunks = kB * 8, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row, rows a warp clears at once
     const int piece = 1 << min(P.page_shift, 6), chunk = lane % kChunks;
     const int first_row = (warp - 2) * kRowsAtOnce + lane / kChunks;
@@ -515,6 +525,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (w.lo <= hi) {
             clear(max(lo_piece - j0, anchored ? 1 : 0), w.lo - j0);
             clear(hi + 1 - j0, (hi | (piece - 1)) + 1 - j0);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (w.gaps && j0 + kKeys - 1 > w.p0) {
+          const int from = (warp - 2) * 64;  // half of the tile's keys per warp
+          for (uint64_t none = ~seen_keys(P, w.q_row, w.p0, w.tokens, j0 + from); none; none &= none - 1) {
+            const int row = from + __ffsll((long long)none) - 1;
+            if (lane < kChunks)
+              *reinterpret_cast<uint4*>(sm.v[s][chunk >> 3] + row * 128 + (chunk & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();

@@ -206,6 +206,35 @@ def test_large_logits_and_scales(aa):
             _attend(aa, d, 64, 2, 64, softmax_scale=scale)
 
 
+@pytest.mark.parametrize("new,Hq,Hkv,D,ps", [(5, 8, 2, 128, 16), (16, 4, 4, 64, 64), (15, 4, 1, 64, 32), (40, 4, 1, 128, 64),
+                                             (90, 14, 2, 128, 16), (300, 2, 2, 64, 128)])
+@pytest.mark.parametrize("anchor", [False, True])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_rows_that_see_nothing_hide_their_own_keys(aa, new, Hq, Hkv, D, ps, anchor, bad):
+    """Rows whose first key lies behind their position leave keys between seen ones that no row sees: behind the last row
+    that sees any, in front of the first, and in between. NaN and infinities there stay out of the result."""
+    g = torch.Generator().manual_seed(new)
+    for held in (0, 77, 1500):
+        kv = held + new
+        p = torch.arange(held, kv)
+        tail, middle, front = torch.zeros(new, dtype=torch.long), p - 3, p.clone()
+        tail[new * 2 // 3:] = 1 << 30
+        middle[new // 4:new // 2] = kv + 5
+        front[:new // 3] = held + new // 3 + 1
+        some = torch.where(torch.rand(new, generator=g) < 0.4, p + 1 + torch.randint(0, 4, (new,), generator=g), p - 1)
+        for name, lo in (("tail", tail), ("middle", middle), ("front", front), ("some", some)):
+            d = ref.make_batch(new, [kv, 40], [new, 1], Hq, Hkv, D, ps, device="cuda")
+            j = torch.arange(kv)
+            seen = ((j >= lo[:, None]) & (j <= p[:, None])).any(0)
+            seen[0] |= anchor
+            hidden = j[~seen]
+            for pages in (d["k_pages"], d["v_pages"]):
+                pages[0, d["table"][0].cpu()[hidden // ps].long().cuda(), :, (hidden % ps).cuda()] = bad
+            key_lo = torch.cat([lo, torch.zeros(1, dtype=torch.long)]).to(torch.int32).cuda()
+            o, _ = _attend(aa, d, ps, Hkv, D, tag=f"{name} {held}", key_lo=key_lo, anchor=anchor)
+            assert torch.isfinite(o.float()).all()
+
+
 @pytest.mark.parametrize("logit", [2e4, 5e4, -2e4, -5e4])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("new,kv", [(1, 500), (1, 20000), (120, 500), (120, 3500)])
