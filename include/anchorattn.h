@@ -538,7 +538,8 @@ aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const v
  *    sequence with more is still computed, only slower.
  *  - key_lo: device int32 [T] or NULL (0 for every row).
  *  - softmax_scale <= 0 selects 1/sqrt(D).
- *  - o [T, q_heads, D] bf16; lse [q_heads, T] fp32 or NULL; neither in the pool.
+ *  - o [T, q_heads, D] bf16; lse [q_heads, T] fp32 or NULL. They and the workspace's
+ *    bytes that the call uses overlap neither one another, nor an input or the pool.
  *  - workspace: aa_cache_attend_workspace_bytes() bytes, 256-byte aligned,
  *    contents ignored; calls that may overlap need one each.
  *  - num_seqs * Hkv < 2^27; q_heads * total_tokens < 2^31. */

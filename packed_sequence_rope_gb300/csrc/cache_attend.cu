@@ -65,16 +65,31 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   if (!o || !aligned16(o)) return fail(AA_ERR_INVALID_ARG, "o must be a 16-byte aligned device pointer");
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(key_lo) & 3u))
     return fail(AA_ERR_INVALID_ARG, "lse and key_lo must be 4-byte aligned device pointers");
-  if (overlap(o, (size_t)T * q_heads * D * 2, q, rows_span(T, q_stride, q_heads, D)))
-    return fail(AA_ERR_INVALID_ARG, "o overlaps q");
-  if ((st = check_outside_pool(c, "o", o, (size_t)T * q_heads * D * 2)) != AA_OK ||
-      (lse && (st = check_outside_pool(c, "lse", lse, (size_t)T * q_heads * 4)) != AA_OK))
-    return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(AA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
-  if (workspace_bytes <
-      aa_cache_attend_workspace_bytes(c, batch->num_seqs, T, max_q, batch->table_width, q_heads))
+  const size_t used = aa_cache_attend_workspace_bytes(c, batch->num_seqs, T, max_q, batch->table_width, q_heads);
+  if (workspace_bytes < used)
     return fail(AA_ERR_INVALID_ARG, "workspace is smaller than aa_cache_attend_workspace_bytes()");
+  // what the call writes lies apart: the kernels' index ranges come from the workspace
+  const struct {
+    const char* name;
+    const void* at;
+    size_t bytes;
+  } written[] = {{"o", o, (size_t)T * q_heads * D * 2}, {"lse", lse, (size_t)T * q_heads * 4}, {"the workspace", workspace, used > 256 ? used : 0}},
+    read[] = {{"q", q, rows_span(T, q_stride, q_heads, D)},
+              {"key_lo", key_lo, (size_t)T * 4},
+              {"page_table", batch->page_table, (size_t)batch->num_seqs * batch->table_width * 4},
+              {"cu_q", batch->cu_q, ((size_t)batch->num_seqs + 1) * 4},
+              {"kv_len", batch->kv_len, (size_t)batch->num_seqs * 4}};
+  for (const auto& x : written) {
+    if (!x.at || !x.bytes) continue;
+    if ((st = check_outside_pool(c, x.name, x.at, x.bytes)) != AA_OK) return st;
+    auto apart = [&](const auto& y) { return !y.at || !y.bytes || &y == &x || !overlap(x.at, x.bytes, y.at, y.bytes); };
+    for (const auto& y : written)
+      if (!apart(y)) return fail(AA_ERR_INVALID_ARG, std::string(x.name) + " overlaps " + y.name);
+    for (const auto& y : read)
+      if (!apart(y)) return fail(AA_ERR_INVALID_ARG, std::string(x.name) + " overlaps " + y.name);
+  }
   AttendParams P;
   P.batch = batch_params(c, batch);
   P.q = static_cast<const __nv_bfloat16*>(q);

@@ -635,6 +635,46 @@ def test_results_in_the_pool_are_refused(aa):
         c.check_device_error()
 
 
+def test_results_that_overlap_are_refused(aa):
+    """o, lse and the part of the workspace that is used: apart from one another, from q and key_lo, and from the pool.
+    Nothing is launched."""
+    T, Hq, D = 100, 4, 64
+    d = ref.make_batch(2, [1300], [T], Hq, 2, D, 16, device="cuda")
+    with _cache(aa, d, 16, 2, D) as c:
+        W = d["table"].shape[1]
+        need = c.workspace_bytes(1, T, T, W, Hq)
+        arena = torch.full((need + (1 << 20),), 7, dtype=torch.uint8, device="cuda")
+        o_bytes, lse_bytes = T * Hq * D * 2, T * Hq * 4
+        o_at = lambda at: arena[at:at + o_bytes].view(torch.bfloat16).view(T, Hq, D)
+        lse_at = lambda at: arena[at:at + lse_bytes].view(torch.float32).view(Hq, T)
+        lo_at = lambda at: arena[at:at + 4 * T].view(torch.int32)
+        before, pools = arena.clone(), [p.clone() for p in (c.k_pages, c.v_pages)]
+        good = dict(q=d["q"], page_table=d["table"], cu_q=d["cu"], kv_len=d["kv"], max_q=T)
+        tail = need // 256 * 256 + 256
+        q = o_at(tail)
+        for change in (dict(out=o_at(0), lse=lse_at(256)), dict(out=o_at(0), lse=lse_at(o_bytes - 16)),
+                       dict(out=o_at(0), workspace=arena), dict(out=o_at(need - 256), workspace=arena),
+                       dict(lse=lse_at(need - 256), workspace=arena), dict(lse=lse_at(tail), q=q),
+                       dict(q=o_at(need - 256), workspace=arena), dict(key_lo=lo_at(need - 256), workspace=arena),
+                       dict(key_lo=lo_at(tail), lse=lse_at(tail)), dict(key_lo=lo_at(tail), out=o_at(tail)),
+                       dict(cu_q=lo_at(tail)[:2], lse=lse_at(tail)), dict(kv_len=lo_at(tail)[:1], out=o_at(tail)),
+                       dict(page_table=lo_at(need - 256)[:W][None], workspace=arena)):
+            with pytest.raises(aa.AAError, match="overlap"):
+                c.attend(**(good | change))
+        L, b = aa.lib(), aa.binding.AACacheBatch(d["table"].data_ptr(), d["cu"].data_ptr(), d["kv"].data_ptr(), 1, W, T, 0)
+        out = torch.zeros_like(d["q"])
+        for at in (c.k_pages.data_ptr(), c.v_pages.data_ptr() - need + 256):  # its first, its last bytes in the pool
+            st = L.aa_cache_attend(c._h, ctypes.addressof(b), d["q"].data_ptr(), Hq * D, Hq, T, None, 0, 0.0, out.data_ptr(),
+                                   None, at, need, None)
+            assert st == 1 and "overlap" in L.aa_last_error().decode()
+        torch.cuda.synchronize()
+        assert torch.equal(arena, before) and torch.equal(c.k_pages, pools[0]) and torch.equal(c.v_pages, pools[1])
+        # behind the bytes that the call needs an arena may hold the results
+        o, lse = c.attend(**good, out=o_at(tail), lse=lse_at(tail + o_bytes), workspace=arena, return_lse=True)
+        c.check_device_error()
+        ref.check_attend(o, lse, ref.attend(d["q"], *pools, d["table"], d["cu"], d["kv"]))
+
+
 # ------------------------------------------------------------------ the run of them together
 def test_serving_run_against_the_packed_forward(aa):
     """A packed sequence of documents is prefilled in chunks and then continued token by token through the cache, with
