@@ -548,9 +548,11 @@ aa_status aa_cache_attend(aa_cache_t cache, const aa_cache_batch* batch, const v
                           void* workspace, size_t workspace_bytes, aa_stream_t stream);
 
 /* Bytes of device scratch aa_cache_attend needs for a batch of these sizes
- * (partial results of keys that are split among CTAs): some 20 to 80 MB, nearly
- * independent of the batch, or 256 bytes where nothing is split. A smaller batch
- * may need more. 0 for invalid sizes. */
+ * (partial results of keys that are split among CTAs). Chunks: 20 MB at D = 64, 40 at
+ * 128, and 32 bytes per sequence and per 256 rows of a kv head more. Few new tokens
+ * over long contexts: the results of up to 76 splits, 4 * D + 8 bytes per row and split.
+ * 256 bytes where nothing is split. A smaller batch may need more. 0 for invalid
+ * sizes. */
 size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
                                        int32_t table_width, int32_t q_heads);
 

@@ -42,7 +42,7 @@ extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs
   if (total_tokens >= (1 << 30) || num_seqs > (1 << 20) || (int64_t)table_width * c->cfg.page_size >= (1ll << 30)) return 0;
   if (takes_short(c, num_seqs, max_q, table_width, q_heads / Hkv))
     return short_workspace_bytes(c, num_seqs, total_tokens, max_q, table_width, q_heads / Hkv);
-  return chunk_workspace_bytes(c, num_seqs, total_tokens, q_heads / Hkv);
+  return chunk_workspace_bytes(c, num_seqs, total_tokens, table_width, q_heads / Hkv);
 }
 
 extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, const void* q, int64_t q_stride,

@@ -17,7 +17,7 @@
 //   chunk_join_kernel     joins the partial results of each cut unit, in order
 // The second and third are launched as programmatic dependents, so that their
 // start-up overlaps the kernel before them. Where the page tables hold few keys
-// a unit is short, and the second kernel alone takes whole units.
+// a unit is short, and the second kernel alone takes whole units, without a workspace.
 //
 // Roles in attend_chunk_kernel (640 threads):
 //   warp 0      finds the CTA's next piece of work and copies its query tiles and
@@ -880,6 +880,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) chunk_join_kernel(c
 
 // ---------------------------------------------------------------- launches
 int ctas_for(const aa_cache_s* c) { return std::min(c->num_sms, kMaxCtas); }
+bool whole_units(int table_width, int page_shift) { return ((int64_t)table_width << page_shift) <= kWholeKeys; }
 int slots_for(int tokens, int seqs, int tile_tokens) { return tokens / (2 * tile_tokens) + seqs; }
 
 template <int HD>
@@ -889,19 +890,26 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   C.a = P;
   C.tile_tokens = 128 / P.group;
   C.slots = slots_for(b.T, b.B, C.tile_tokens);
-  C.whole_units = ((int64_t)b.W << P.page_shift) <= kWholeKeys;
+  C.whole_units = whole_units(b.W, P.page_shift);
   const int ctas = ctas_for(c);
   C.ctas = ctas;
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  C.part_o = reinterpret_cast<float4*>(w);
-  w += align256((size_t)ctas * 4 * 128 * HD * 4);
-  C.part_ml = reinterpret_cast<float2*>(w);
-  w += align256((size_t)ctas * 4 * 128 * 8);
-  C.cuts = reinterpret_cast<Cut*>(w);
-  w += align256((size_t)ctas * sizeof(Cut));
-  C.units = reinterpret_cast<Unit*>(w);
-  w += align256((size_t)C.slots * sizeof(Unit));
-  C.tiles_end = reinterpret_cast<int64_t*>(w);
+  C.tiles_end = nullptr;
+  C.units = nullptr;
+  C.part_o = nullptr;
+  C.part_ml = nullptr;
+  C.cuts = nullptr;
+  if (!C.whole_units) {
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    C.part_o = reinterpret_cast<float4*>(w);
+    w += align256((size_t)ctas * 4 * 128 * HD * 4);
+    C.part_ml = reinterpret_cast<float2*>(w);
+    w += align256((size_t)ctas * 4 * 128 * 8);
+    C.cuts = reinterpret_cast<Cut*>(w);
+    w += align256((size_t)ctas * sizeof(Cut));
+    C.units = reinterpret_cast<Unit*>(w);
+    w += align256((size_t)C.slots * sizeof(Unit));
+    C.tiles_end = reinterpret_cast<int64_t*>(w);
+  }
   CUtensorMap tq;
   aa_status st = make_query_map(&tq, P.q, b.T, P.q_stride, b.Hkv, P.group, HD, C.tile_tokens);
   if (st != AA_OK) return st;
@@ -931,7 +939,8 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
 
 }  // namespace
 
-size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int group) {
+size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int table_width, int group) {
+  if (whole_units(table_width, __builtin_ctz((unsigned)c->cfg.page_size))) return 256;  // nothing is kept
   const size_t slots = slots_for(total_tokens, num_seqs, 128 / group), ctas = ctas_for(c);
   return align256(ctas * 4 * 128 * c->cfg.head_dim * 4) + align256(ctas * 4 * 128 * 8) + align256(ctas * sizeof(Cut)) +
          align256(slots * sizeof(Unit)) + align256((slots + 1) * 8);

@@ -325,6 +325,26 @@ def test_strides_layers_and_rows_behind_the_batch(aa):
             c.check_device_error()
 
 
+def test_calls_of_whole_units_need_no_workspace(aa):
+    """Tables of at most 768 keys: a unit's keys are never split, so there is nothing to keep; above, there is."""
+    for ps in (16, 64, 128):
+        W = 768 // ps
+        d = ref.make_batch(ps, [700, 300, 90], [90, 40, 90], 8, 2, 128, ps, device="cuda", extra_width=0)
+        table = torch.nn.functional.pad(d["table"], (0, W - d["table"].shape[1]), value=-1)
+        with _cache(aa, d, ps, 2, 128) as c:
+            assert c.workspace_bytes(3, d["T"], 90, W, 8) == 256
+            assert c.workspace_bytes(3, d["T"], 90, W + 1, 8) > 1 << 20
+            work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+            got = c.attend(d["q"], table, d["cu"], d["kv"], 90, workspace=work, return_lse=True)
+            c.check_device_error()
+            assert (work == 0).all()
+            wide = torch.nn.functional.pad(table, (0, 1), value=-1)
+            with pytest.raises(aa.AAError, match="workspace"):
+                c.attend(d["q"], wide, d["cu"], d["kv"], 90, workspace=work)
+        want = ref.attend(d["q"], d["k_pages"], d["v_pages"], d["table"], d["cu"], d["kv"])
+        ref.check_attend(*got, want)
+
+
 def test_batches_of_nothing(aa):
     d = ref.make_batch(1, [5, 0], [0, 0], 2, 1, 64, 16, pad=3, device="cuda")
     out = torch.full_like(d["q"], 7.0)
