@@ -23,7 +23,7 @@ __all__ = ["RopeAxes", "rope_axes"]
 
 
 class RopeAxes:
-    """A multi-axis rotation: which axis and frequency each pair has. Holds no device memory.
+    """A multi-axis rotation: which axis and frequency each pair has. Holds no device memory; may be copied and pickled.
 
     sections: pairs per axis, adding up to head_dim / 2; laid one after the other, or, with interleaved=True, dealt
     to the axes in turn until each has its count. axis_of_pair gives the map itself instead. theta: [head_dim / 2]
@@ -67,7 +67,11 @@ class RopeAxes:
         _check(lib().aa_rope_axes_init(ctypes.addressof(self._c), head_dim, self.num_axes, self.layout,
                                        (ctypes.c_int32 * max(half, 1))(*axis_of_pair),
                                        (ctypes.c_double * max(half, 1))(*[float(x) for x in theta])))
-        self._at = ctypes.addressof(self._c)
+
+    @property
+    def _at(self):
+        """The table's address, for the native calls: asked of _c at each of them, since a copy has a _c of its own."""
+        return ctypes.addressof(self._c)
 
     def apply(self, pos, q, k=None, inverse=False, out_q=None, out_k=None, stream=None):
         """Rotate q [T, Hq, D] (and k [T, Hk, D]) by pos, int32 [axes, T]; inverse=True turns back. Token strides of

@@ -231,6 +231,24 @@ def test_rope_axes_sections_and_fixed_point_angles(aa):
             assert abs(d - round(d)) * 2 * np.pi < 2.0 ** -20, (p, pos)
 
 
+def test_copies_of_a_rotation_are_their_own(aa):
+    """A copied, pickled or unpickled RopeAxes has a table of its own, which outlives the original's."""
+    import copy
+    import gc
+    import pickle
+    make = lambda: aa.RopeAxes(128, sections=(16, 24, 24), base=5e6, layout=aa.ROPE_HALF)
+    original = make()
+    want = bytes(original._c)
+    copies = [copy.copy(original), copy.deepcopy(original), pickle.loads(pickle.dumps(original)), copy.deepcopy({"r": original})["r"]]
+    del original
+    gc.collect()
+    others = [aa.RopeAxes(64, sections=(32,), base=1e4) for _ in range(64)]  # what reuses freed memory
+    for r in copies:
+        assert r._at == ctypes.addressof(r._c) and bytes(r._c) == want
+        assert (r.head_dim, r.num_axes, r.layout, r.axis_of_pair) == (128, 3, aa.ROPE_HALF, make().axis_of_pair)
+    assert len({r._at for r in copies[1:] + others}) == 3 + 64
+
+
 def test_rope_axes_apply_refusals(aa):
     r, A = aa.RopeAxes(64, sections=(16, 16)), 1 << 20  # addresses that are never read: refused first
     ok = dict(T=4, q=A, qs=128, qo=A * 2, hq=2, k=A * 3, ks=128, ko=A * 4, hk=2, pos=A * 5)
