@@ -400,7 +400,7 @@ aa_status aa_rope_axes_init(aa_rope_axes* rope, int32_t head_dim, int32_t num_ax
  *    token are contiguous. fp32 arithmetic, rounded once to bf16.
  *  - k may be NULL with k_heads = 0. q_out = q (k_out = k) rotates in place
  *    if that input is contiguous; outputs overlap nothing else.
- *  - total_tokens = 0 is an empty call. */
+ *  - total_tokens = 0 is an empty call; its pointers are not looked at. */
 aa_status aa_rope_axes_apply(const aa_rope_axes* rope, const int32_t* pos, int32_t total_tokens, const void* q,
                              int64_t q_stride, void* q_out, int32_t q_heads, const void* k, int64_t k_stride,
                              void* k_out, int32_t k_heads, int32_t inverse, aa_stream_t stream);

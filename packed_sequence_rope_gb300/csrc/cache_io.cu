@@ -190,10 +190,10 @@ extern "C" aa_status aa_cache_append(aa_cache_t c, const aa_cache_batch* batch, 
   if (rope && !axes_valid(rope)) return fail(AA_ERR_INVALID_ARG, "rope must be filled by aa_rope_axes_init");
   const int D = c->cfg.head_dim, Hkv = c->cfg.num_kv_heads, T = batch->total_tokens;
   if (rope && rope->head_dim != D) return fail(AA_ERR_INVALID_ARG, "rope's head_dim is not the cache's");
+  if (T == 0) return AA_OK;  // tensors without elements have no address
   if (q && !rope) return fail(AA_ERR_INVALID_ARG, "q is rotated: it needs rope");
   if (q ? q_heads < 1 || q_heads > 65536 : q_heads != 0)
     return fail(AA_ERR_INVALID_ARG, "q_heads must be >= 1 with q (at most 65536) and 0 without");
-  if (T == 0) return AA_OK;
   if ((rope != nullptr) != (pos != nullptr)) return fail(AA_ERR_INVALID_ARG, "give both rope and pos or neither");
   if (reinterpret_cast<uintptr_t>(pos) & 3u) return fail(AA_ERR_INVALID_ARG, "pos must be a device pointer to int32");
   if ((st = check_rows("k", k, k_stride, Hkv, D)) != AA_OK || (st = check_rows("v", v, v_stride, Hkv, D)) != AA_OK ||

@@ -139,8 +139,8 @@ extern "C" aa_status aa_rope_axes_apply(const aa_rope_axes* r, const int32_t* po
   if (T < 0 || T >= (1 << 30)) return fail(AA_ERR_INVALID_ARG, "total_tokens must be in [0, 2^30)");
   if (q_heads < 1 || k_heads < 0 || q_heads > 65536 || k_heads > 65536)
     return fail(AA_ERR_INVALID_ARG, "need q_heads >= 1 and k_heads >= 0 (at most 65536)");
+  if (T == 0) return AA_OK;  // tensors without elements have no address
   if ((k_heads == 0) != (k == nullptr)) return fail(AA_ERR_INVALID_ARG, "k must be NULL exactly when k_heads is 0");
-  if (T == 0) return AA_OK;
   if (!pos || (reinterpret_cast<uintptr_t>(pos) & 3u)) return fail(AA_ERR_INVALID_ARG, "pos must be a device pointer to int32");
   const int D = r->head_dim;
   aa_status st = check_turned("q", q, q_stride, q_out, q_heads, D, T);

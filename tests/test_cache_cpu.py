@@ -269,6 +269,15 @@ def test_rope_axes_apply_refusals(aa):
     assert aa.lib().aa_rope_axes_apply(r._at, None, 0, None, 0, None, 2, None, 0, None, 0, 0, None) == 0
 
 
+def test_empty_rotation_with_keys_is_accepted(aa):
+    """No tokens: tensors without elements have no address, and none is read."""
+    r = aa.RopeAxes(64, sections=(16, 16))
+    for k_heads in (0, 2):
+        assert aa.lib().aa_rope_axes_apply(r._at, None, 0, None, 128, None, 2, None, 128, None, k_heads, 0, None) == 0
+    for q_heads, k_heads in ((0, 2), (2, -1), (65537, 0)):  # sizes are still looked at
+        assert aa.lib().aa_rope_axes_apply(r._at, None, 0, None, 128, None, q_heads, None, 128, None, k_heads, 0, None) == 1
+
+
 def test_device_calls_refuse_a_host_only_cache(aa):
     with _cache(aa) as c:
         L = aa.lib()

@@ -359,6 +359,15 @@ def test_batches_of_nothing(aa):
         assert torch.equal(before, d["k_pages"])
 
 
+def test_append_of_no_tokens_with_queries(aa):
+    d = ref.make_batch(1, [5, 0], [0, 0], 2, 1, 64, 16, pad=3, device="cuda")
+    rope, pos = aa.RopeAxes(64, (32,)), torch.zeros(1, 0, dtype=torch.int32, device="cuda")
+    with _cache(aa, d, 16, 1, 64) as c:
+        q = c.append(d["k"][:0], d["v"][:0], d["table"], d["cu"], d["kv"], rope=rope, pos=pos, q=d["q"][:0])
+        assert q.shape == (0, 2, 64)
+        c.check_device_error()
+
+
 def test_runs_agree_bit_for_bit_and_across_streams(aa):
     for new, kv in ((1, [3000, 17]), (5, [900, 40]), (160, [2000, 160])):
         d = ref.make_batch(4, kv, [new, new], 8, 2, 128, 64, device="cuda")

@@ -211,6 +211,17 @@ def test_stream_graph_and_refusals(aa):
             bad()
 
 
+def test_empty_calls_with_keys(aa):
+    rope = aa.RopeAxes(128, (32, 32), base=1e4)
+    q, k, pos = _data(4, 4, 2, 128, 2)
+    yq, yk = rope.apply(pos[:, :0].contiguous(), q[:0], k[:0])
+    assert yq.shape == (0, 4, 128) and yk.shape == (0, 2, 128)
+    q0, k0 = q[:0].clone().requires_grad_(True), k[:0].clone().requires_grad_(True)
+    yq, yk = aa.rope_axes(rope, pos[:, :0].contiguous(), q0, k0)
+    (yq.sum() + yk.sum()).backward()
+    assert q0.grad.shape == (0, 4, 128) and k0.grad.shape == (0, 2, 128)
+
+
 def test_training_step_in_a_graph(aa):
     """Forward and gradient captured after a warm-up on a side stream, whose autograd graph is gone by then (PyTorch ties
     the leaves of a living one to the stream that it was made on, and refuses the capture)."""
