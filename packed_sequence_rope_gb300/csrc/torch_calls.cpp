@@ -94,10 +94,16 @@ Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
 
+// A given result tensor is checked here; written() tells autograd of it once it is.
 Tensor out_or_new(const Tensor* out, const char* name, at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   if (!out) return make(shape, type, dev);
   check_exact(*out, name, shape, type, dev);
+  TORCH_CHECK_VALUE(!(out->requires_grad() && at::GradMode::is_enabled()), name,
+                    " requires grad: the result written into it would carry none");
   return *out;
+}
+void written(const Tensor* out) {
+  if (out && !out->is_inference()) out->unsafeGetTensorImpl()->bump_version();
 }
 
 int64_t as_int(PyObject* o) {
@@ -236,6 +242,8 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Rotated r = rotate(as_handle<const aa_rope_axes*>(a[0]), need(a[1], "pos"), need(a[2], "q"), given(a[3], "k"), as_bool(a[4]),
                      given(a[5], "out_q"), given(a[6], "out_k"), a[7]);
   if (r.status) return PyLong_FromLong(r.status);
+  written(given(a[5], "out_q"));
+  written(given(a[6], "out_k"));
   return wrap(std::move(r.q), std::move(r.k));
   END_HANDLE_TH_ERRORS
 }
@@ -330,6 +338,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            q ? rq->stride : 0, q ? yq.mutable_data_ptr() : nullptr, q ? (int32_t)q->size(1) : 0, on.s);
   });
   if (status) return PyLong_FromLong(status);
+  written(out_q);
   if (q) return THPVariable_Wrap(std::move(yq));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
@@ -379,6 +388,8 @@ PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            (size_t)work.numel(), on.s);
   });
   if (status) return PyLong_FromLong(status);
+  written(out);
+  written(lse_in);
   return wrap(std::move(o), return_lse ? std::move(lse) : Tensor());
   END_HANDLE_TH_ERRORS
 }

@@ -645,6 +645,28 @@ def test_refusals(aa):
         assert (out == 7).all()
 
 
+def test_results_written_into_given_tensors_are_seen_by_autograd(aa):
+    d = ref.make_batch(1, [20, 30], [2, 1], 4, 2, 64, 16, device="cuda")
+    rope, pos = aa.RopeAxes(64, (32,)), torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    with _cache(aa, d, 16, 2, 64) as c:
+        append = lambda **kw: c.append(d["k"], d["v"], d["table"], d["cu"], d["kv"], rope=rope, pos=pos, q=d["q"], **kw)
+        attend = lambda **kw: c.attend(d["q"], d["table"], d["cu"], d["kv"], 2, **kw)
+        lse = torch.zeros(4, 3, device="cuda")
+        for call, out in ((lambda x: append(out_q=x), torch.zeros_like(d["q"])), (lambda x: attend(out=x), torch.zeros_like(d["q"])),
+                          (lambda x: attend(lse=x), lse)):
+            leaf = out.requires_grad_(True)
+            a = leaf * 1
+            y = a * a  # saves a
+            for x in (leaf, a):
+                with pytest.raises(ValueError, match="grad"):
+                    call(x)
+            with torch.no_grad():
+                call(a)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.sum().backward()
+        c.check_device_error()
+
+
 def test_results_in_the_pool_are_refused(aa):
     d = ref.make_batch(2, [20, 30], [2, 1], 4, 2, 64, 16, device="cuda")
     rope, pos = aa.RopeAxes(64, (32,)), torch.zeros(1, 3, dtype=torch.int32, device="cuda")

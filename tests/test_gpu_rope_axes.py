@@ -222,6 +222,27 @@ def test_empty_calls_with_keys(aa):
     assert q0.grad.shape == (0, 4, 128) and k0.grad.shape == (0, 2, 128)
 
 
+def test_results_written_into_given_tensors_are_seen_by_autograd(aa):
+    """A result tensor is a written tensor: a graph that saved its old values says so, and one that would carry a wrong
+    gradient is refused."""
+    rope = aa.RopeAxes(64, (32,), base=1e4)
+    x, _, pos = _data(9, 2, 1, 64, 1)
+    x.requires_grad_(True)
+    a = x * 2
+    y = a * a  # saves a
+    for out in (a, x):
+        with pytest.raises(ValueError, match="grad"):
+            rope.apply(pos, a.detach().clone(), out_q=out)
+    y.float().sum().backward(retain_graph=True)  # refused calls have written nothing
+    with torch.no_grad():
+        rope.apply(pos, a, out_q=a)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()
+    with torch.inference_mode():
+        z = torch.zeros_like(a)
+    assert torch.equal(rope.apply(pos, a.detach(), out_q=z), rope.apply(pos, a.detach()))
+
+
 def test_training_step_in_a_graph(aa):
     """Forward and gradient captured after a warm-up on a side stream, whose autograd graph is gone by then (PyTorch ties
     the leaves of a living one to the stream that it was made on, and refuses the capture)."""
