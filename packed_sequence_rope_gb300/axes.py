@@ -67,11 +67,15 @@ class RopeAxes:
         _check(lib().aa_rope_axes_init(ctypes.addressof(self._c), head_dim, self.num_axes, self.layout,
                                        (ctypes.c_int32 * max(half, 1))(*axis_of_pair),
                                        (ctypes.c_double * max(half, 1))(*[float(x) for x in theta])))
+        self._at = ctypes.addressof(self._c)
 
-    @property
-    def _at(self):
-        """The table's address, for the native calls: asked of _c at each of them, since a copy has a _c of its own."""
-        return ctypes.addressof(self._c)
+    # _at, the table's address, belongs to this object's _c: a copy or an unpickled object takes its own
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_at"}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._at = ctypes.addressof(self._c)
 
     def apply(self, pos, q, k=None, inverse=False, out_q=None, out_k=None, stream=None):
         """Rotate q [T, Hq, D] (and k [T, Hk, D]) by pos, int32 [axes, T]; inverse=True turns back. Token strides of
