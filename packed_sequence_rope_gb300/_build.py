@@ -17,6 +17,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libanchorattn.so")
 CALLS = os.path.join(PKG, "_calls.so")
 CALLS_SOURCE = "torch_calls.cpp"
+CALLS_FOR = os.path.join(BUILD, "calls_for.txt")  # what _calls.so was compiled for
 SOURCES = ["plan.cpp", "rope.cu", "fwd.cu", "bwd.cu", "bwd_static.cu", "shift_diag.cu", "segments.cu",
            "rope_axes.cu", "cache.cpp", "cache_io.cu", "cache_attend.cu",
            "cache_attend_short.cu", "cache_attend_chunk.cu"]
@@ -71,9 +72,17 @@ def _link(cmd, target):
     os.replace(target + ".tmp", target)
 
 
+def _calls_for() -> str:
+    with open(os.path.join(_torch(), "version.py")) as f:
+        return f"{sys.version}\n{f.read()}"
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS) or not os.path.exists(CALLS_FOR):
         return True
+    with open(CALLS_FOR) as f:
+        if f.read() != _calls_for():  # another torch or Python since
+            return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "anchorattn.h")]
     return any(os.path.getmtime(d) > t for d in deps)
@@ -89,8 +98,12 @@ def build(force: bool = False, verbose: bool = True) -> str:
         calls = calls.result()
     _link([_nvcc(), "-shared", "-cudart", "static", "-o", LIB + ".tmp"] + objs + ["-lpthread", "-ldl", "-lrt"], LIB)
     lib = os.path.join(_torch(), "lib")
+    if os.path.exists(CALLS_FOR):
+        os.remove(CALLS_FOR)
     _link(["g++", "-shared", "-o", CALLS + ".tmp", calls, "-L" + PKG, "-l:" + os.path.basename(LIB), "-L" + lib,
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], CALLS)
+    with open(CALLS_FOR, "w") as f:
+        f.write(_calls_for())
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB

@@ -2,6 +2,7 @@
 after growing, shrinking, forking, compacting and freeing, against a plain model of it; arguments that must be
 refused before anything is launched."""
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -287,3 +288,17 @@ def test_device_calls_refuse_a_host_only_cache(aa):
             assert st == 1 and "host_only" in L.aa_last_error().decode()
         assert L.aa_cache_attend_workspace_bytes(None, 1, 1, 1, 1, 1) == 0
         assert L.aa_cache_attend_workspace_bytes(c._h, 0, 1, 1, 1, 2) == 0
+
+
+def test_native_calls_are_rebuilt_for_another_torch(aa, tmp_path, monkeypatch):
+    """_calls.so fits the torch that it was compiled for: with another one the build is stale."""
+    from packed_sequence_rope_gb300 import _build
+    assert not _build._stale()
+    real = _build._torch()
+    with open(os.path.join(real, "version.py")) as f:
+        text = f.read()
+    (tmp_path / "version.py").write_text(text + "\n# another build\n")
+    with monkeypatch.context() as m:
+        m.setattr(_build, "_torch", lambda: str(tmp_path))
+        assert _build._stale()
+    assert not _build._stale()
