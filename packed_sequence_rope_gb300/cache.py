@@ -94,6 +94,9 @@ class PagedCache:
         except Exception:
             pass
 
+    def __reduce__(self):  # copy.copy and copy.deepcopy ask it too
+        raise TypeError("a PagedCache owns its handle: it cannot be copied or pickled")
+
     def __enter__(self):
         return self
 

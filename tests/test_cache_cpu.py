@@ -187,6 +187,18 @@ def test_bookkeeping_refusals(aa, call, msg):
         assert [_pages(c, s) for s in range(4)] == before
 
 
+def test_a_cache_is_not_copied(aa):
+    """Two objects with one handle would free it twice."""
+    import copy
+    import pickle
+    with _cache(aa) as c:
+        c.resize([0], [20])
+        for call in (copy.copy, copy.deepcopy, pickle.dumps):
+            with pytest.raises(TypeError, match="PagedCache"):
+                call(c)
+        assert _pages(c, 0) == [0, 1]
+
+
 def test_cache_without_sequences_refuses_bookkeeping(aa):
     with _cache(aa, seqs=0) as c:
         for call in (lambda: c.resize([0], [1]), lambda: c.fork(0, 0), c.compact):
