@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
       for (int e = 0; e < 2; ++e) {
         const int row = row0 + 8 * e, tok = row / P.group;
         const bool on = row < rows;
-        row_lo[e] = on ? first_key(P, span.q0 + i0 + tok) : 0;
+        row_lo[e] = kLo && on ? first_key(P, span.q0 + i0 + tok) : 0;
         row_hi[e] = on ? p0 + tok : INT_MAX;
         const __nv_bfloat16* q = P.q + (int64_t)(span.q0 + i0 + tok) * P.q_stride +
                                  (int64_t)(g * P.group + row - tok * P.group) * HD + 2 * (lane & 3);
