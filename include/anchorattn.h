@@ -437,7 +437,9 @@ aa_status aa_rope_axes_apply(const aa_rope_axes* rope, const int32_t* pos, int32
  *
  * A page number outside [0, num_pages), or a position outside the table, is
  * never used as an address: the token is skipped (append) or reads as zeros
- * (attend), an error word is set, and aa_cache_check_error() reports it. */
+ * (attend), an error word is set, and aa_cache_check_error() reports it. A
+ * position below 0 (kv_len[b] < n_b) is such an error for append; for attend its
+ * row sees no key, which is none. */
 typedef struct {
   int32_t num_layers;        /* >= 1                                             */
   int32_t num_pages;         /* >= 1; num_layers * num_pages * Hkv * page_size < 2^31 */
@@ -528,7 +530,7 @@ aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const v
  * (the mask of [ARCH §3.4 Anchor]: key_lo is the first token of the query's
  * document; or p - W + 1 for a sliding window):
  *   O_i = sum_j softmax_j(scale * q_i . k_j) v_j,  LSE_i = ln sum_j exp(...).
- * A row that sees no key gives O = 0 and LSE = -inf. Keys that no new token of
+ * A row that sees no key, or whose logits are all -inf, gives O = 0 and LSE = -inf. Keys that no new token of
  * their sequence sees do not reach the result, whatever they hold (NaN,
  * infinities); what a row sees makes it NaN as the formula does, and a value that
  * is not finite may reach the other rows of its sequence in the call too.

@@ -18,8 +18,10 @@ using namespace aa;
 // Few rows: the kernel for them, whose row tile holds kShortRows. Its warps share a
 // 16-row tile's keys at 16 rows, but at 33 to 64 take 16 rows each and all keys,
 // which at D = 128 costs more than HBM does; there the other kernel takes the calls
-// with work for every SM, and those of short contexts. Measured, microseconds of
-// this one / the other, 8 kv heads of 128, group 4:
+// with work for every SM, and those of short contexts. Up to 32 rows stay here over
+// short contexts too, where many sequences would be faster there (first line). 64
+// units and kWholeKeys are where the two met on 152 SMs. Measured, microseconds
+// of this one / the other, 8 kv heads of 128, group 4:
 //   rows, sequences   300 keys     2048        16384
 //   32, 1             10.1 / 10.5  9.6 / 16.7  20.6 / 27.1
 //   32, 42            31.8 / 27.2  81.1 / 89.1 457 / 534
