@@ -530,9 +530,9 @@ aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const v
  * (the mask of [ARCH §3.4 Anchor]: key_lo is the first token of the query's
  * document; or p - W + 1 for a sliding window):
  *   O_i = sum_j softmax_j(scale * q_i . k_j) v_j,  LSE_i = ln sum_j exp(...).
- * A row that sees no key, or whose logits are all -inf, gives O = 0 and LSE = -inf. Keys that no new token of
- * their sequence sees do not reach the result, whatever they hold (NaN,
- * infinities); what a row sees makes it NaN as the formula does, and a value that
+ * A row that sees no key, or whose logits are all -inf, gives O = 0 and LSE = -inf.
+ * Keys that no new token of their sequence sees do not reach the result, whatever
+ * they hold (NaN, infinities); what a row sees makes it NaN as the formula does, and a value that
  * is not finite may reach the other rows of its sequence in the call too.
  *  - q [T, q_heads, D] bf16, ROTATED (q_stride elements from token to token);
  *    q_heads % Hkv == 0, at most 64 query heads per kv head.

@@ -77,7 +77,9 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
     const char* name;
     const void* at;
     size_t bytes;
-  } written[] = {{"o", o, (size_t)T * q_heads * D * 2}, {"lse", lse, (size_t)T * q_heads * 4}, {"the workspace", workspace, used > 256 ? used : 0}},
+  } written[] = {{"o", o, (size_t)T * q_heads * D * 2},
+                 {"lse", lse, (size_t)T * q_heads * 4},
+                 {"the workspace", workspace, used > 256 ? used : 0}},  // 256: none is in use
     read[] = {{"q", q, rows_span(T, q_stride, q_heads, D)},
               {"key_lo", key_lo, (size_t)T * 4},
               {"page_table", batch->page_table, (size_t)batch->num_seqs * batch->table_width * 4},
@@ -86,7 +88,9 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   for (const auto& x : written) {
     if (!x.at || !x.bytes) continue;
     if ((st = check_outside_pool(c, x.name, x.at, x.bytes)) != AA_OK) return st;
-    auto apart = [&](const auto& y) { return !y.at || !y.bytes || &y == &x || !overlap(x.at, x.bytes, y.at, y.bytes); };
+    auto apart = [&](const auto& y) {
+      return !y.at || !y.bytes || &y == &x || !overlap(x.at, x.bytes, y.at, y.bytes);
+    };
     for (const auto& y : written)
       if (!apart(y)) return fail(AA_ERR_INVALID_ARG, std::string(x.name) + " overlaps " + y.name);
     for (const auto& y : read)

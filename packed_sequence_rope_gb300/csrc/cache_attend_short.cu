@@ -461,7 +461,9 @@ cudaError_t launch(const aa_cache_s* c, const AttendParams& P, const ShortShape&
 
 template <int HD, bool kLo>
 cudaError_t launch(const aa_cache_s* c, const AttendParams& P, const ShortShape& f, const ShortParts& S, cudaStream_t s) {
-  return f.rt == 1 ? launch<HD, 1, kLo>(c, P, f, S, s) : f.rt == 2 ? launch<HD, 2, kLo>(c, P, f, S, s) : launch<HD, 4, kLo>(c, P, f, S, s);
+  return f.rt == 1   ? launch<HD, 1, kLo>(c, P, f, S, s)
+         : f.rt == 2 ? launch<HD, 2, kLo>(c, P, f, S, s)
+                     : launch<HD, 4, kLo>(c, P, f, S, s);
 }
 
 }  // namespace
