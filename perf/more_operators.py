@@ -11,7 +11,8 @@ A sequence b has kv_len[b] tokens, the last n_b = cu_q[b + 1] - cu_q[b] of them 
 kv_len[b] - n_b + i. Page tables are random permutations of the pool, as after hours of serving; unused entries hold -1.
 
 8-bit pages: a token's D values of a kv head are e4m3 numbers times 2^e, one e for keys and one for values, stored as
-e + 127: the smallest e in [-100, 120] for which the largest magnitude is at most 448 * 2^e; rounded to the nearest, ties to even.
+e + 127: the smallest e in [-100, 119] for which the largest magnitude is at most 448 * 2^e (119 if there is none); rounded to
+the nearest, ties to even, and to at most 448.
 
 Trees: new token i of a sequence sees the cached tokens from its key_lo on and the new tokens c whose bit is set, bit
 c % 64 of word c // 64 of its row of masks.
@@ -293,8 +294,8 @@ def _turn(x, cos, sin, half):
 def _quantise(x):
     """x fp32 [..., D] as e4m3 numbers and their scales' bytes."""
     m, e = torch.frexp(x.abs().amax(-1))
-    e = (e - 9 + (m > 0.875).int()).clamp(-100, 120)  # 448 = 0.875 * 2^9
-    codes = torch.ldexp(x, -e[..., None].float()).to(torch.float8_e4m3fn)
+    e = (e - 9 + (m > 0.875).int()).clamp(-100, 119)  # 448 = 0.875 * 2^9
+    codes = torch.ldexp(x, -e[..., None].float()).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
     return codes, (e + 127).to(torch.uint8)
 
 
@@ -474,10 +475,10 @@ def _exact_held(x):
     """The values that 8-bit pages hold of x [..., D] in 64 bits: multiples of 2^-9 up to 2^-6, then of 1/8 of the power of two
     below, times the row's scale."""
     top = x.abs().amax(-1, keepdim=True)
-    scale = torch.exp2(torch.clamp(torch.ceil(torch.log2(top / 448.0)), -100, 120))
-    scale = torch.where(top > 448.0 * scale, 2 * scale, scale)  # should the logarithm have rounded across a border
+    scale = torch.exp2(torch.clamp(torch.ceil(torch.log2(top / 448.0)), -100, 119))
+    scale = torch.where((top > 448.0 * scale) & (scale < 2.0 ** 119), 2 * scale, scale)  # should the logarithm have rounded across a border
     scale = torch.where((top <= 224.0 * scale) & (scale > 2.0 ** -100), scale / 2, scale)
-    y = x / scale
+    y = (x / scale).clamp(-448.0, 448.0)
     step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6)))) / 8
     return torch.round(y / step) * step * scale  # ties to even
 
