@@ -414,13 +414,26 @@ aa_status aa_rope_axes_apply(const aa_rope_axes* rope, const int32_t* pos, int32
  * (page_size * D * 2 bytes, what one copy into shared memory takes). Keys are
  * stored ROTATED, so a page needs no positions.
  *
+ * 8-bit pages (aa_cache_create_fp8) hold half of the bytes: k_pages and v_pages are
+ * e4m3 numbers (one byte each), and k_scales and v_scales, [num_layers, num_pages,
+ * Hkv, page_size] bytes, give each token's D values of a head their power of two: the
+ * values are code * 2^(byte - 127). aa_cache_append chooses the smallest exponent in
+ * [-100, 119] that keeps the row's largest magnitude within 448 times it, and rounds
+ * the (rotated) fp32 values once, to the nearest, ties to even: within 2^-4 of the value
+ * or 2^-10 of the power, whichever is more (magnitudes above 448 * 2^119, bf16's
+ * largest 14 %, become that). A row with a value that is not finite gets byte 255 and
+ * is NaN as a whole. Pages that the caller fills have bytes in [1, 254] or 255 for
+ * NaN and no NaN codes (0x7f, 0xff read as +-480). All other calls are the same for
+ * both kinds.
+ *
  * Two halves:
  *  - Bookkeeping on the host (aa_cache_resize, _fork, _compact, _tables,
  *    _stats): which page belongs to which sequence, with a reference count
  *    for each page, so that forked sequences share what they have in common.
  *    The handle is not thread-safe. A caller with its own scheduler leaves
  *    this half alone (max_seqs = 0) and passes its own page tables below.
- *  - Device calls (aa_cache_append, _attend, _copy_pages): stream-ordered,
+ *  - Device calls (aa_cache_append, _read, _attend, _attend_tree, _tree_masks,
+ *    _accept, _copy_pages): stream-ordered,
  *    no allocation, no host synchronisation. Everything that changes from
  *    step to step (page tables, lengths) is read on the device, so a step can
  *    be captured in a CUDA graph once and replayed with new contents.
@@ -456,6 +469,11 @@ typedef struct aa_cache_s* aa_cache_t;
  * (NULL with host_only). The handle belongs to the current device; the device
  * calls below refuse another one. Its contents need no clearing. */
 aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, void* v_pages, aa_cache_t* out);
+
+/* A cache with 8-bit pages (see above): four caller-owned arrays, each 16-byte aligned,
+ * apart from one another, alive as long as the handle (NULL with host_only). */
+aa_status aa_cache_create_fp8(const aa_cache_config* cfg, void* k_pages, void* k_scales, void* v_pages, void* v_scales,
+                              aa_cache_t* out);
 
 /* Free a handle (synchronises the device). NULL is accepted. */
 aa_status aa_cache_destroy(aa_cache_t cache);
@@ -523,6 +541,13 @@ aa_status aa_cache_append(aa_cache_t cache, const aa_cache_batch* batch, const v
                           int64_t v_stride, const aa_rope_axes* rope, const int32_t* pos, const void* q,
                           int64_t q_stride, void* q_out, int32_t q_heads, aa_stream_t stream);
 
+/* What the pages hold of the new tokens, in bf16 (exactly; 8-bit pages decoded):
+ * k, v [T, Hkv, D] contiguous, 16-byte aligned, apart from each other, the batch's
+ * arrays and the pool. The keys are as stored, rotated. A token whose page number or
+ * position is out of range reads as zeros. With kv_len and cu_q of the caller's
+ * choice this reads any run of cached tokens that ends at kv_len. */
+aa_status aa_cache_read(aa_cache_t cache, const aa_cache_batch* batch, void* k, void* v, aa_stream_t stream);
+
 /* Attention of the new tokens over their sequences' cached keys and values
  * (the new ones included: append first). For new token i of sequence b, at
  * position p, and every query head h, over the visible keys
@@ -549,6 +574,42 @@ aa_status aa_cache_attend(aa_cache_t cache, const aa_cache_batch* batch, const v
                           int32_t max_q, const int32_t* key_lo, int32_t anchor, float softmax_scale, void* o, float* lse,
                           void* workspace, size_t workspace_bytes, aa_stream_t stream);
 
+/* Drafted trees. The new tokens of a sequence are a tree of drafted continuations: all
+ * lie behind its `base` = kv_len[b] - n_b cached tokens, token i in row base + i
+ * of the pages, but each follows its parent only. aa_cache_attend_tree is
+ * aa_cache_attend with other visible keys: new token i of sequence b sees the cached
+ * j in [max(key_lo, 0), base), j = 0 if anchor != 0 and base > 0, and new token c of
+ * its sequence if bit c % 64 of word c / 64 of its row of `tree` is set (device
+ * uint64 [T, tree_words], 1 <= tree_words <= 2^14; bits at n_b and above are not looked at, tokens past the
+ * masks' width are not seen). Any mask will do, also one where tokens see later ones.
+ * Where base < 0 the tokens without a position see nothing. The workspace is
+ * aa_cache_attend's. */
+aa_status aa_cache_attend_tree(aa_cache_t cache, const aa_cache_batch* batch, const void* q, int64_t q_stride,
+                               int32_t q_heads, int32_t max_q, const int32_t* key_lo, int32_t anchor, const uint64_t* tree,
+                               int32_t tree_words, float softmax_scale, void* o, float* lse, void* workspace,
+                               size_t workspace_bytes, aa_stream_t stream);
+
+/* Masks and positions of drafted trees: parents (device int32 [T]) gives each new
+ * token's parent as its index among its sequence's new tokens, smaller than its own,
+ * or -1 for one that follows the cached tokens. mask (uint64 [T, tree_words]): the
+ * token's ancestors and itself; pos (int32 [T]): kv_len - n_b + the number of its
+ * ancestors, the position that it is rotated at. A parent out of range counts as -1
+ * and sets the error word. Rows outside [cu_q[0], cu_q[num_seqs]) are left as they were. */
+aa_status aa_cache_tree_masks(aa_cache_t cache, const int32_t* parents, const int32_t* cu_q, const int32_t* kv_len,
+                              int32_t num_seqs, int32_t total_tokens, int32_t tree_words, uint64_t* mask, int32_t* pos,
+                              aa_stream_t stream);
+
+/* Keep the accepted tokens of drafted trees: path (device int32 [num_seqs, path_width])
+ * lists the indices of the kept new tokens of each sequence, ascending, up to the
+ * first negative entry. Their keys and values move up, path[i] to row base + i, in all
+ * layers; what lies behind them is no longer of use: the sequence's length is now
+ * base + the number kept (aa_cache_resize, or a caller's own kv_len). A path that does
+ * not ascend or leaves its sequence's new tokens sets the error word, and nothing of
+ * that sequence moves. batch->layer and total_tokens are not used. The pages written
+ * to are the sequences' own (aa_cache_resize has seen to it). */
+aa_status aa_cache_accept(aa_cache_t cache, const aa_cache_batch* batch, const int32_t* path, int32_t path_width,
+                          aa_stream_t stream);
+
 /* Bytes of device scratch aa_cache_attend needs for a batch of these sizes
  * (partial results of keys that are split among CTAs). Chunks: 20 MB at D = 64, 40 at
  * 128, and 32 bytes per sequence and per 256 rows of a kv head more. Few new tokens
@@ -560,7 +621,7 @@ size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32
 
 /* Synchronise `stream`, read and clear the cache's device error word:
  * AA_ERR_INVALID_ARG if a device call met a page number or a position outside
- * its range since the last check, AA_ERR_TIMEOUT if a bounded device wait ran
+ * its range, a parent or a path of drafted tokens that is none, since the last check, AA_ERR_TIMEOUT if a bounded device wait ran
  * out, AA_OK otherwise. */
 aa_status aa_cache_check_error(aa_cache_t cache, aa_stream_t stream);
 

@@ -28,7 +28,8 @@ EXPORTS = ["aa_plan", "aa_plan_with_theta", "aa_plan_segments", "aa_plan_destroy
            "aa_last_error", "aa_shift_diag_workspace_bytes", "aa_shift_diag", "aa_shard_plan",
            "aa_rope_axes_init", "aa_rope_axes_apply", "aa_cache_create", "aa_cache_destroy", "aa_cache_resize",
            "aa_cache_fork", "aa_cache_compact", "aa_cache_tables", "aa_cache_stats", "aa_cache_copy_pages",
-           "aa_cache_append", "aa_cache_attend", "aa_cache_attend_workspace_bytes", "aa_cache_check_error"]
+           "aa_cache_append", "aa_cache_attend", "aa_cache_attend_workspace_bytes", "aa_cache_check_error",
+           "aa_cache_create_fp8", "aa_cache_read", "aa_cache_attend_tree", "aa_cache_tree_masks", "aa_cache_accept"]
 
 
 class AAShardPiece(ctypes.Structure):
@@ -111,6 +112,7 @@ def lib():
             "aa_rope_axes_init": ([vp, i32, i32, i32, i32p, ctypes.POINTER(ctypes.c_double)], ctypes.c_int),
             "aa_rope_axes_apply": ([vp, vp, i32, vp, i64, vp, i32, vp, i64, vp, i32, i32, vp], ctypes.c_int),
             "aa_cache_create": ([vp, vp, vp, ctypes.POINTER(vp)], ctypes.c_int),
+            "aa_cache_create_fp8": ([vp, vp, vp, vp, vp, ctypes.POINTER(vp)], ctypes.c_int),
             "aa_cache_destroy": ([vp], ctypes.c_int),
             "aa_cache_resize": ([vp, i32p, i32p, i32, vp], ctypes.c_int),
             "aa_cache_fork": ([vp, i32, i32], ctypes.c_int),
@@ -123,6 +125,11 @@ def lib():
                                 ctypes.c_int),
             "aa_cache_attend_workspace_bytes": ([vp, i32, i32, i32, i32, i32], ctypes.c_size_t),
             "aa_cache_check_error": ([vp, vp], ctypes.c_int),
+            "aa_cache_read": ([vp, vp, vp, vp, vp], ctypes.c_int),
+            "aa_cache_attend_tree": ([vp, vp, vp, i64, i32, i32, vp, i32, vp, i32, ctypes.c_float, vp, vp, vp,
+                                      ctypes.c_size_t, vp], ctypes.c_int),
+            "aa_cache_tree_masks": ([vp, vp, vp, vp, i32, i32, i32, vp, vp, vp], ctypes.c_int),
+            "aa_cache_accept": ([vp, vp, vp, i32, vp], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)

@@ -8,6 +8,18 @@
         o = cache.attend(q, table, cu_q, kv_len, max_q, layer=layer)
     cache.fork(0, 1)                                         # sequence 1 shares sequence 0's pages
 
+PagedCache(..., dtype=torch.float8_e4m3fn) keeps the pages in 8 bits, quantised as append writes them: half of the memory
+and of what a decoding step reads. All calls are the same; read gives back what the pages hold.
+
+A step of drafted trees, verified in one pass:
+
+    mask, pos = cache.tree_masks(parents, cu_q, kv_len, max_q)    # from each drafted token's parent
+    for layer in range(32):
+        q = cache.append(k, v, table, cu_q, kv_len, layer=layer, rope=rope, pos=pos, q=q)
+        o = cache.attend(q, table, cu_q, kv_len, max_q, layer=layer, tree=mask)
+    cache.accept(table, cu_q, kv_len, path)                       # the kept tokens' indices, -1 behind them
+    cache.resize([0], [base + kept])
+
 A step of single tokens is the same three calls with one row per sequence. Everything that changes from step to step is
 read on the device, so append and attend can be captured in a CUDA graph (after one eager call each) and replayed.
 append and attend are for answering: their results carry no gradient (rope_axes and anchor_attention's do).
@@ -47,43 +59,64 @@ def _i32p(a):
 
 
 class PagedCache:
-    """The pool of pages, bf16 [num_layers, num_pages, Hkv, page_size, D] for keys and for values, and which sequence holds
-    which page. k_pages / v_pages: tensors to use as the pool (else allocated, uncleared, on `device`). max_seqs = 0: no
-    bookkeeping, the caller has page tables of its own."""
+    """The pool of pages, [num_layers, num_pages, Hkv, page_size, D] for keys and for values, and which sequence holds
+    which page. dtype: torch.bfloat16, or torch.float8_e4m3fn for 8-bit pages with k_scales / v_scales, float8_e8m0fnu
+    [num_layers, num_pages, Hkv, page_size] (a token's power of two: page value * scale is what it stands for). k_pages /
+    v_pages (and the scales): tensors to use as the pool, whose type they give (else allocated, uncleared, on `device`).
+    max_seqs = 0: no bookkeeping, the caller has page tables of its own."""
 
     def __init__(self, num_pages, page_size, num_kv_heads, head_dim, num_layers=1, max_seqs=0, k_pages=None, v_pages=None,
-                 device=None, host_only=False):
+                 device=None, host_only=False, dtype=None, k_scales=None, v_scales=None):
         self._h, self._dev = None, -1
         self.cfg = AACacheConfig(int(num_layers), int(num_pages), int(page_size), int(num_kv_heads), int(head_dim),
                                  int(max_seqs), int(bool(host_only)))
         self.L, self.P, self.ps = int(num_layers), int(num_pages), int(page_size)
         self.Hkv, self.D, self.host_only = int(num_kv_heads), int(head_dim), bool(host_only)
         h = ctypes.c_void_p()
+        if dtype is None:
+            dtype = k_pages.dtype if isinstance(k_pages, torch.Tensor) else torch.bfloat16
+        if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"dtype must be torch.bfloat16 or torch.float8_e4m3fn, got {dtype}")
+        self.dtype, fp8 = dtype, dtype == torch.float8_e4m3fn
         if host_only:
             _check(lib().aa_cache_create(ctypes.addressof(self.cfg), None, None, ctypes.byref(h)))
-            self.k_pages = self.v_pages = self.device = None
+            self.k_pages = self.v_pages = self.k_scales = self.v_scales = self.device = None
             self._h, self._dev = h, -1
             return
         shape = (self.L, self.P, self.Hkv, self.ps, self.D)
         if (k_pages is None) != (v_pages is None):
             raise ValueError("give both k_pages and v_pages or neither")
+        if any((x is not None) != (fp8 and k_pages is not None) for x in (k_scales, v_scales)):
+            raise ValueError("k_scales and v_scales go with 8-bit k_pages and v_pages")
         if k_pages is None:
             if min(shape) < 1:
                 raise ValueError("sizes must be >= 1")
             dev = torch.device("cuda" if device is None else device)
-            k_pages = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-            v_pages = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            k_pages = torch.empty(shape, dtype=dtype, device=dev)
+            v_pages = torch.empty(shape, dtype=dtype, device=dev)
+            if fp8:
+                k_scales, v_scales = (torch.empty(shape[:-1], dtype=torch.uint8, device=dev).view(torch.float8_e8m0fnu)
+                                      for _ in range(2))
         elif device is not None:
             raise ValueError("device goes without k_pages and v_pages")
-        for name, x in (("k_pages", k_pages), ("v_pages", v_pages)):
-            if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16 or x.device != k_pages.device:
-                raise ValueError(f"{name} must be a bfloat16 CUDA tensor, both on one device")
-            if x.shape != shape or not x.is_contiguous():
-                raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(x.shape)}")
+        pool = [("k_pages", k_pages, dtype, shape), ("v_pages", v_pages, dtype, shape)]
+        if fp8:
+            pool += [("k_scales", k_scales, torch.float8_e8m0fnu, shape[:-1]),
+                     ("v_scales", v_scales, torch.float8_e8m0fnu, shape[:-1])]
+        for name, x, kind, size in pool:
+            if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != kind or x.device != k_pages.device:
+                raise ValueError(f"{name} must be a {str(kind)[6:]} CUDA tensor, all on one device")
+            if x.shape != size or not x.is_contiguous():
+                raise ValueError(f"{name} must be contiguous with shape {size}, got {tuple(x.shape)}")
         self.k_pages, self.v_pages, self.device = k_pages, v_pages, k_pages.device
+        self.k_scales, self.v_scales = k_scales, v_scales
         with torch.cuda.device(self.device):
-            _check(lib().aa_cache_create(ctypes.addressof(self.cfg), k_pages.data_ptr(), v_pages.data_ptr(),
-                                         ctypes.byref(h)))
+            if fp8:
+                _check(lib().aa_cache_create_fp8(ctypes.addressof(self.cfg), k_pages.data_ptr(), k_scales.data_ptr(),
+                                                 v_pages.data_ptr(), v_scales.data_ptr(), ctypes.byref(h)))
+            else:
+                _check(lib().aa_cache_create(ctypes.addressof(self.cfg), k_pages.data_ptr(), v_pages.data_ptr(),
+                                             ctypes.byref(h)))
         self._h, self._dev = h, self.device.index
 
     # ---- lifetime
@@ -179,6 +212,30 @@ class PagedCache:
             _check(r)
         return r
 
+    def read(self, page_table, cu_q, kv_len, total_tokens, layer=0, out_k=None, out_v=None, stream=None):
+        """What the pages hold of the new tokens: k (as stored, rotated) and v, bf16 [total_tokens, Hkv, D]. Rows outside
+        the batch are not written."""
+        r = native().cache_read(self._device_handle(), self._dev, self.Hkv, self.D, page_table, cu_q, kv_len, total_tokens,
+                                layer, out_k, out_v, stream)
+        if type(r) is int:
+            _check(r)
+        return r
+
+    def tree_masks(self, parents, cu_q, kv_len, max_q, out_mask=None, out_pos=None, stream=None):
+        """Masks int64 [T, ceil(max_q / 64)] and positions int32 [T] of drafted trees, for attend's tree and append's pos.
+        parents: int32 [T], each new token's parent among its sequence's new tokens before it, -1: the cached tokens."""
+        r = native().cache_tree_masks(self._device_handle(), self._dev, parents, cu_q, kv_len, max_q, out_mask, out_pos, stream)
+        if type(r) is int:
+            _check(r)
+        return r
+
+    def accept(self, page_table, cu_q, kv_len, path, stream=None):
+        """Move the kept new tokens' keys and values up behind the cached tokens, in all layers: token path[b, i] to place i.
+        path: int32 [B, any], ascending indices among the sequence's new tokens, negative behind the last."""
+        r = native().cache_accept(self._device_handle(), self._dev, page_table, cu_q, kv_len, path, stream)
+        if r:
+            _check(r)
+
     def workspace_bytes(self, num_seqs, total_tokens, max_q, table_width, q_heads):
         return int(lib().aa_cache_attend_workspace_bytes(self._h, int(num_seqs), int(total_tokens), int(max_q),
                                                          int(table_width), int(q_heads)))
@@ -189,11 +246,13 @@ class PagedCache:
         return torch.empty(max(n, 256), device=self.device, dtype=torch.uint8)
 
     def attend(self, q, page_table, cu_q, kv_len, max_q, layer=0, key_lo=None, anchor=False, softmax_scale=0.0, out=None,
-               lse=None, workspace=None, return_lse=False, stream=None):
+               lse=None, workspace=None, return_lse=False, stream=None, tree=None):
         """Attention of the new tokens' rotated q [T, Hq, D] over their sequences' pages: o [T, Hq, D], and with
-        return_lse the log-sum-exp [Hq, T] fp32. key_lo: int32 [T], the first key each row sees; anchor: key 0 is seen too."""
+        return_lse the log-sum-exp [Hq, T] fp32. key_lo: int32 [T], the first key each row sees; anchor: key 0 is seen too.
+        tree: int64 [T, words], drafted trees: bit c % 64 of word c // 64 says whether the row sees new token c of its
+        sequence (tree_masks makes them of parents); of the cached ones it sees all from key_lo on."""
         r = native().cache_attend(self._device_handle(), self._dev, self.D, q, page_table, cu_q, kv_len, max_q, layer, key_lo,
-                                  anchor, softmax_scale or 0.0, out, lse, workspace, return_lse, stream)
+                                  anchor, softmax_scale or 0.0, out, lse, workspace, return_lse, tree, stream)
         if type(r) is int:
             _check(r)
         return r

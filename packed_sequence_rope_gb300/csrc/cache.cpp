@@ -42,9 +42,14 @@ aa_status check_batch(const aa_cache_s* c, const aa_cache_batch* b) {
 }
 
 aa_status check_outside_pool(const aa_cache_s* c, const char* what, const void* out, size_t bytes) {
-  const size_t pool = (size_t)c->cfg.num_layers * c->cfg.num_pages * c->page_elems() * 2;
+  const size_t pages = (size_t)c->cfg.num_layers * c->cfg.num_pages, pool = pages * c->page_bytes();
   if (overlap(out, bytes, c->k_pages, pool) || overlap(out, bytes, c->v_pages, pool))
     return fail(AA_ERR_INVALID_ARG, std::string(what) + " overlaps the cache's pages");
+  if (c->fp8()) {
+    const size_t scales = pages * c->cfg.num_kv_heads * c->cfg.page_size;
+    if (overlap(out, bytes, c->k_scales, scales) || overlap(out, bytes, c->v_scales, scales))
+      return fail(AA_ERR_INVALID_ARG, std::string(what) + " overlaps the cache's scales");
+  }
   return AA_OK;
 }
 
@@ -206,7 +211,9 @@ aa_status guarded(Fn fn) {
 
 using namespace aa;
 
-extern "C" aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, void* v_pages, aa_cache_t* out) {
+// Both kinds of handles; k_scales NULL: 16-bit pages.
+static aa_status create(const aa_cache_config* cfg, bool fp8, void* k_pages, void* k_scales, void* v_pages, void* v_scales,
+                        aa_cache_t* out) {
   if (!out) return fail(AA_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
   if (!cfg) return fail(AA_ERR_INVALID_ARG, "config is NULL");
@@ -223,9 +230,17 @@ extern "C" aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, 
   if (!host_only) {
     if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages))
       return fail(AA_ERR_INVALID_ARG, "k_pages and v_pages must be 16-byte aligned device pointers");
-    const size_t bytes = (size_t)rows * cfg->head_dim * 2;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(k_pages), b = reinterpret_cast<uintptr_t>(v_pages);
-    if (a < b + bytes && b < a + bytes) return fail(AA_ERR_INVALID_ARG, "k_pages and v_pages overlap");
+    const size_t bytes = (size_t)rows * cfg->head_dim * (fp8 ? 1 : 2);
+    if (overlap(k_pages, bytes, v_pages, bytes)) return fail(AA_ERR_INVALID_ARG, "k_pages and v_pages overlap");
+    if (fp8) {
+      if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales))
+        return fail(AA_ERR_INVALID_ARG, "k_scales and v_scales must be 16-byte aligned device pointers");
+      for (const void* x : {k_scales, v_scales})
+        if (overlap(x, (size_t)rows, k_pages, bytes) || overlap(x, (size_t)rows, v_pages, bytes))
+          return fail(AA_ERR_INVALID_ARG, "scales and pages overlap");
+      if (overlap(k_scales, (size_t)rows, v_scales, (size_t)rows))
+        return fail(AA_ERR_INVALID_ARG, "k_scales and v_scales overlap");
+    }
   }
   aa_cache_s* c = nullptr;
   aa_status st = guarded([&] {
@@ -234,6 +249,8 @@ extern "C" aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, 
     c->host_only = host_only;
     c->k_pages = k_pages;
     c->v_pages = v_pages;
+    c->k_scales = static_cast<uint8_t*>(k_scales);
+    c->v_scales = static_cast<uint8_t*>(v_scales);
     c->seqs.resize(cfg->max_seqs);
     if (cfg->max_seqs) {
       c->refs.assign(cfg->num_pages, 0);
@@ -251,8 +268,9 @@ extern "C" aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, 
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) st = cuda_fail(e, "cache set-up");
     const int box = std::min(cfg->page_size, 64);
-    if (st == AA_OK) st = make_pool_map(&c->k_map64, k_pages, (int64_t)rows, cfg->head_dim, box);
-    if (st == AA_OK) st = make_pool_map(&c->v_map64, v_pages, (int64_t)rows, cfg->head_dim, box);
+    const auto make_map = fp8 ? make_pool_map_fp8 : make_pool_map;
+    if (st == AA_OK) st = make_map(&c->k_map64, k_pages, (int64_t)rows, cfg->head_dim, box);
+    if (st == AA_OK) st = make_map(&c->v_map64, v_pages, (int64_t)rows, cfg->head_dim, box);
   }
   if (st != AA_OK) {
     if (c && c->err) cudaFree(c->err);
@@ -261,6 +279,15 @@ extern "C" aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, 
   }
   *out = c;
   return AA_OK;
+}
+
+extern "C" aa_status aa_cache_create(const aa_cache_config* cfg, void* k_pages, void* v_pages, aa_cache_t* out) {
+  return create(cfg, false, k_pages, nullptr, v_pages, nullptr, out);
+}
+
+extern "C" aa_status aa_cache_create_fp8(const aa_cache_config* cfg, void* k_pages, void* k_scales, void* v_pages,
+                                         void* v_scales, aa_cache_t* out) {
+  return create(cfg, true, k_pages, k_scales, v_pages, v_scales, out);
 }
 
 extern "C" aa_status aa_cache_destroy(aa_cache_t c) {
@@ -362,6 +389,10 @@ extern "C" aa_status aa_cache_check_error(aa_cache_t c, aa_stream_t stream) {
   if (word == kCacheBadPage) return fail(AA_ERR_INVALID_ARG, "a page table holds a page number outside the pool");
   if (word == kCacheBadPosition)
     return fail(AA_ERR_INVALID_ARG, "a position lies outside its page table (kv_len below the new tokens, or the table too narrow)");
+  if (word == kCacheBadTree)
+    return fail(AA_ERR_INVALID_ARG, "a drafted token's parent is neither -1 nor one of the new tokens before it");
+  if (word == kCacheBadPath)
+    return fail(AA_ERR_INVALID_ARG, "a path of accepted tokens does not ascend, or leaves its sequence's new tokens");
   char buf[96];
   std::snprintf(buf, sizeof buf, "device-side wait timed out or launch check failed (site code %d)", (int)word);
   return fail(AA_ERR_TIMEOUT, buf);

@@ -3,7 +3,8 @@
 // For new token i of sequence b, at position p = kv_len - n_b + i, and query
 // head h ("When Precision Meets Position", architecture page §3.4
 // "AnchorAttention: The Shared Anchor Design", "Mask construction"):
-//   visible keys: [max(key_lo, 0), p], and key 0 with the anchor (p >= 0)
+//   visible keys: [max(key_lo, 0), p], and key 0 with the anchor (p >= 0); of a
+//   drafted tree the cached keys from key_lo on and the new ones of the row's mask
 //   O_i = sum_j softmax_j(scale * q_i . k_j) v_j, LSE_i = ln sum_j exp(...)
 // in one pass with the running maximum and sum of the softmax. This file checks the
 // arguments and chooses between cache_attend_short.cu (few rows per sequence: the
@@ -30,6 +31,7 @@ using namespace aa;
 //   64, 42            49.1 / 27.7  117 / 92.0  621 / 537
 // With D = 64: 64 rows of 42 sequences 24.4 / 25.0, 56.9 / 76.2 and 314 / 469.
 static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
+  if (c->fp8()) return true;
   const int64_t rows = (int64_t)std::max(max_q, 1) * group;
   if (rows <= 32 || c->cfg.head_dim == 64) return rows <= kShortRows;
   return rows <= kShortRows && (int64_t)table_width * c->cfg.page_size > kWholeKeys &&
@@ -47,10 +49,10 @@ extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs
   return chunk_workspace_bytes(c, num_seqs, total_tokens, table_width, q_heads / Hkv);
 }
 
-extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, const void* q, int64_t q_stride,
-                                     int32_t q_heads, int32_t max_q, const int32_t* key_lo, int32_t anchor,
-                                     float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
-                                     aa_stream_t stream) {
+static aa_status attend(aa_cache_t c, const aa_cache_batch* batch, const void* q, int64_t q_stride, int32_t q_heads,
+                        int32_t max_q, const int32_t* key_lo, int32_t anchor, const uint64_t* tree, int32_t tree_words,
+                        float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                        aa_stream_t stream) {
   aa_status st = check_compute_cache(c);
   if (st != AA_OK) return st;
   if ((st = check_batch(c, batch)) != AA_OK) return st;
@@ -67,6 +69,7 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   if (!o || !aligned16(o)) return fail(AA_ERR_INVALID_ARG, "o must be a 16-byte aligned device pointer");
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(key_lo) & 3u))
     return fail(AA_ERR_INVALID_ARG, "lse and key_lo must be 4-byte aligned device pointers");
+  if (reinterpret_cast<uintptr_t>(tree) & 7u) return fail(AA_ERR_INVALID_ARG, "tree must be an 8-byte aligned device pointer");
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(AA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   const size_t used = aa_cache_attend_workspace_bytes(c, batch->num_seqs, T, max_q, batch->table_width, q_heads);
@@ -82,6 +85,7 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
                  {"the workspace", workspace, used > 256 ? used : 0}},  // 256: none is in use
     read[] = {{"q", q, rows_span(T, q_stride, q_heads, D)},
               {"key_lo", key_lo, (size_t)T * 4},
+              {"tree", tree, (size_t)T * tree_words * 8},
               {"page_table", batch->page_table, (size_t)batch->num_seqs * batch->table_width * 4},
               {"cu_q", batch->cu_q, ((size_t)batch->num_seqs + 1) * 4},
               {"kv_len", batch->kv_len, (size_t)batch->num_seqs * 4}};
@@ -106,10 +110,33 @@ extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, 
   P.Hq = q_heads;
   P.group = q_heads / Hkv;
   P.anchor = anchor != 0;
+  P.k_scales = c->k_scales;
+  P.v_scales = c->v_scales;
+  P.tree = tree;
+  P.tree_words = tree_words;
   P.page_shift = __builtin_ctz((unsigned)c->cfg.page_size);
   P.scale_log2 = (float)((softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!takes_short(c, batch->num_seqs, max_q, batch->table_width, P.group)) return launch_attend_chunk(c, P, workspace, s);
-  cudaError_t e = launch_attend_short(c, P, max_q, workspace, s);
+  cudaError_t e = (c->fp8() ? launch_attend_short_fp8 : launch_attend_short)(c, P, max_q, workspace, s);
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
+}
+
+extern "C" aa_status aa_cache_attend(aa_cache_t c, const aa_cache_batch* batch, const void* q, int64_t q_stride,
+                                     int32_t q_heads, int32_t max_q, const int32_t* key_lo, int32_t anchor,
+                                     float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     aa_stream_t stream) {
+  return attend(c, batch, q, q_stride, q_heads, max_q, key_lo, anchor, nullptr, 0, softmax_scale, o, lse, workspace,
+                workspace_bytes, stream);
+}
+
+extern "C" aa_status aa_cache_attend_tree(aa_cache_t c, const aa_cache_batch* batch, const void* q, int64_t q_stride,
+                                          int32_t q_heads, int32_t max_q, const int32_t* key_lo, int32_t anchor,
+                                          const uint64_t* tree, int32_t tree_words, float softmax_scale, void* o, float* lse,
+                                          void* workspace, size_t workspace_bytes, aa_stream_t stream) {
+  if (tree_words < 1 || tree_words > kMaxTreeWords)
+    return fail(AA_ERR_INVALID_ARG, "tree_words must be in [1, " + std::to_string(kMaxTreeWords) + "]");
+  if (!tree && batch && batch->total_tokens > 0) return fail(AA_ERR_INVALID_ARG, "tree must be an 8-byte aligned device pointer");
+  return attend(c, batch, q, q_stride, q_heads, max_q, key_lo, anchor, tree, tree_words, softmax_scale, o, lse, workspace,
+                workspace_bytes, stream);
 }

@@ -17,6 +17,11 @@ struct AttendParams {
   int64_t q_stride;
   int Hq, group, anchor, page_shift;
   float scale_log2;    // softmax scale * log2 e
+  // 8-bit pages: a byte per token and kv head, as aa_cache_s has them
+  const uint8_t *k_scales, *v_scales;
+  // drafted trees: [T, tree_words] masks of the new tokens, NULL without
+  const uint64_t* tree;
+  int tree_words;
 };
 
 // New tokens [q0, q0 + n) of sequence b that hold kv tokens. Rows outside the
@@ -56,6 +61,31 @@ __device__ __forceinline__ uint64_t seen_keys(const AttendParams& P, int q_row, 
     sees_b |= lo <= b && b <= hi;
   }
   return __ballot_sync(0xffffffffu, sees_a) | (uint64_t)__ballot_sync(0xffffffffu, sees_b) << 32;
+}
+
+// Drafted trees: which of the keys j + x, x < 64, that are new tokens row t of the
+// batch sees, the n new ones of its sequence lying at [base, base + n). Bit x. Keys
+// in front of base have none.
+__device__ __forceinline__ uint64_t tree_keys(const AttendParams& P, int64_t t, int base, int n, int j) {
+  const int c = j - base;  // the new token that bit 0 stands for
+  if (c <= -64 || c >= n) return 0;
+  const uint64_t* row = P.tree + t * P.tree_words;
+  const int w = c >> 6, shift = c & 63;  // c < 0: word -1 does not exist
+  uint64_t bits = w >= 0 && w < P.tree_words ? __ldg(row + w) >> shift : 0;
+  if (shift && w + 1 < P.tree_words) bits |= __ldg(row + w + 1) << (64 - shift);
+  return n - c < 64 ? bits & ((1ull << (n - c)) - 1) : bits;
+}
+
+// seen_keys() for drafted trees: bit x, some of the tokens q_row + i (i < tokens, the
+// sequence's new tokens i0 + i) sees key j + x (a whole warp asks). Keys in front of
+// base count as seen: together the rows see all from their smallest first key on.
+__device__ __forceinline__ uint64_t tree_seen_keys(const AttendParams& P, int q_row, int i0, int tokens, int base, int n, int j) {
+  uint64_t any = 0;
+  for (int i = threadIdx.x & 31; i < tokens; i += 32)
+    if (base + i0 + i >= 0) any |= tree_keys(P, q_row + i, base, n, j);
+  any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)any);
+  const int c = base - j;  // keys of the window in front of base
+  return c <= 0 ? any : c >= 64 ? ~0ull : any | ((1ull << c) - 1);
 }
 
 // Four channels of a row divided by its sum, in bf16; 0 for a row that saw
@@ -122,6 +152,7 @@ constexpr int kWholeKeys = 768;
 // short: at most kShortRows rows (max_q * group) of a sequence and kv head at a time.
 constexpr int kShortRows = 64;
 cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int max_q, void* workspace, cudaStream_t s);
+cudaError_t launch_attend_short_fp8(const aa_cache_s* c, const AttendParams& P, int max_q, void* workspace, cudaStream_t s);
 size_t short_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int max_q, int table_width, int group);
 aa_status launch_attend_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
 size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int table_width, int group);

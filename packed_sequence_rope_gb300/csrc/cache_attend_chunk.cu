@@ -54,7 +54,9 @@ constexpr int kUnitCost = 2;
 
 // A unit as chunk_plan_kernel describes it: tokens [i0, i0 + tokens) of a
 // sequence, their positions [p0, p0 + tokens), the smallest of their first keys;
-// gaps: some of them see nothing, so that keys between seen ones may be unseen.
+// gaps: some of them see nothing, so that keys between seen ones may be unseen; of a
+// drafted tree, whose rows may see all of their sequence's new tokens, the position of
+// the first of these.
 struct Unit {
   int32_t seq, q_row, tokens, p0, lo, gaps;
 };
@@ -107,8 +109,16 @@ __device__ __forceinline__ Unit load_unit(const ChunkParams& C, int slot, int* c
       u.lo = __reduce_min_sync(0xffffffffu, lo);
       u.gaps = __any_sync(0xffffffffu, gaps);
     }
+    int hi = u.p0 + u.tokens - 1;
+    bool anchor = P.anchor;
+    if (P.tree) {
+      u.gaps = s.kv - s.n;
+      u.lo = min(u.lo, max(u.gaps, 0));
+      hi = s.kv - 1;
+      anchor = anchor && u.gaps > 0;
+    }
     // rows that see nothing are written too: at least one tile
-    *count = max(KeyTiles<kKeys>(u.lo, u.p0 + u.tokens - 1, P.anchor).count, 1);
+    *count = max(KeyTiles<kKeys>(u.lo, hi, anchor).count, 1);
   }
   return u;
 }
@@ -178,6 +188,7 @@ struct Shares {
 // One piece of work: key tiles [first, first + take) of a unit's `count`.
 struct Piece {
   int valid, g, seq, q_row, tokens, p0, lo, gaps;
+  int hi;                  // the last key that a row may see
   int first, take, whole;  // whole: the unit is not cut
   int part;                // else: which of the CTA's two partial results
 };
@@ -250,7 +261,7 @@ __device__ __forceinline__ uint32_t visible_bits(int j, int lo, int hi) {
 // softmax steps; q_full and q_free the CTA's row tiles of Q; o_full the pieces
 // in which the row tile exists. As in the packed forward every wait is bounded and its outcome made
 // uniform in a warp before anything collective.
-template <int HD>
+template <int HD, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ChunkParams C) {
@@ -359,18 +370,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           at = until;
         }
       }
+      w.hi = w.p0 + w.tokens - 1;
+      if (kTree && w.valid) w.hi = load_seq(b, w.seq, P.page_shift).kv - 1;
       if (lane == 0) {
         sm.piece[li & 1] = w;
         ptx::mbar_arrive(&sm.piece_full[li & 1]);
       }
       __syncwarp();
       if (!w.valid) break;
-      const int hi = w.p0 + w.tokens - 1;
-      const KeyTiles<kKeys> keys(w.lo, hi, P.anchor);
+      const int hi = w.hi;
+      const bool anchor = P.anchor && (!kTree || w.gaps > 0);
+      const KeyTiles<kKeys> keys(w.lo, hi, anchor);
       auto row_of = [&](int i) {
         const int j = keys.tile(i) * kKeys + (part << piece_shift);
         // pieces that no row sees are not looked up (lo > hi: the rows see the anchor at most)
-        const bool seen = j <= hi && ((w.lo <= hi && j + (1 << piece_shift) > w.lo) || (j == 0 && P.anchor));
+        const bool seen = j <= hi && ((w.lo <= hi && j + (1 << piece_shift) > w.lo) || (j == 0 && anchor));
         return lane < copies && i < w.first + w.take && i < keys.count && seen ? pool_row(b, w.seq, w.g, j, P.page_shift)
                                                                                : kNoRow;
       };
@@ -505,8 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int li = 0; ok; ++li) {
       Piece w;
       if (!read_piece(sm, li, b.err, abort_flag, 470, &w)) break;
-      const int hi = w.p0 + w.tokens - 1;
-      const KeyTiles<kKeys> keys(w.lo, hi, P.anchor);
+      const int hi = w.hi;
+      const bool anchor = P.anchor && (!kTree || w.gaps > 0);
+      const KeyTiles<kKeys> keys(w.lo, hi, anchor);
       for (int i = w.first; i < w.first + w.take; ++i, ++ks) {
         const int s = ks % kStages;
         if (!(ok = warp_wait(&sm.v_full[s], (ks / kStages) & 1, b.err, abort_flag, 471))) break;
@@ -519,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int row = from + first_row; row < to; row += 2 * kRowsAtOnce)
               *reinterpret_cast<uint4*>(sm.v[s][chunk >> 3] + row * 128 + (chunk & 7) * 16) = make_uint4(0, 0, 0, 0);
           };
-          const bool anchored = P.anchor && j0 == 0 && hi >= 0 && w.lo > 0;
+          const bool anchored = anchor && j0 == 0 && hi >= 0 && w.lo > 0;
           const int lo_piece = w.lo & ~(piece - 1);  // its copy starts here
           if (anchored) clear(1, w.lo <= hi ? min(piece, w.lo) : piece);
           if (w.lo <= hi) {
@@ -529,9 +544,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::fence_proxy_async_smem();
           __syncwarp();
         }
-        if (w.gaps && j0 + kKeys - 1 > w.p0) {
+        if (kTree ? j0 + kKeys > w.gaps : w.gaps && j0 + kKeys - 1 > w.p0) {
           const int from = (warp - 2) * 64;  // half of the tile's keys per warp
-          for (uint64_t none = ~seen_keys(P, w.q_row, w.p0, w.tokens, j0 + from); none; none &= none - 1) {
+          const uint64_t some = kTree ? tree_seen_keys(P, w.q_row, w.p0 - w.gaps, w.tokens, w.gaps, hi + 1 - w.gaps, j0 + from)
+                                      : seen_keys(P, w.q_row, w.p0, w.tokens, j0 + from);
+          for (uint64_t none = ~some; none; none &= none - 1) {
             const int row = from + __ffsll((long long)none) - 1;
             if (lane < kChunks)
               *reinterpret_cast<uint4*>(sm.v[s][chunk >> 3] + row * 128 + (chunk & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -569,10 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row_valid) {
         lo = first_key(P, w.q_row + t * C.tile_tokens + in_tile);
         hi = w.p0 + t * C.tile_tokens + in_tile;
+        if constexpr (kTree) hi = min(hi, w.gaps - 1);  // of the cached keys; the row's mask says which new ones
       }
       const bool anchored = P.anchor && row_valid && hi >= 0 && half == 0;
       const int take = w.take;
-      const KeyTiles<kKeys> keys(w.lo, w.p0 + w.tokens - 1, P.anchor);
+      const KeyTiles<kKeys> keys(w.lo, w.hi, P.anchor && (!kTree || w.gaps > 0));
       int j0 = keys.tile(w.first) * kKeys + half * 64;  // this warp's first key
       int next_j0 = keys.tile(w.first + 1) * kKeys + half * 64;
       float m = -INFINITY, l = 0.f;
@@ -622,13 +640,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool full0 = __all_sync(0xffffffffu, lo <= j0 && j0 + 31 <= hi);
         const bool full1 = __all_sync(0xffffffffu, lo <= j0 + 32 && j0 + 63 <= hi);
         ptx::tmem_wait_ld();
+        uint64_t tree = 0;  // new tokens among the warp's keys
+        if constexpr (kTree) {
+          if (j0 + 64 > w.gaps && row_valid && w.p0 + t * C.tile_tokens + in_tile >= 0)
+            tree = tree_keys(P, w.q_row + t * C.tile_tokens + in_tile, w.gaps, w.hi + 1 - w.gaps, j0);
+        }
         if (!full0) {
-          const uint32_t bits = visible_bits(j0, lo, hi) | (j0 == 0 && anchored ? 1u : 0u);
+          const uint32_t bits = visible_bits(j0, lo, hi) | (j0 == 0 && anchored ? 1u : 0u) | (uint32_t)tree;
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[e] = (bits >> e) & 1u ? sv[e] : -INFINITY;
         }
         if (!full1) {
-          const uint32_t bits = visible_bits(j0 + 32, lo, hi);
+          const uint32_t bits = visible_bits(j0 + 32, lo, hi) | (uint32_t)(tree >> 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[32 + e] = (bits >> e) & 1u ? sv[32 + e] : -INFINITY;
         }
@@ -883,7 +906,7 @@ int ctas_for(const aa_cache_s* c) { return std::min(c->num_sms, kMaxCtas); }
 bool whole_units(int table_width, int page_shift) { return ((int64_t)table_width << page_shift) <= kWholeKeys; }
 int slots_for(int tokens, int seqs, int tile_tokens) { return tokens / (2 * tile_tokens) + seqs; }
 
-template <int HD>
+template <int HD, bool kTree>
 aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {
   const BatchParams& b = P.batch;
   ChunkParams C;
@@ -913,21 +936,22 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   CUtensorMap tq;
   aa_status st = make_query_map(&tq, P.q, b.T, P.q_stride, b.Hkv, P.group, HD, C.tile_tokens);
   if (st != AA_OK) return st;
+  const auto kernel = attend_chunk_kernel<HD, kTree>;
   const size_t smem = sizeof(ChunkSmem<HD>);
   static std::once_flag once[kMaxDevices];
   static cudaError_t result[kMaxDevices];
   cudaError_t e = once_per_device(once, result, c->device, [&] {
-    return cudaFuncSetAttribute(attend_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel smem attribute");
   if (C.whole_units) {
     const unsigned grid = (unsigned)std::min<int64_t>((int64_t)C.slots * b.Hkv, ctas);
-    e = launch_after(attend_chunk_kernel<HD>, dim3(grid), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
+    e = launch_after(kernel, dim3(grid), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
     return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_chunk_kernel launch");
   }
   chunk_plan_kernel<<<1, 1024, 0, s>>>(C);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "chunk_plan_kernel launch");
-  e = launch_after(attend_chunk_kernel<HD>, dim3((unsigned)ctas), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
+  e = launch_after(kernel, dim3((unsigned)ctas), kThreads, smem, s, tq, c->k_map64, c->v_map64, C);
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel launch");
   const bool few = (int64_t)C.slots * b.Hkv * kHelpParts <= ctas && ((int64_t)b.W << P.page_shift) > kHelpKeys;
   static_assert(256 / kJoinRows <= kHelpParts * kJoinBlocks, "a block for each piece of the few units");
@@ -947,7 +971,8 @@ size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens
 }
 
 aa_status launch_attend_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {
-  return c->cfg.head_dim == 128 ? launch<128>(c, P, workspace, s) : launch<64>(c, P, workspace, s);
+  if (P.tree) return c->cfg.head_dim == 128 ? launch<128, true>(c, P, workspace, s) : launch<64, true>(c, P, workspace, s);
+  return c->cfg.head_dim == 128 ? launch<128, false>(c, P, workspace, s) : launch<64, false>(c, P, workspace, s);
 }
 
 }  // namespace aa

@@ -30,6 +30,25 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* __restrict__ cu_q, i
   return warp_last(num_seqs, [&](int i) { return __ldg(cu_q + i) <= t; });
 }
 
+// Four e4m3 numbers b0 .. b3 as bf16 pairs (b0, b2) and (b1, b3), exactly: sign, exponent
+// and significand moved to their places in bf16 mean 2^-120 times the number (a
+// subnormal one lands among bf16's subnormals), which one product undoes. NaN codes
+// become 480. Shifts and selections, two of the five on 16-bit halves, are
+// cheaper than the conversion to f16, which would also need f16 weights.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t x, uint32_t up = 0x7b807b80u) {  // up: 2^120 twice
+  const uint32_t even = ((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u);
+  const uint32_t odd = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+  uint2 r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(even), "r"(up));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(odd), "r"(up));
+  return r;
+}
+
+// 2^(byte - 127); NaN for 255, 0 for 0.
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte << 23 | (byte == 255u ? 0x00400000u : 0u));
+}
+
 // One batch as the kernels see it.
 struct BatchParams {
   const int32_t *table, *cu_q, *kv_len;

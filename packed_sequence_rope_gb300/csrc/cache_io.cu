@@ -1,6 +1,14 @@
 // Writing to the paged cache: aa_cache_append (new keys rotated into their
-// pages, values beside them, queries rotated on the way) and the page copies of
-// aa_cache_copy_pages, aa_cache_resize and aa_cache_compact.
+// pages, values beside them, queries rotated on the way; quantised as they are
+// written where the pages hold 8 bits), aa_cache_read, which brings tokens back, and
+// the page copies of aa_cache_copy_pages, aa_cache_resize and aa_cache_compact.
+//
+// 8-bit pages: a row of D values is stored as e4m3 codes c with x = c * 2^e, e the
+// smallest integer in [-100, 119] that keeps max |x| within 448 * 2^e, and a byte e + 127.
+// A power of two costs a floating-point code no accuracy, and makes what a page
+// holds exact in bf16 (4-bit significands). e >= -100 keeps a weight times 2^e of the
+// attention in bf16's normal range, e <= 119 what a page holds within its range. A row with a value that is not finite has byte
+// 255, which makes all of it NaN.
 //
 // Both are bound by HBM (a decoding step's few rows by the launch): every byte
 // is read and written once, in 16-byte accesses. A compaction of 256 pages of
@@ -25,8 +33,64 @@ struct AppendParams {
   const int32_t* pos;
   const __nv_bfloat16 *q, *k, *v;
   __nv_bfloat16 *q_out, *k_pages, *v_pages;
+  uint8_t *k_scales, *v_scales;  // 8-bit pages; k_pages and v_pages are then bytes
   int64_t q_stride, k_stride, v_stride;
   int Hq, page_shift;
+};
+
+// Sixteen values of a row in fp32, eight from each of the places where Pairs8 has them.
+template <int HD, int L>
+struct Values16 {
+  float a[8], b[8];
+  __device__ __forceinline__ explicit Values16(const Pairs8<HD, L>& x) {
+    const uint32_t u[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 va = ptx::unpack_bf16x2(u[e]), vb = ptx::unpack_bf16x2(u[4 + e]);
+      a[2 * e] = va.x;
+      a[2 * e + 1] = va.y;
+      b[2 * e] = vb.x;
+      b[2 * e + 1] = vb.y;
+    }
+  }
+  __device__ __forceinline__ void turn(const float2* cs) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (L == 0) {
+        float* x = e < 4 ? a + 2 * e : b + 2 * e - 8;
+        rope_pair(x[0], x[1], cs[e].x, cs[e].y);
+      } else {
+        rope_pair(a[e], b[e], cs[e].x, cs[e].y);
+      }
+    }
+  }
+  // Quantises the row, which HD / 16 neighbouring lanes hold, into `row`; its scale's
+  // byte goes to *scale.
+  __device__ __forceinline__ void store(uint8_t* row, uint8_t* scale, int chunk) const {
+    constexpr int kLanes = HD / 16;
+    const uint32_t lanes = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) & ~(kLanes - 1));
+    uint32_t top = 0;  // the largest magnitude's bits; NaN and infinity are above all numbers
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, max(__float_as_uint(a[e]) & 0x7fffffffu, __float_as_uint(b[e]) & 0x7fffffffu));
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(lanes, top, d));
+    // 448 = 1.75 * 2^8
+    const int e = min(max((int)(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 119);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    uint32_t w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float* v = x < 2 ? a + 4 * x : b + 4 * x - 8;
+      w[x] = ptx::pack_e4m3x2(v[0] * down, v[1] * down) | ptx::pack_e4m3x2(v[2] * down, v[3] * down) << 16;
+    }
+    if constexpr (L == 0) {
+      *reinterpret_cast<uint4*>(row + 16 * chunk) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      *reinterpret_cast<uint2*>(row + 8 * chunk) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(row + HD / 2 + 8 * chunk) = make_uint2(w[2], w[3]);
+    }
+    if (chunk == 0) *scale = top >= 0x7f800000u ? 255 : (uint8_t)(e + 127);
+  }
 };
 
 // Pool row of token t for kv head 0; -1 if it has none (an error), -2 if the
@@ -53,7 +117,7 @@ __device__ __forceinline__ int64_t find_slot(const BatchParams& b, int t, int pa
 // L: the pairing (0, 1), or 2 to store the keys as they are. A block takes
 // kTokens rows; as in rope_axes_kernel the angles of a token are computed once
 // for all heads, while the first row is in flight.
-template <int HD, int L, int kTokens>
+template <int HD, int L, int kTokens, bool k8>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int kHalf = HD / 2, kChunks = HD / 16, kRows = kThreads / kChunks / kTokens;
   static_assert(kTokens <= kThreads / 32, "a warp looks up each token");
@@ -94,6 +158,18 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   for (int h = row % kRows; h < heads; h += kRows) {
     if (h >= kRows) load(x, h);
     const int g = h - P.Hq;
+    if constexpr (k8) {
+      if (g >= 0) {
+        if (at < 0) continue;  // all lanes of a row
+        Values16<HD, L == 2 ? 0 : L> y(x);
+        if constexpr (L != 2)
+          if (g < b.Hkv) y.turn(mine);
+        const int64_t row = at + ((int64_t)(g < b.Hkv ? g : g - b.Hkv) << P.page_shift);
+        uint8_t* pages = reinterpret_cast<uint8_t*>(g < b.Hkv ? P.k_pages : P.v_pages);
+        y.store(pages + row * HD, (g < b.Hkv ? P.k_scales : P.v_scales) + row, chunk);
+        continue;
+      }
+    }
     if constexpr (L != 2)
       if (g < b.Hkv) x.turn(mine);
     if (g < 0)
@@ -104,12 +180,82 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   }
 }
 
-template <int HD, int L>
+template <int HD, int L, bool k8>
 cudaError_t launch_append(const AppendParams& P, cudaStream_t s) {
   if (P.batch.T <= kFewTokens)
-    cache_append_kernel<HD, L, 1><<<(unsigned)P.batch.T, kThreads, 0, s>>>(P);
+    cache_append_kernel<HD, L, 1, k8><<<(unsigned)P.batch.T, kThreads, 0, s>>>(P);
   else
-    cache_append_kernel<HD, L, 2><<<(unsigned)((P.batch.T + 1) / 2), kThreads, 0, s>>>(P);
+    cache_append_kernel<HD, L, 2, k8><<<(unsigned)((P.batch.T + 1) / 2), kThreads, 0, s>>>(P);
+  return cudaGetLastError();
+}
+
+template <int HD, int L>
+cudaError_t launch_append(const AppendParams& P, cudaStream_t s) {
+  return P.k_scales ? launch_append<HD, L, true>(P, s) : launch_append<HD, L, false>(P, s);
+}
+
+// ---------------------------------------------------------------- reading back
+struct ReadParams {
+  BatchParams batch;
+  const uint8_t *k_pages, *v_pages, *k_scales, *v_scales;
+  __nv_bfloat16 *k, *v;
+  int page_shift;
+};
+
+// A block takes kTokens rows of k and v; a thread 16 channels of a head. Bound by HBM
+// like the append, a step's few rows by the launch.
+template <int HD, int kTokens, bool k8>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams P) {
+  constexpr int kChunks = HD / 16, kRows = kThreads / kChunks / kTokens;
+  __shared__ int64_t slot[kTokens];
+  const BatchParams& b = P.batch;
+  const int t0 = (int)blockIdx.x * kTokens, warp = threadIdx.x >> 5;
+  if (warp < kTokens) {
+    const int64_t at = find_slot(b, t0 + warp, P.page_shift);
+    if ((threadIdx.x & 31) == 0) slot[warp] = at;
+  }
+  __syncthreads();
+  const int chunk = threadIdx.x % kChunks, row = threadIdx.x / kChunks, tok = row / kRows;
+  const int64_t at = slot[tok], t = t0 + tok;
+  if (at == -2) return;
+  for (int h = row % kRows; h < 2 * b.Hkv; h += kRows) {
+    const int g = h < b.Hkv ? h : h - b.Hkv;
+    const int64_t from = at + ((int64_t)g << P.page_shift);
+    uint4* to = reinterpret_cast<uint4*>((h < b.Hkv ? P.k : P.v) + (t * b.Hkv + g) * HD + 16 * chunk);
+    uint4 y[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // a token whose page is none
+    if (at >= 0) {
+      const uint8_t* pages = h < b.Hkv ? P.k_pages : P.v_pages;
+      if constexpr (k8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(pages + from * HD + 16 * chunk);
+        const float up = scale_of((h < b.Hkv ? P.k_scales : P.v_scales)[from]);
+        const uint32_t c[4] = {x.x, x.y, x.z, x.w};
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint2 v = e4m3x4_to_bf16(c[e]);  // codes (0, 2), (1, 3)
+          const float2 even = ptx::unpack_bf16x2(v.x), odd = ptx::unpack_bf16x2(v.y);
+          w[2 * e] = ptx::pack_bf16x2(even.x * up, odd.x * up);
+          w[2 * e + 1] = ptx::pack_bf16x2(even.y * up, odd.y * up);
+        }
+        y[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        y[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else {
+        const uint4* x = reinterpret_cast<const uint4*>(pages + (from * HD + 16 * chunk) * 2);
+        y[0] = x[0];
+        y[1] = x[1];
+      }
+    }
+    to[0] = y[0];
+    to[1] = y[1];
+  }
+}
+
+template <int HD, bool k8>
+cudaError_t launch_read(const ReadParams& P, cudaStream_t s) {
+  if (P.batch.T <= kFewTokens)
+    cache_read_kernel<HD, 1, k8><<<(unsigned)P.batch.T, kThreads, 0, s>>>(P);
+  else
+    cache_read_kernel<HD, 2, k8><<<(unsigned)((P.batch.T + 1) / 2), kThreads, 0, s>>>(P);
   return cudaGetLastError();
 }
 
@@ -127,6 +273,8 @@ struct CopyParams {
   uint8_t *k_pages, *v_pages;
   int64_t page_bytes, layer_bytes;
   int blocks_per_page;
+  uint8_t *k_scales, *v_scales;  // 8-bit pages: copied by the first block of a page, which is never larger
+  int64_t scale_bytes, scale_layer;
 };
 
 template <int N>
@@ -137,6 +285,12 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CopyParams P
   const uint8_t* src = pool + pair.src * P.page_bytes;
   uint8_t* dst = pool + pair.dst * P.page_bytes;
   const int64_t at = (int64_t)part * kCopyBytes + threadIdx.x * 16;
+  if (P.k_scales && part == 0) {
+    uint8_t* scales = ((which & 1) ? P.v_scales : P.k_scales) + (int64_t)(which >> 1) * P.scale_layer;
+    for (int64_t x = threadIdx.x * 16; x < P.scale_bytes; x += kThreads * 16)
+      *reinterpret_cast<uint4*>(scales + pair.dst * P.scale_bytes + x) =
+          *reinterpret_cast<const uint4*>(scales + pair.src * P.scale_bytes + x);
+  }
   uint4 v[kCopyVecs];
 #pragma unroll
   for (int i = 0; i < kCopyVecs; ++i)
@@ -161,7 +315,11 @@ aa_status launch_copy_pages(const aa_cache_s* c, const std::vector<PagePair>& pa
   CopyParams P;
   P.k_pages = static_cast<uint8_t*>(c->k_pages);
   P.v_pages = static_cast<uint8_t*>(c->v_pages);
-  P.page_bytes = c->page_elems() * 2;
+  P.page_bytes = c->page_bytes();
+  P.k_scales = c->k_scales;
+  P.v_scales = c->v_scales;
+  P.scale_bytes = (int64_t)c->cfg.num_kv_heads * c->cfg.page_size;
+  P.scale_layer = P.scale_bytes * c->cfg.num_pages;
   P.layer_bytes = P.page_bytes * c->cfg.num_pages;
   P.blocks_per_page = (int)((P.page_bytes + kCopyBytes - 1) / kCopyBytes);
   const int n = (int)pairs.size();
@@ -215,6 +373,8 @@ extern "C" aa_status aa_cache_append(aa_cache_t c, const aa_cache_batch* batch, 
   P.q_out = static_cast<__nv_bfloat16*>(q_out);
   P.k_pages = static_cast<__nv_bfloat16*>(c->k_pages);
   P.v_pages = static_cast<__nv_bfloat16*>(c->v_pages);
+  P.k_scales = c->k_scales;
+  P.v_scales = c->v_scales;
   P.q_stride = q_stride;
   P.k_stride = k_stride;
   P.v_stride = v_stride;
@@ -228,4 +388,43 @@ extern "C" aa_status aa_cache_append(aa_cache_t c, const aa_cache_batch* batch, 
   else
     e = L == 0 ? launch_append<64, 0>(P, s) : L == 1 ? launch_append<64, 1>(P, s) : launch_append<64, 2>(P, s);
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "cache_append_kernel launch");
+}
+
+extern "C" aa_status aa_cache_read(aa_cache_t c, const aa_cache_batch* batch, void* k, void* v, aa_stream_t stream) {
+  aa_status st = check_compute_cache(c);
+  if (st != AA_OK) return st;
+  if ((st = check_batch(c, batch)) != AA_OK) return st;
+  const int D = c->cfg.head_dim, Hkv = c->cfg.num_kv_heads, T = batch->total_tokens;
+  if (T == 0) return AA_OK;
+  const size_t bytes = (size_t)T * Hkv * D * 2;
+  const struct {
+    const char* name;
+    const void* at;
+    size_t bytes;
+  } read[] = {{"page_table", batch->page_table, (size_t)batch->num_seqs * batch->table_width * 4},
+              {"cu_q", batch->cu_q, ((size_t)batch->num_seqs + 1) * 4},
+              {"kv_len", batch->kv_len, (size_t)batch->num_seqs * 4}};
+  for (const auto& [name, x] : {std::pair<const char*, const void*>{"k", k}, {"v", v}}) {
+    if (!x || !aligned16(x)) return fail(AA_ERR_INVALID_ARG, std::string(name) + " must be a 16-byte aligned device pointer");
+    if ((st = check_outside_pool(c, name, x, bytes)) != AA_OK) return st;
+    for (const auto& y : read)
+      if (overlap(x, bytes, y.at, y.bytes)) return fail(AA_ERR_INVALID_ARG, std::string(name) + " overlaps " + y.name);
+  }
+  if (overlap(k, bytes, v, bytes)) return fail(AA_ERR_INVALID_ARG, "k overlaps v");
+  ReadParams P;
+  P.batch = batch_params(c, batch);
+  P.k_pages = static_cast<const uint8_t*>(c->k_pages);
+  P.v_pages = static_cast<const uint8_t*>(c->v_pages);
+  P.k_scales = c->k_scales;
+  P.v_scales = c->v_scales;
+  P.k = static_cast<__nv_bfloat16*>(k);
+  P.v = static_cast<__nv_bfloat16*>(v);
+  P.page_shift = __builtin_ctz((unsigned)c->cfg.page_size);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (c->fp8())
+    e = D == 128 ? launch_read<128, true>(P, s) : launch_read<64, true>(P, s);
+  else
+    e = D == 128 ? launch_read<128, false>(P, s) : launch_read<64, false>(P, s);
+  return e == cudaSuccess ? AA_OK : cuda_fail(e, "cache_read_kernel launch");
 }

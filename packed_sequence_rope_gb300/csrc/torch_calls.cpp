@@ -345,10 +345,10 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // cache_attend(cache, device, head_dim, q, table, cu_q, kv_len, max_q, layer, key_lo, anchor, scale, out, lse,
-//              workspace, return_lse, stream)
+//              workspace, return_lse, tree, stream)
 PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  check_count("cache_attend", n, 17);
+  check_count("cache_attend", n, 18);
   const auto cache = as_handle<aa_cache_t>(a[0]);
   const at::Device dev(at::kCUDA, (c10::DeviceIndex)as_int(a[1]));
   const int64_t D = as_int(a[2]);
@@ -359,7 +359,7 @@ PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t max_q = as_i32(a[7], "max_q");
   const aa_cache_batch batch = batch_of(a[4], a[5], a[6], T, as_i32(a[8], "layer"), dev);
   const Tensor *key_lo = given(a[9], "key_lo"), *out = given(a[12], "out"), *lse_in = given(a[13], "lse"),
-               *work_in = given(a[14], "workspace");
+               *work_in = given(a[14], "workspace"), *tree = given(a[16], "tree");
   const double scale = PyFloat_AsDouble(a[11]);
   if (scale == -1.0 && PyErr_Occurred()) throw python_error();
   const bool anchor = as_bool(a[10]), return_lse = as_bool(a[15]);
@@ -367,8 +367,16 @@ PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_kind(*key_lo, "key_lo", at::kInt, dev);
     TORCH_CHECK_VALUE(key_lo->dim() == 1 && key_lo->size(0) == T, "key_lo must have shape ", shape_text({T}));
   }
-  const OnStream on(a[16], dev);
-  Tensor lo, lse, work;
+  int64_t words = 0;
+  if (tree) {
+    check_kind(*tree, "tree", at::kLong, dev);
+    TORCH_CHECK_VALUE(tree->dim() == 2 && tree->size(0) == T && tree->size(1) >= 1 && tree->size(1) <= INT32_MAX,
+                      "tree must have shape ", shape_text({T, -1}), " with at least one word, got ", shape_text(tree->sizes()));
+    words = tree->size(1);
+  }
+  const OnStream on(a[17], dev);
+  Tensor lo, lse, work, masks;
+  if (tree) masks = tree->contiguous();
   if (key_lo) lo = key_lo->contiguous();
   Tensor o = out_or_new(out, "out", q.sizes(), at::kBFloat16, dev);
   if (lse_in || return_lse) lse = out_or_new(lse_in, "lse", {H, T}, at::kFloat, dev);
@@ -382,15 +390,97 @@ PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const Rows rq(q);
   const int status = without_gil([&] {
-    return aa_cache_attend(cache, &batch, rq.ptr, rq.stride, (int32_t)H, max_q, key_lo ? lo.const_data_ptr<int32_t>() : nullptr,
-                           anchor, (float)scale, o.mutable_data_ptr(),
-                           lse.defined() ? static_cast<float*>(lse.mutable_data_ptr()) : nullptr, work.mutable_data_ptr(),
-                           (size_t)work.numel(), on.s);
+    const int32_t* first = key_lo ? lo.const_data_ptr<int32_t>() : nullptr;
+    float* sums = lse.defined() ? static_cast<float*>(lse.mutable_data_ptr()) : nullptr;
+    if (tree)
+      return aa_cache_attend_tree(cache, &batch, rq.ptr, rq.stride, (int32_t)H, max_q, first, anchor,
+                                  static_cast<const uint64_t*>(masks.const_data_ptr()), (int32_t)words, (float)scale,
+                                  o.mutable_data_ptr(), sums, work.mutable_data_ptr(), (size_t)work.numel(), on.s);
+    return aa_cache_attend(cache, &batch, rq.ptr, rq.stride, (int32_t)H, max_q, first, anchor, (float)scale,
+                           o.mutable_data_ptr(), sums, work.mutable_data_ptr(), (size_t)work.numel(), on.s);
   });
   if (status) return PyLong_FromLong(status);
   written(out);
   written(lse_in);
   return wrap(std::move(o), return_lse ? std::move(lse) : Tensor());
+  END_HANDLE_TH_ERRORS
+}
+
+// cache_read(cache, device, Hkv, head_dim, table, cu_q, kv_len, total_tokens, layer, out_k, out_v, stream)
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count("cache_read", n, 12);
+  const auto cache = as_handle<aa_cache_t>(a[0]);
+  const at::Device dev(at::kCUDA, (c10::DeviceIndex)as_int(a[1]));
+  const int64_t H = as_int(a[2]), D = as_int(a[3]), T = as_i32(a[7], "total_tokens");
+  TORCH_CHECK_VALUE(T >= 0, "total_tokens must be >= 0");
+  const aa_cache_batch batch = batch_of(a[4], a[5], a[6], T, as_i32(a[8], "layer"), dev);
+  const Tensor *out_k = given(a[9], "out_k"), *out_v = given(a[10], "out_v");
+  const OnStream on(a[11], dev);
+  Tensor k = out_or_new(out_k, "out_k", {T, H, D}, at::kBFloat16, dev);
+  Tensor v = out_or_new(out_v, "out_v", {T, H, D}, at::kBFloat16, dev);
+  const int status = without_gil([&] { return aa_cache_read(cache, &batch, k.mutable_data_ptr(), v.mutable_data_ptr(), on.s); });
+  if (status) return PyLong_FromLong(status);
+  written(out_k);
+  written(out_v);
+  return wrap(std::move(k), std::move(v));
+  END_HANDLE_TH_ERRORS
+}
+
+// A vector of 32-bit integers on the device, contiguous.
+const Tensor& ints(PyObject* o, const char* name, int64_t size, at::Device dev) {
+  const Tensor& t = need(o, name);
+  check_kind(t, name, at::kInt, dev);
+  TORCH_CHECK_VALUE(t.dim() == 1 && t.is_contiguous() && (size < 0 || t.size(0) == size), name,
+                    " must be contiguous with shape ", shape_text({size}), ", got ", shape_text(t.sizes()));
+  return t;
+}
+
+// cache_tree_masks(cache, device, parents, cu_q, kv_len, max_q, out_mask, out_pos, stream)
+PyObject* cache_tree_masks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count("cache_tree_masks", n, 9);
+  const auto cache = as_handle<aa_cache_t>(a[0]);
+  const at::Device dev(at::kCUDA, (c10::DeviceIndex)as_int(a[1]));
+  const Tensor &parents = ints(a[2], "parents", -1, dev), &kv = ints(a[4], "kv_len", -1, dev);
+  const int64_t T = parents.size(0), B = kv.size(0);
+  const Tensor& cu = ints(a[3], "cu_q", B + 1, dev);
+  TORCH_CHECK_VALUE(B <= INT32_MAX && T <= INT32_MAX, "the batch is too large");
+  const int32_t max_q = as_i32(a[5], "max_q");
+  TORCH_CHECK_VALUE(max_q >= 0, "max_q must be >= 0");
+  const int64_t words = std::max<int64_t>(1, ((int64_t)max_q + 63) / 64);
+  const Tensor *out_mask = given(a[6], "out_mask"), *out_pos = given(a[7], "out_pos");
+  const OnStream on(a[8], dev);
+  Tensor mask = out_or_new(out_mask, "out_mask", {T, words}, at::kLong, dev);
+  Tensor pos = out_or_new(out_pos, "out_pos", {T}, at::kInt, dev);
+  const int status = without_gil([&] {
+    return aa_cache_tree_masks(cache, parents.const_data_ptr<int32_t>(), cu.const_data_ptr<int32_t>(),
+                               kv.const_data_ptr<int32_t>(), (int32_t)B, (int32_t)T, (int32_t)words,
+                               static_cast<uint64_t*>(mask.mutable_data_ptr()), pos.mutable_data_ptr<int32_t>(), on.s);
+  });
+  if (status) return PyLong_FromLong(status);
+  written(out_mask);
+  written(out_pos);
+  return wrap(std::move(mask), std::move(pos));
+  END_HANDLE_TH_ERRORS
+}
+
+// cache_accept(cache, device, table, cu_q, kv_len, path, stream)
+PyObject* cache_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count("cache_accept", n, 7);
+  const auto cache = as_handle<aa_cache_t>(a[0]);
+  const at::Device dev(at::kCUDA, (c10::DeviceIndex)as_int(a[1]));
+  const aa_cache_batch batch = batch_of(a[2], a[3], a[4], 0, 0, dev);
+  const Tensor& path = need(a[5], "path");
+  check_kind(path, "path", at::kInt, dev);
+  TORCH_CHECK_VALUE(path.dim() == 2 && path.size(0) == batch.num_seqs && path.size(1) <= INT32_MAX && path.is_contiguous(),
+                    "path must be contiguous with shape ", shape_text({batch.num_seqs, -1}), ", got ", shape_text(path.sizes()));
+  const OnStream on(a[6], dev);
+  const int status = without_gil([&] {
+    return aa_cache_accept(cache, &batch, path.const_data_ptr<int32_t>(), (int32_t)path.size(1), on.s);
+  });
+  return PyLong_FromLong(status);
   END_HANDLE_TH_ERRORS
 }
 
@@ -430,6 +520,9 @@ PyMethodDef methods[] = {
     {"rope_autograd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_autograd)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"cache_attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_attend)), METH_FASTCALL, nullptr},
+    {"cache_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_read)), METH_FASTCALL, nullptr},
+    {"cache_tree_masks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_tree_masks)), METH_FASTCALL, nullptr},
+    {"cache_accept", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_accept)), METH_FASTCALL, nullptr},
     {"cache_copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_copy_pages)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
