@@ -31,7 +31,7 @@ using namespace aa;
 //   64, 42            49.1 / 27.7  117 / 92.0  621 / 537
 // With D = 64: 64 rows of 42 sequences 24.4 / 25.0, 56.9 / 76.2 and 314 / 469.
 static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
-  if (c->fp8()) return true;
+  if (c->fp8()) return (int64_t)std::max(max_q, 1) * group <= kShortRows;
   const int64_t rows = (int64_t)std::max(max_q, 1) * group;
   if (rows <= 32 || c->cfg.head_dim == 64) return rows <= kShortRows;
   return rows <= kShortRows && (int64_t)table_width * c->cfg.page_size > kWholeKeys &&
@@ -117,7 +117,7 @@ static aa_status attend(aa_cache_t c, const aa_cache_batch* batch, const void* q
   P.page_shift = __builtin_ctz((unsigned)c->cfg.page_size);
   P.scale_log2 = (float)((softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!takes_short(c, batch->num_seqs, max_q, batch->table_width, P.group)) return launch_attend_chunk(c, P, workspace, s);
+  if (!takes_short(c, batch->num_seqs, max_q, batch->table_width, P.group)) return (c->fp8() ? launch_attend_chunk_fp8 : launch_attend_chunk)(c, P, workspace, s);
   cudaError_t e = (c->fp8() ? launch_attend_short_fp8 : launch_attend_short)(c, P, max_q, workspace, s);
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
 }

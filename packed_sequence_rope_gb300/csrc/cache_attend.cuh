@@ -155,6 +155,7 @@ cudaError_t launch_attend_short(const aa_cache_s* c, const AttendParams& P, int 
 cudaError_t launch_attend_short_fp8(const aa_cache_s* c, const AttendParams& P, int max_q, void* workspace, cudaStream_t s);
 size_t short_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int max_q, int table_width, int group);
 aa_status launch_attend_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
+aa_status launch_attend_chunk_fp8(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
 size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int table_width, int group);
 
 }  // namespace aa
