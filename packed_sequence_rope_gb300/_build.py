@@ -21,7 +21,7 @@ CALLS_FOR = os.path.join(BUILD, "calls_for.txt")  # what _calls.so was compiled 
 SOURCES = ["plan.cpp", "rope.cu", "fwd.cu", "bwd.cu", "bwd_static.cu", "shift_diag.cu", "segments.cu",
            "rope_axes.cu", "cache.cpp", "cache_io.cu", "cache_attend.cu",
            "cache_attend_short.cu", "cache_attend_short_fp8.cu", "cache_attend_chunk.cu",
-           "cache_attend_chunk_fp8.cu", "cache_tree.cu"]
+           "cache_attend_chunk_fp8.cu", "cache_attend_wide.cu", "cache_tree.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -31,11 +31,32 @@ using namespace aa;
 //   64, 42            49.1 / 27.7  117 / 92.0  621 / 537
 // With D = 64: 64 rows of 42 sequences 24.4 / 25.0, 56.9 / 76.2 and 314 / 469.
 static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
-  if (c->fp8()) return (int64_t)std::max(max_q, 1) * group <= kShortRows;
   const int64_t rows = (int64_t)std::max(max_q, 1) * group;
   if (rows <= 32 || c->cfg.head_dim == 64) return rows <= kShortRows;
   return rows <= kShortRows && (int64_t)table_width * c->cfg.page_size > kWholeKeys &&
          (int64_t)num_seqs * c->cfg.num_kv_heads < 64;
+}
+
+// 8-bit pages: the kernel of few rows makes codes bf16 once per 16 rows, the chunk kernel
+// once per 128; with more rows the codes are made bf16 ahead of the chunk kernel of 16-bit
+// pages. Measured, microseconds of the three, 8 kv heads of 128, group 4:
+//   rows, sequences   300 keys             2048                 16384
+//   32, 1             14.6 / 16.5 / 18.6   14.6 / 22.4 / 24.7   28.9 / 37.8 / 51.6
+//   32, 42            41.2 / 39.3 / 47.9   99.0 / 137 / 181     597 / 802 / 1236
+//   64, 1             22.0 / 16.5 / 18.6   22.7 / 22.8 / 25.6   45.3 / 39.1 / 53.4
+//   64, 42            67.9 / 42.4 / 47.7   193 / 139 / 184      1258 / 804 / 1239
+//   128, 42           131 / 58.3 / 49.6    373 / 143 / 187      2512 / 809 / 1247
+//   256, 1            71.8 / 16.8 / 20.9   78.0 / 25.0 / 28.8   156 / 59.6 / 56.7
+//   256, 42           248 / 68.4 / 72.4    735 / 260 / 206      5030 / 1584 / 1294
+enum Path { kShort, kChunk, kShortCodes, kChunkCodes, kWide };
+
+static Path path_of(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
+  if (!c->fp8()) return takes_short(c, num_seqs, max_q, table_width, group) ? kShort : kChunk;
+  const int64_t rows = (int64_t)std::max(max_q, 1) * group;
+#ifdef AA_TUNE
+  if (const char* e = getenv("AA_PATH")) return e[0] == 's' ? kShortCodes : e[0] == 'c' ? kChunkCodes : kWide;
+#endif
+  return rows <= 32 ? kShortCodes : rows <= 128 || !wide_fits(c, table_width) ? kChunkCodes : kWide;
 }
 
 extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
@@ -44,9 +65,13 @@ extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs
   const int Hkv = c->cfg.num_kv_heads;
   if (c->host_only || q_heads % Hkv || q_heads / Hkv > 64) return 0;
   if (total_tokens >= (1 << 30) || num_seqs > (1 << 20) || (int64_t)table_width * c->cfg.page_size >= (1ll << 30)) return 0;
-  if (takes_short(c, num_seqs, max_q, table_width, q_heads / Hkv))
-    return short_workspace_bytes(c, num_seqs, total_tokens, max_q, table_width, q_heads / Hkv);
-  return chunk_workspace_bytes(c, num_seqs, total_tokens, table_width, q_heads / Hkv);
+  const int group = q_heads / Hkv;
+  switch (const Path path = path_of(c, num_seqs, max_q, table_width, group)) {
+    case kShort:
+    case kShortCodes: return short_workspace_bytes(c, num_seqs, total_tokens, max_q, table_width, group);
+    case kWide: return wide_workspace_bytes(c, num_seqs, total_tokens, table_width, group);
+    default: return chunk_workspace_bytes(c, num_seqs, total_tokens, table_width, group, path == kChunkCodes);
+  }
 }
 
 static aa_status attend(aa_cache_t c, const aa_cache_batch* batch, const void* q, int64_t q_stride, int32_t q_heads,
@@ -117,8 +142,11 @@ static aa_status attend(aa_cache_t c, const aa_cache_batch* batch, const void* q
   P.page_shift = __builtin_ctz((unsigned)c->cfg.page_size);
   P.scale_log2 = (float)((softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!takes_short(c, batch->num_seqs, max_q, batch->table_width, P.group)) return (c->fp8() ? launch_attend_chunk_fp8 : launch_attend_chunk)(c, P, workspace, s);
-  cudaError_t e = (c->fp8() ? launch_attend_short_fp8 : launch_attend_short)(c, P, max_q, workspace, s);
+  const Path path = path_of(c, batch->num_seqs, max_q, batch->table_width, P.group);
+  if (path == kChunk) return launch_attend_chunk(c, P, workspace, s);
+  if (path == kChunkCodes) return launch_attend_chunk_fp8(c, P, workspace, s);
+  if (path == kWide) return launch_attend_wide(c, P, workspace, s);
+  cudaError_t e = (path == kShort ? launch_attend_short : launch_attend_short_fp8)(c, P, max_q, workspace, s);
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_short_kernel launch");
 }
 

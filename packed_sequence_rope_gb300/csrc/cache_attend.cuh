@@ -156,6 +156,11 @@ cudaError_t launch_attend_short_fp8(const aa_cache_s* c, const AttendParams& P, 
 size_t short_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int max_q, int table_width, int group);
 aa_status launch_attend_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
 aa_status launch_attend_chunk_fp8(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
-size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int table_width, int group);
+size_t chunk_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int table_width, int group, bool from_codes);
+// 8-bit pages by way of 16-bit copies of a few sequences at a time, kWideBytes at most.
+constexpr size_t kWideBytes = 1ull << 30;
+bool wide_fits(const aa_cache_s* c, int table_width);
+size_t wide_workspace_bytes(const aa_cache_s* c, int num_seqs, int total_tokens, int table_width, int group);
+aa_status launch_attend_wide(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s);
 
 }  // namespace aa

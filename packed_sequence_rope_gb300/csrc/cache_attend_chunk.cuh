@@ -33,11 +33,15 @@
 // PV0(j), S0(j + 1), PV1(j), S1(j + 1) keeps the tensor cores busy with one tile
 // while the other's softmax runs.
 //
-// 8-bit pages (k8): warps 2, 3, 20 and 21 make each tile of codes bf16, scales included, in
-// the buffer that it was copied to, so that the products and the softmax are those of
-// 16-bit pages. The codes are copied to the buffer's second half. What becomes its first half
-// is converted at once, the rest held in registers until all of it has been read. The
-// values that no row sees become zeros on the way.
+// 8-bit pages (k8): a unit is one row tile. Warps 12-15 make the tiles of keys bf16,
+// scales included, warps 16-19 the values, so that the products and the softmax are those
+// of 16-bit pages. The codes come in halves of a tile, through buffers of their own. The
+// values that no row sees become zeros on the way, and warps 2 and 3 have nothing to do.
+// Converting costs about as many instructions as the softmax of a row tile, so the second
+// row tile's warps do it; four more warps beside them leave 80 registers a thread, which
+// the softmax does not fit. The loops are kept rolled: their code, the softmax's and the
+// issue loop's run at the same time and share the instruction cache (unrolled, five of
+// six cycles of a warp passed waiting for instructions).
 #pragma once
 
 #include <algorithm>
@@ -49,11 +53,14 @@ namespace {
 
 constexpr int kKeys = 128;
 constexpr int kSoftmaxWarps = 16;
-constexpr int kConvertWarps = 4;
-template <bool k8>
-constexpr int kThreads = 32 * (4 + kSoftmaxWarps + (k8 ? kConvertWarps - 2 : 0));
-template <bool k8>  // of a published piece: all warps but the first
-constexpr int kReaders = kThreads<k8> / 32 - 1;
+constexpr int kThreads = 32 * (4 + kSoftmaxWarps);
+// Where keys and values are read: 16-bit pages, 8-bit pages, or what wide_kernel has made of 8-bit pages.
+enum ChunkFrom { kFromPages, kFromCodes, kFromWide };
+constexpr int kConvertWarps = 4;             // for keys, and as many for values
+template <bool k8>  // of a published piece: all warps but the first; with 8-bit pages without warps 2 and 3
+constexpr int kReaders = kThreads / 32 - (k8 ? 3 : 1);
+// Row tiles of a unit.
+inline __host__ __device__ constexpr int tiles_of(bool k8) { return k8 ? 1 : 2; }
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
@@ -81,6 +88,8 @@ struct alignas(16) Cut {
 struct ChunkParams {
   AttendParams a;
   int tile_tokens;     // tokens per row tile: 128 / group
+  int unit_tokens;     // tokens per unit
+  int wide_keys;       // kFromWide: rows of a sequence and kv head
   int slots;           // room for the units of one kv head
   int ctas;            // of the attention kernel, unless it takes whole units
   int whole_units;     // short contexts: CTAs take whole units, there is no plan and nothing to join
@@ -94,12 +103,12 @@ struct ChunkParams {
 // ---------------------------------------------------------------- the plan
 // The unit of a slot and its number of key tiles; no tokens and 0 if the slot is
 // empty (a whole warp asks). Sequence b's units start at slot
-// cu_q[b] / (2 tile_tokens) + b, which leaves room for a rounded-up count and
+// cu_q[b] / unit_tokens + b, which leaves room for a rounded-up count and
 // needs no scan over the sequences before it.
 __device__ __forceinline__ Unit load_unit(const ChunkParams& C, int slot, int* count) {
   const AttendParams& P = C.a;
   const BatchParams& b = P.batch;
-  const int lane = threadIdx.x & 31, unit_tokens = 2 * C.tile_tokens;
+  const int lane = threadIdx.x & 31, unit_tokens = C.unit_tokens;
   const int seq = warp_last(b.B, [&](int i) { return __ldg(b.cu_q + i) / unit_tokens + i <= slot; });
   const SeqSpan s = load_seq(b, seq, P.page_shift);
   const int64_t i0 = (int64_t)(slot - __ldg(b.cu_q + seq) / unit_tokens - seq) * unit_tokens;
@@ -210,12 +219,15 @@ struct ChunkSmem {
   static constexpr int kStages = HD == 128 ? 2 : 4;
   // a piece's two row tiles of Q and one of the next piece: its first S product
   // does not wait for a copy
-  static constexpr int kQ = 3;
+  static constexpr int kQ = k8 ? 2 : 3;
   alignas(1024) uint8_t q[kQ][kB][16384];
   alignas(1024) uint8_t k[kStages][kB][16384];
   alignas(1024) uint8_t v[kStages][kB][16384];
-  alignas(16) uint8_t k_scales[kStages][k8 ? kKeys : 16], v_scales[kStages][k8 ? kKeys : 16];
-  uint64_t k_ready[kStages];  // 8-bit pages: the keys are bf16
+  // 8-bit pages: codes of half a tile, keys (0) and values (1), and their scales
+  alignas(1024) uint8_t codes[2][k8 ? 2 : 1][k8 ? kKeys / 2 * HD : 16];
+  alignas(16) uint8_t scales[2][k8 ? 2 : 1][k8 ? kKeys / 2 : 16];
+  uint64_t c_full[2][2], c_empty[2][2];
+  uint64_t k_ready[kStages];  // the keys are bf16
   uint64_t q_full[kQ], q_free[kQ];
   uint64_t piece_full[2], piece_empty[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
@@ -230,6 +242,8 @@ struct ChunkSmem {
   uint32_t tmem_base;
   int abort_flag;
 };
+
+static_assert(sizeof(ChunkSmem<128, true>) <= 232448 && sizeof(ChunkSmem<128, false>) <= 232448, "what a CTA can have");
 
 // A converged warp waits, bounded, and gives up with the rest of the CTA. One lane
 // asks for all. (A suspend-time hint on the question costs wake-up time: 871 us
@@ -269,65 +283,33 @@ __device__ __forceinline__ uint32_t visible_bits(int j, int lo, int hi) {
   return first <= 0 ? upto : first > 31 ? 0u : upto & (~0u << first);
 }
 
-// One tile of 8-bit pages, kKeys rows of codes in the second half of `tile`, becomes bf16
-// in its place, by kConvertWarps warps (thread tc of them). row_scale(row) is the row's scale
-// byte, or -1 for zeros. False if a warp gives up.
-template <int HD, class RowScale>
-__device__ __forceinline__ bool convert_tile(uint8_t* tile, int tc, bool ok, RowScale row_scale) {
-  constexpr int kHalves = 2, kAtOnce = HD / 32;  // 16-byte chunks of codes a thread takes in each half
-  const uint8_t* codes = tile + kKeys * HD;
+// Half a tile of codes becomes rows [row0, row0 + 64) of a bf16 tile, by kConvertWarps
+// warps (thread tc of them). Rows whose bit of `seen` is 0 become zeros.
+template <int HD>
+__device__ __forceinline__ void convert_half(const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int row0, int tc,
+                                             uint64_t seen) {
+  constexpr int kPerRow = HD / 64, kChunks = kKeys / 2 * HD / 16 / (32 * kConvertWarps);  // 16-byte chunks of codes a thread takes
   // Eight lanes take four chunks of rows r and r ^ 5: they meet eight different groups of
   // banks in both swizzles, where they read and where they write.
   const int c = tc & 3, flip = tc & 4 ? 5 : 0, r0 = tc >> 3 << 1;
-  uint4 held[kAtOnce];
-  auto row_of = [&](int half, int i) { return (HD == 128 ? i * 32 + r0 : half * 64 + i * 32 + r0) ^ flip; };
-  auto load = [&](int half, int i) {
-    const int row = row_of(half, i);
-    return *reinterpret_cast<const uint4*>(
-        codes + (HD == 128 ? sw128_chunk(row, half * 4 + c) : (uint32_t)(row * 64 + ((c ^ (row >> 1 & 3)) << 4))));
-  };
-  auto store = [&](int half, int i, const uint4& x) {
-    const int row = row_of(half, i), scale = row_scale(row);
-    // 2^-120 times the code (as in e4m3x4_to_bf16) times 2^120 times the scale, 2^(scale - 7);
-    // in two factors where bf16 does not reach
-    const uint32_t up = scale == 255 ? 0x7fc0u : (uint32_t)min(scale + 120, 254) << 7;
-    const uint32_t up2 = up | up << 16;
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t four = e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w;
-      const uint32_t y = __byte_perm(four, 0u, e & 1 ? 0x3424 : 0x1404);  // two codes in the high bytes of 16-bit halves
-      const uint32_t b = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
-      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[e]) : "r"(b), "r"(up2));
-    }
-    if (scale > 134 && scale < 255) {
-      const uint32_t more = (uint32_t)(scale - 7) << 7, more2 = more | more << 16;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[e]) : "r"(w[e]), "r"(more2));
-    }
-    if (scale < 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 0;
-    }
-    uint8_t* out = tile + (HD == 128 ? half * 16384 : 0);
-    *reinterpret_cast<uint4*>(out + sw128_chunk(row, 2 * c)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(out + sw128_chunk(row, 2 * c + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
-  };
-  if (ok) {
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) held[i] = load(0, i);
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const uint4 x = held[i];
-      held[i] = load(1, i);
-      store(0, i, x);
-    }
+#pragma unroll 4
+  for (int i = 0; i < kChunks; ++i) {
+    const int row = (i / kPerRow * 32 + r0) ^ flip, block = i % kPerRow;
+    const uint4 x = *reinterpret_cast<const uint4*>(
+        codes + (HD == 128 ? sw128_chunk(row, block * 4 + c) : (uint32_t)(row * 64 + ((c ^ (row >> 1 & 3)) << 4))));
+    uint4 y[2];
+    decode16(x, scales[row], !(seen >> row & 1), y);
+    uint8_t* out = tile + block * 16384;
+    *reinterpret_cast<uint4*>(out + sw128_chunk(row0 + row, 2 * c)) = y[0];
+    *reinterpret_cast<uint4*>(out + sw128_chunk(row0 + row, 2 * c + 1)) = y[1];
   }
-  if (!ptx::bar_and(9, 32 * kConvertWarps, ok)) return false;  // all codes have been read
-#pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) store(1, i, held[i]);
-  static_assert(kHalves * kAtOnce * 16 * 32 * kConvertWarps == kKeys * HD, "every code once");
-  return true;
+}
+
+// Bit x: key j + x lies in [lo, hi], x < 64.
+__device__ __forceinline__ uint64_t keys_between(int j, int lo, int hi) {
+  const int last = hi - j, first = lo - j;
+  const uint64_t upto = last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1ull;
+  return first <= 0 ? upto : first > 63 ? 0ull : upto & (~0ull << first);
 }
 
 // Barrier phases: pieces count the piece ring; the K and V rings count the
@@ -335,11 +317,12 @@ __device__ __forceinline__ bool convert_tile(uint8_t* tile, int tc, bool ok, Row
 // softmax steps; q_full and q_free the CTA's row tiles of Q; o_full the pieces
 // in which the row tile exists. As in the packed forward every wait is bounded and its outcome made
 // uniform in a warp before anything collective.
-template <int HD, bool kTree, bool k8>
-__global__ void __launch_bounds__(kThreads<k8>, 1)
+template <int HD, bool kTree, int kFrom>
+__global__ void __launch_bounds__(kThreads, 1)
     attend_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ChunkParams C) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  constexpr bool k8 = kFrom == kFromCodes;
   using Smem = ChunkSmem<HD, k8>;
   constexpr int kB = HD / 64, kStages = Smem::kStages, kQ = Smem::kQ, kTmemCols = 512;
   constexpr uint32_t kTileBytes = kKeys * HD * 2;
@@ -376,6 +359,10 @@ __global__ void __launch_bounds__(kThreads<k8>, 1)
       ptx::mbar_init(&sm.k_ready[s], kConvertWarps);
       ptx::mbar_init(&sm.v_clean[s], k8 ? kConvertWarps : 2);
     }
+    for (int s = 0; s < 4; ++s) {
+      ptx::mbar_init(&sm.c_full[s >> 1][s & 1], 1);
+      ptx::mbar_init(&sm.c_empty[s >> 1][s & 1], kConvertWarps);
+    }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     ptx::fence_mbar_init();
@@ -399,6 +386,7 @@ __global__ void __launch_bounds__(kThreads<k8>, 1)
     }
     Cut cut{-1, 0, 0, 0};
     int nq = 0, ks = 0, nk = 0;  // row tiles of Q, key tiles whose V, whose K has been asked for
+    int nc[2][2] = {{0, 0}, {0, 0}};  // 8-bit pages: halves of each buffer
     bool ok = true;
     // a key tile is `pieces` page pieces, each kB column blocks of K, then of V
     const int piece_shift = min(P.page_shift, 6), pieces = kKeys >> piece_shift;
@@ -461,42 +449,49 @@ __global__ void __launch_bounds__(kThreads<k8>, 1)
         const int j = keys.tile(i) * kKeys + (part << piece_shift);
         // pieces that no row sees are not looked up (lo > hi: the rows see the anchor at most)
         const bool seen = j <= hi && ((w.lo <= hi && j + (1 << piece_shift) > w.lo) || (j == 0 && anchor));
-        return lane < copies && i < w.first + w.take && i < keys.count && seen ? pool_row(b, w.seq, w.g, j, P.page_shift)
-                                                                               : kNoRow;
+        if (!(lane < copies && i < w.first + w.take && i < keys.count && seen)) return kNoRow;
+        return kFrom == kFromWide ? (int)((w.seq * b.Hkv + w.g) * C.wide_keys + j) : pool_row(b, w.seq, w.g, j, P.page_shift);
       };
       int next = row_of(w.first);
       auto load_keys = [&](int i) {
         const int s = ks % kStages, row = next;
         next = row_of(i + 1);  // in flight while this stage is waited for
-        // K's buffer is free one product earlier than V's, and V is wanted later
-        for (int v = 0; v < 2; ++v) {
-          uint64_t* full = v ? &sm.v_full[s] : &sm.k_full[s];
-          if (ks >= kStages)
-            ok = warp_wait(v ? &sm.v_empty[s] : &sm.k_empty[s], ((ks / kStages) - 1) & 1, b.err,
-                                                       abort_flag, 451);
-          if (!ok) return;
-          if constexpr (k8) {
-            // the scales of pieces that are not looked up: zeros, as their codes will be
-            const bool none = lane < copies && row < 0;
-            uint8_t* scales = (v ? sm.v_scales[s] : sm.k_scales[s]) + (part << piece_shift);
-            if (none)
-              for (int x = 0; x < 1 << piece_shift; x += 16) *reinterpret_cast<uint4*>(scales + x) = make_uint4(0, 0, 0, 0);
-            const int scaled = __popc(__ballot_sync(0xffffffffu, lane < copies && row >= 0));
-            if (lane == 0) ptx::mbar_arrive_expect_tx(full, kTileBytes / 2 + (uint32_t)(scaled << piece_shift));
-            __syncwarp();
-            if (lane < copies) {
-              ptx::tma_load_2d((v ? sm.v[s][0] : sm.k[s][0]) + kTileBytes / 2 + (part << piece_shift) * HD, v ? &tmV : &tmK,
-                               full, 0, row);
-              if (!none) ptx::bulk_load(scales, (v ? P.v_scales : P.k_scales) + row, 1u << piece_shift, full);
+        if constexpr (k8) {
+          for (int h = 0; h < 2; ++h)
+            for (int v = 0; v < 2; ++v) {
+              if (ks > 0) ok = warp_wait(&sm.c_empty[v][h], (ks - 1) & 1, b.err, abort_flag, 451);
+              if (!ok) return;
+              const bool mine = lane < copies && part / (pieces / 2) == h;
+              const int at = (part - h * (pieces / 2)) << piece_shift;
+              uint8_t* scales = sm.scales[v][h] + at;
+              // the scales of pieces that are not looked up: zeros, as their codes will be
+              if (mine && row < 0)
+                for (int x = 0; x < 1 << piece_shift; x += 16) *reinterpret_cast<uint4*>(scales + x) = make_uint4(0, 0, 0, 0);
+              const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
+              if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][h], kTileBytes / 4 + (uint32_t)(scaled << piece_shift));
+              __syncwarp();
+              if (mine) {
+                ptx::tma_load_2d(sm.codes[v][h] + at * HD, v ? &tmV : &tmK, &sm.c_full[v][h], 0, row);
+                if (row >= 0)
+                  ptx::bulk_load(scales, (v ? P.v_scales : P.k_scales) + row, 1u << piece_shift, &sm.c_full[v][h]);
+              }
+              nc[v][h] = ks + 1;
             }
-          } else {
+        } else {
+          // K's buffer is free one product earlier than V's, and V is wanted later
+          for (int v = 0; v < 2; ++v) {
+            uint64_t* full = v ? &sm.v_full[s] : &sm.k_full[s];
+            if (ks >= kStages)
+              ok = warp_wait(v ? &sm.v_empty[s] : &sm.k_empty[s], ((ks / kStages) - 1) & 1, b.err,
+                                                         abort_flag, 451);
+            if (!ok) return;
             if (lane == 0) ptx::mbar_arrive_expect_tx(full, kTileBytes);
             __syncwarp();
             if (lane < copies)
               ptx::tma_load_2d((v ? sm.v[s][block] : sm.k[s][block]) + (part << piece_shift) * 128, v ? &tmV : &tmK, full,
                                block * 64, row);
+            if (v == 0) nk = ks + 1;
           }
-          if (v == 0) nk = ks + 1;
         }
         ++ks;
       };
@@ -520,6 +515,11 @@ __global__ void __launch_bounds__(kThreads<k8>, 1)
     // every issued copy lands before the CTA exits
     for (int u = max(nq - kQ, 0); u < nq; ++u)
       ptx::mbar_wait(&sm.q_full[u % kQ], (u / kQ) & 1, kDrainNs, b.err, 459);
+    if constexpr (k8) {
+      for (int x = 0; x < 4; ++x)
+        if (nc[x >> 1][x & 1] > 0) ptx::mbar_wait(&sm.c_full[x >> 1][x & 1], (nc[x >> 1][x & 1] - 1) & 1, kDrainNs, b.err, 459);
+      ks = nk = 0;
+    }
     for (int u = max(nk - kStages, 0); u < nk; ++u)
       ptx::mbar_wait(&sm.k_full[u % kStages], (u / kStages) & 1, kDrainNs, b.err, 459);
     for (int u = max(ks - kStages, 0); u < ks; ++u)
@@ -597,47 +597,43 @@ __global__ void __launch_bounds__(kThreads<k8>, 1)
     __syncwarp();
     ptx::mma_commit_warp(&sm.drain);
     ptx::mbar_wait(&sm.drain, 0, kDrainNs, b.err, 469);
-  } else if (k8 && (warp < 4 || warp >= 4 + kSoftmaxWarps)) {
-    // ------------------------------------------------------------ codes to bf16
-    const int tc = tid - 32 * (warp < 4 ? 2 : 2 + kSoftmaxWarps);
+  } else if (k8 && warp < 4) {
+  } else if (k8 && warp >= 12) {
+    // ------------------------------------------------------------ codes to bf16: keys (warps 12-15), values (16-19)
+    const int v = warp >= 16, tc = tid & (32 * kConvertWarps - 1);
     int ks = 0;
-    for (int li = 0;; ++li) {
+    bool ok = true;
+    for (int li = 0; ok; ++li) {
       Piece w;
-      const bool got = read_piece(sm, li, b.err, abort_flag, 470, &w);
-      if (!ptx::bar_and(9, 32 * kConvertWarps, got)) break;
-      const int hi = w.hi;
+      if (!read_piece(sm, li, b.err, abort_flag, 470, &w)) break;
       const bool anchor = P.anchor && (!kTree || w.gaps > 0);
-      const KeyTiles<kKeys> keys(w.lo, hi, anchor);
-      bool ok = true;
+      const KeyTiles<kKeys> keys(w.lo, w.hi, anchor);
       for (int i = w.first; i < w.first + w.take; ++i, ++ks) {
         const int s = ks % kStages, j0 = keys.tile(i) * kKeys;
-        ok = warp_wait(&sm.k_full[s], (ks / kStages) & 1, b.err, abort_flag, 471);
-        if (!(ok = convert_tile<HD>(sm.k[s][0], tc, ok, [&](int row) { return (int)sm.k_scales[s][row]; }))) break;
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.k_ready[s]);
-        // Values that no row sees have weight 0, but 0 * NaN is not: they become zeros. These are
-        // the rows outside [lo, hi] but for the anchor's, and where rows of the unit see
-        // nothing (or of a tree some only) those of the new tokens that none of them sees.
-        uint64_t some[2] = {~0ull, ~0ull};
-        if (kTree ? j0 + kKeys > w.gaps : w.gaps && j0 + kKeys - 1 > w.p0) {
+        if (ks >= kStages) ok = warp_wait(v ? &sm.v_empty[s] : &sm.k_empty[s], (ks / kStages - 1) & 1, b.err, abort_flag, 473);
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x)
-            some[x] = kTree ? tree_seen_keys(P, w.q_row, w.p0 - w.gaps, w.tokens, w.gaps, hi + 1 - w.gaps, j0 + 64 * x)
-                            : seen_keys(P, w.q_row, w.p0, w.tokens, j0 + 64 * x);
+        for (int h = 0; h < 2 && ok; ++h) {
+          // Values that no row sees have weight 0, but 0 * NaN is not: they become zeros. These are
+          // the rows outside [lo, hi] but for the anchor's, and where rows of the unit see
+          // nothing (or of a tree some only) those of the new tokens that none of them sees.
+          const int j = j0 + 64 * h;
+          uint64_t seen = ~0ull;
+          if (v) {
+            seen = keys_between(j, w.lo, w.hi) | (j == 0 && anchor && w.hi >= 0 ? 1ull : 0ull);
+            if (kTree ? j + 64 > w.gaps : w.gaps && j + 63 > w.p0)
+              seen &= kTree ? tree_seen_keys(P, w.q_row, w.p0 - w.gaps, w.tokens, w.gaps, w.hi + 1 - w.gaps, j)
+                            : seen_keys(P, w.q_row, w.p0, w.tokens, j);
+          }
+          if (!(ok = warp_wait(&sm.c_full[v][h], ks & 1, b.err, abort_flag, 471))) break;
+          convert_half<HD>(sm.codes[v][h], sm.scales[v][h], v ? sm.v[s][0] : sm.k[s][0], 64 * h, tc, seen);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.c_empty[v][h]);
         }
-        ok = warp_wait(&sm.v_full[s], (ks / kStages) & 1, b.err, abort_flag, 472);
-        ok = convert_tile<HD>(sm.v[s][0], tc, ok, [&](int row) {
-          const int j = j0 + row;
-          const bool seen = ((j >= w.lo && j <= hi) || (j == 0 && anchor && hi >= 0)) && ((row < 64 ? some[0] : some[1]) >> (row & 63) & 1);
-          return seen ? (int)sm.v_scales[s][row] : -1;
-        });
         if (!ok) break;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.v_clean[s]);
+        if (lane == 0) ptx::mbar_arrive(v ? &sm.v_clean[s] : &sm.k_ready[s]);
       }
-      if (!ok) break;
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ clearing unseen values (warps 2 and 3)
@@ -1039,15 +1035,19 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) chunk_join_kernel(c
 // ---------------------------------------------------------------- launches
 inline int ctas_for(const aa_cache_s* c) { return std::min(c->num_sms, kMaxCtas); }
 inline bool whole_units(int table_width, int page_shift) { return ((int64_t)table_width << page_shift) <= kWholeKeys; }
-inline int slots_for(int tokens, int seqs, int tile_tokens) { return tokens / (2 * tile_tokens) + seqs; }
+inline int slots_for(int tokens, int seqs, int unit_tokens) { return tokens / unit_tokens + seqs; }
 
-template <int HD, bool kTree, bool k8>
-aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {
+template <int HD, bool kTree, int kFrom>
+aa_status launch(const aa_cache_s* c, const AttendParams& P, const CUtensorMap& k_map, const CUtensorMap& v_map, int wide_keys,
+                 void* workspace, cudaStream_t s) {
+  constexpr bool k8 = kFrom == kFromCodes;
   const BatchParams& b = P.batch;
   ChunkParams C;
   C.a = P;
   C.tile_tokens = 128 / P.group;
-  C.slots = slots_for(b.T, b.B, C.tile_tokens);
+  C.unit_tokens = tiles_of(k8) * C.tile_tokens;
+  C.wide_keys = wide_keys;
+  C.slots = slots_for(b.T, b.B, C.unit_tokens);
   C.whole_units = whole_units(b.W, P.page_shift);
   const int ctas = ctas_for(c);
   C.ctas = ctas;
@@ -1071,7 +1071,7 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   CUtensorMap tq;
   aa_status st = make_query_map(&tq, P.q, b.T, P.q_stride, b.Hkv, P.group, HD, C.tile_tokens);
   if (st != AA_OK) return st;
-  const auto kernel = attend_chunk_kernel<HD, kTree, k8>;
+  const auto kernel = attend_chunk_kernel<HD, kTree, kFrom>;
   const size_t smem = sizeof(ChunkSmem<HD, k8>);
   static std::once_flag once[kMaxDevices];
   static cudaError_t result[kMaxDevices];
@@ -1081,12 +1081,12 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel smem attribute");
   if (C.whole_units) {
     const unsigned grid = (unsigned)std::min<int64_t>((int64_t)C.slots * b.Hkv, ctas);
-    e = launch_after(kernel, dim3(grid), kThreads<k8>, smem, s, tq, c->k_map64, c->v_map64, C);
+    e = launch_after(kernel, dim3(grid), kThreads, smem, s, tq, k_map, v_map, C);
     return e == cudaSuccess ? AA_OK : cuda_fail(e, "attend_chunk_kernel launch");
   }
   chunk_plan_kernel<<<1, 1024, 0, s>>>(C);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "chunk_plan_kernel launch");
-  e = launch_after(kernel, dim3((unsigned)ctas), kThreads<k8>, smem, s, tq, c->k_map64, c->v_map64, C);
+  e = launch_after(kernel, dim3((unsigned)ctas), kThreads, smem, s, tq, k_map, v_map, C);
   if (e != cudaSuccess) return cuda_fail(e, "attend_chunk_kernel launch");
   const bool few = (int64_t)C.slots * b.Hkv * kHelpParts <= ctas && ((int64_t)b.W << P.page_shift) > kHelpKeys;
   static_assert(256 / kJoinRows <= kHelpParts * kJoinBlocks, "a block for each piece of the few units");
@@ -1096,11 +1096,14 @@ aa_status launch(const aa_cache_s* c, const AttendParams& P, void* workspace, cu
   return AA_OK;
 }
 
-template <bool k8>
-aa_status launch_chunk(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {
+template <int kFrom>
+aa_status launch_chunk(const aa_cache_s* c, const AttendParams& P, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                       int wide_keys, void* workspace, cudaStream_t s) {
   if (P.tree)
-    return c->cfg.head_dim == 128 ? launch<128, true, k8>(c, P, workspace, s) : launch<64, true, k8>(c, P, workspace, s);
-  return c->cfg.head_dim == 128 ? launch<128, false, k8>(c, P, workspace, s) : launch<64, false, k8>(c, P, workspace, s);
+    return c->cfg.head_dim == 128 ? launch<128, true, kFrom>(c, P, k_map, v_map, wide_keys, workspace, s)
+                                  : launch<64, true, kFrom>(c, P, k_map, v_map, wide_keys, workspace, s);
+  return c->cfg.head_dim == 128 ? launch<128, false, kFrom>(c, P, k_map, v_map, wide_keys, workspace, s)
+                                : launch<64, false, kFrom>(c, P, k_map, v_map, wide_keys, workspace, s);
 }
 
 }  // namespace

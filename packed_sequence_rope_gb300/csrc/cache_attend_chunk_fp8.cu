@@ -4,7 +4,7 @@
 namespace aa {
 
 aa_status launch_attend_chunk_fp8(const aa_cache_s* c, const AttendParams& P, void* workspace, cudaStream_t s) {
-  return launch_chunk<true>(c, P, workspace, s);
+  return launch_chunk<kFromCodes>(c, P, c->k_map64, c->v_map64, 0, workspace, s);
 }
 
 }  // namespace aa

@@ -227,18 +227,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       const uint8_t* pages = h < b.Hkv ? P.k_pages : P.v_pages;
       if constexpr (k8) {
         const uint4 x = *reinterpret_cast<const uint4*>(pages + from * HD + 16 * chunk);
-        const float up = scale_of((h < b.Hkv ? P.k_scales : P.v_scales)[from]);
-        const uint32_t c[4] = {x.x, x.y, x.z, x.w};
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint2 v = e4m3x4_to_bf16(c[e]);  // codes (0, 2), (1, 3)
-          const float2 even = ptx::unpack_bf16x2(v.x), odd = ptx::unpack_bf16x2(v.y);
-          w[2 * e] = ptx::pack_bf16x2(even.x * up, odd.x * up);
-          w[2 * e + 1] = ptx::pack_bf16x2(even.y * up, odd.y * up);
-        }
-        y[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        y[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        decode16(x, (h < b.Hkv ? P.k_scales : P.v_scales)[from], false, y);
       } else {
         const uint4* x = reinterpret_cast<const uint4*>(pages + (from * HD + 16 * chunk) * 2);
         y[0] = x[0];
