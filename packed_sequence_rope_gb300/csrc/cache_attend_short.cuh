@@ -19,13 +19,20 @@
 // not fill the GPU (one user with a long context), each unit gets several
 // clusters; their results go to the workspace and a second kernel joins them.
 //
-// 8-bit pages (k8) take the same path at half of the bytes. A key's 16 codes of a
-// product step are one 16-byte row of a matrix load, 4 codes per lane; made bf16 they
-// are the step's operand with its channels in another order, which the queries'
-// operand shares. Loaded transposed, a lane's codes are two channels of two keys:
-// operands of two products, for the even and the odd channels. The keys' scales
-// multiply the logits, the values' the weights: powers of two, so that both are what
-// they were with the values themselves.
+// 8-bit pages (k8) take the same path at half of the bytes; what bounds it then is the
+// work on each key. A key's 16 codes of a product step are one 16-byte row of a matrix
+// load, 4 codes per lane; made f16 (one conversion for two codes, exact; to bf16 there
+// is none, and its four bit operations and a product made a decoding step of 64
+// sequences to 32K keys 627 us) they are the step's operand with its channels in another
+// order, which the queries' operand shares. Loaded transposed, a lane's codes are two
+// channels of two keys: operands of two products, for the even and the odd channels.
+// The other operands are f16 then, within its range by powers of two: a row of queries
+// times the one that brings its maximum to 2^14, which keeps every value down to 2^-39 of it exact; and
+// the weights. The keys' scales multiply the logits. A value's scale 2^e joins its weight,
+// 2^(s + e - m) with m the row's running maximum of s + e, so that weights lie below 2^15,
+// are rounded to 11 bits down to 2^-21 of the largest at least, and to multiples of 2^-24 of 2^7 below:
+// the weights smaller than that take 2^-32 of the largest value times weight each at most out of
+// the result. Their sum has its own maximum, since scales of tokens may lie far apart.
 #pragma once
 
 #include "cache_attend.cuh"
@@ -36,6 +43,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
+
+constexpr float kWeightsUp = 7.0f;      // 8-bit pages: weights are 2^7 times what the maximum gives, at most 2^15
+constexpr float kLaneThreshold = 64.0f;  // and their sum is brought to a new maximum only where that is 2^64 times the last
 
 constexpr int kSplitRanks = 4, kSplitTiles = 8;
 
@@ -202,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
       const int row0 = rg * 16 + (lane >> 2);
       int row_lo[2], row_hi[2];  // this lane's two rows' visible keys
       uint32_t qf[HD / 16][4];
+      float sl2[2] = {P.scale_log2, P.scale_log2};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = row0 + 8 * e, tok = row / P.group;
@@ -214,17 +225,43 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
         for (int ks = 0; ks < HD / 16; ++ks) {
           if constexpr (k8) {
             const uint2 x = on ? __ldg(reinterpret_cast<const uint2*>(q + ks * 16)) : make_uint2(0u, 0u);
-            qf[ks][e] = __byte_perm(x.x, x.y, 0x5410);      // channels 0 and 2 of the lane's four
-            qf[ks][e + 2] = __byte_perm(x.x, x.y, 0x7632);  // 1 and 3
+            qf[ks][e] = x.x;
+            qf[ks][e + 2] = x.y;
           } else {
             qf[ks][e] = on ? __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16)) : 0u;
             qf[ks][e + 2] = on ? __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16 + 8)) : 0u;
           }
         }
       }
+      if constexpr (k8) {
+        // to f16 by the power of two that brings the row's largest finite magnitude to [2^14, 2^15)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t u = (qf[ks][e + (x & 2)] >> (x & 1) * 16) & 0x7fffu;
+              top = max(top, u < 0x7f80u ? u : 0u);
+            }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const uint32_t up = min(268u - (top >> 7), 253u);  // biased exponent of the power
+          const float by = __uint_as_float(up << 23);
+          sl2[e] = P.scale_log2 * __uint_as_float((254u - up) << 23);
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks) {
+            const float2 a = ptx::unpack_bf16x2(qf[ks][e]), c = ptx::unpack_bf16x2(qf[ks][e + 2]);
+            qf[ks][e] = ptx::pack_f16x2(a.x * by, a.y * by);      // channels 0 and 1 of the lane's four
+            qf[ks][e + 2] = ptx::pack_f16x2(c.x * by, c.y * by);  // 2 and 3
+          }
+        }
+      }
       const int all_lo = __reduce_max_sync(0xffffffffu, max(row_lo[0], row_lo[1]));
       const int all_hi = __reduce_min_sync(0xffffffffu, min(row_hi[0], row_hi[1]));
       float o[HD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float lane_m[2] = {-INFINITY, -INFINITY};  // 8-bit pages: what l is relative to, each lane's own
 #pragma unroll
       for (int e = 0; e < HD / 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
 
@@ -235,7 +272,6 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
         float sc[kWarpKeys / 8][4];
 #pragma unroll
         for (int e = 0; e < kWarpKeys / 8; ++e) sc[e][0] = sc[e][1] = sc[e][2] = sc[e][3] = 0.f;
-        float vscale[k8 ? kWarpKeys / 8 : 1][2];
         if constexpr (k8) {
 #pragma unroll
           for (int e = 0; e < kWarpKeys / 8; ++e) {
@@ -246,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
               ptx::ldmatrix4(ptx::smem_u32(sm.k[s][0]) + chunk_fp8<HD>(kg * kWarpKeys + e * 8 + (lane & 7), c * 4 + (lane >> 3)), kf);
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const uint2 b2 = e4m3x4_to_bf16(kf[x]);
-                ptx::mma_16816(sc[e], qf[c * 4 + x], b2.x, b2.y);
+                ptx::mma_16816_f16(sc[e], qf[c * 4 + x], ptx::e4m3x2_to_f16((uint16_t)kf[x]),
+                                   ptx::e4m3x2_to_f16((uint16_t)(kf[x] >> 16)));
               }
             }
             const int at = kg * kWarpKeys + e * 8 + 2 * (lane & 3);
@@ -327,55 +363,95 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
             }
           }
         }
+        uint32_t pf[kWarpKeys / 8][2];
         if constexpr (k8) {
+          float mt[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};  // largest s, s + e
+          float sv[kWarpKeys / 8][4];
 #pragma unroll
           for (int e = 0; e < kWarpKeys / 8; ++e) {
             const uint32_t of_v = *reinterpret_cast<const uint16_t*>(&sm.scales[s][1][kg * kWarpKeys + e * 8 + 2 * (lane & 3)]);
-            vscale[e][0] = scale_of(of_v & 255u);
-            vscale[e][1] = scale_of(of_v >> 8);
-          }
-        }
-        float mt[2] = {-INFINITY, -INFINITY};
+            const float e0 = exponent_of(of_v & 255u), e1 = exponent_of(of_v >> 8);
 #pragma unroll
-        for (int e = 0; e < kWarpKeys / 8; ++e) {
-          mt[0] = fmaxf(mt[0], fmaxf(sc[e][0], sc[e][1]));
-          mt[1] = fmaxf(mt[1], fmaxf(sc[e][2], sc[e][3]));
-        }
-        bool need = false;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          mt[w] = fmaxf(mt[w], __shfl_xor_sync(0xffffffffu, mt[w], 1));
-          mt[w] = fmaxf(mt[w], __shfl_xor_sync(0xffffffffu, mt[w], 2)) * P.scale_log2;
-          need |= mt[w] > m[w] + kRescaleThreshold || (m[w] == -INFINITY && mt[w] > -INFINITY);
-        }
-        if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const float mn = fmaxf(m[w], mt[w]);
-            const float f = m[w] == -INFINITY ? 0.f : exp2f(m[w] - mn);
-            l[w] *= f;
-            m[w] = mn;
-#pragma unroll
-            for (int e = 0; e < HD / 8; ++e) {
-              o[e][2 * w] *= f;
-              o[e][2 * w + 1] *= f;
+            for (int x = 0; x < 4; ++x) {
+              sc[e][x] *= sl2[x >> 1];
+              sv[e][x] = sc[e][x] + (x & 1 ? e1 : e0);
+              mt[x >> 1] = fmaxf(mt[x >> 1], sc[e][x]);
+              mv[x >> 1] = fmaxf(mv[x >> 1], sv[e][x]);
             }
           }
-        }
-        const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-        uint32_t pf[kWarpKeys / 8][2];
-#pragma unroll
-        for (int e = 0; e < kWarpKeys / 8; ++e)
+          bool need = false;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const float a = ptx::ex2(fmaf(sc[e][2 * w], P.scale_log2, -base[w]));
-            const float c = ptx::ex2(fmaf(sc[e][2 * w + 1], P.scale_log2, -base[w]));
-            l[w] += a + c;
-            if constexpr (k8)
-              pf[e][w] = ptx::pack_bf16x2(a * vscale[e][0], c * vscale[e][1]);
-            else
-              pf[e][w] = ptx::pack_bf16x2(a, c);  // the weights enter the product in bf16, their sum stays fp32
+            mv[w] = fmaxf(mv[w], __shfl_xor_sync(0xffffffffu, mv[w], 1));
+            mv[w] = fmaxf(mv[w], __shfl_xor_sync(0xffffffffu, mv[w], 2));
+            need |= mv[w] > m[w] + kRescaleThreshold || (m[w] == -INFINITY && mv[w] > -INFINITY);
+            if (mt[w] > lane_m[w] + kLaneThreshold || (lane_m[w] == -INFINITY && mt[w] > -INFINITY)) {
+              l[w] *= lane_m[w] == -INFINITY ? 0.f : exp2f(lane_m[w] - mt[w]);
+              lane_m[w] = mt[w];
+            }
           }
+          if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float mn = fmaxf(m[w], mv[w]);
+              const float f = m[w] == -INFINITY ? 0.f : exp2f(m[w] - mn);
+              m[w] = mn;
+#pragma unroll
+              for (int e = 0; e < HD / 8; ++e) {
+                o[e][2 * w] *= f;
+                o[e][2 * w + 1] *= f;
+              }
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const float base = lane_m[w] == -INFINITY ? 0.f : lane_m[w];
+            const float base_v = m[w] == -INFINITY ? 0.f : m[w] - kWeightsUp;
+#pragma unroll
+            for (int e = 0; e < kWarpKeys / 8; ++e) {
+              l[w] += ptx::ex2(sc[e][2 * w] - base) + ptx::ex2(sc[e][2 * w + 1] - base);
+              pf[e][w] = ptx::pack_f16x2(ptx::ex2(sv[e][2 * w] - base_v), ptx::ex2(sv[e][2 * w + 1] - base_v));
+            }
+          }
+        } else {
+          float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kWarpKeys / 8; ++e) {
+            mt[0] = fmaxf(mt[0], fmaxf(sc[e][0], sc[e][1]));
+            mt[1] = fmaxf(mt[1], fmaxf(sc[e][2], sc[e][3]));
+          }
+          bool need = false;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            mt[w] = fmaxf(mt[w], __shfl_xor_sync(0xffffffffu, mt[w], 1));
+            mt[w] = fmaxf(mt[w], __shfl_xor_sync(0xffffffffu, mt[w], 2)) * P.scale_log2;
+            need |= mt[w] > m[w] + kRescaleThreshold || (m[w] == -INFINITY && mt[w] > -INFINITY);
+          }
+          if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float mn = fmaxf(m[w], mt[w]);
+              const float f = m[w] == -INFINITY ? 0.f : exp2f(m[w] - mn);
+              l[w] *= f;
+              m[w] = mn;
+#pragma unroll
+              for (int e = 0; e < HD / 8; ++e) {
+                o[e][2 * w] *= f;
+                o[e][2 * w + 1] *= f;
+              }
+            }
+          }
+          const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+          for (int e = 0; e < kWarpKeys / 8; ++e)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float a = ptx::ex2(fmaf(sc[e][2 * w], P.scale_log2, -base[w]));
+              const float c = ptx::ex2(fmaf(sc[e][2 * w + 1], P.scale_log2, -base[w]));
+              l[w] += a + c;
+              pf[e][w] = ptx::pack_bf16x2(a, c);  // the weights enter the product in bf16, their sum stays fp32
+            }
+        }
 #pragma unroll
         for (int kp = 0; kp < kWarpKeys / 16; ++kp) {
           const uint32_t a[4] = {pf[2 * kp][0], pf[2 * kp][1], pf[2 * kp + 1][0], pf[2 * kp + 1][1]};
@@ -388,9 +464,12 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
               ptx::ldmatrix4_t(ptx::smem_u32(sm.v[s][0]) + chunk_fp8<HD>(key, c * 2 + (lane >> 4)), vf);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const uint2 a0 = e4m3x4_to_bf16(vf[2 * x]), a1 = e4m3x4_to_bf16(vf[2 * x + 1]);
-                ptx::mma_16816(o[4 * c + 2 * x], a, a0.x, a1.x);      // channels 0, 2, ..., 14 of the 16
-                ptx::mma_16816(o[4 * c + 2 * x + 1], a, a0.y, a1.y);  // 1, 3, ..., 15
+                // a channel's two keys side by side
+                const uint32_t a0 = __byte_perm(vf[2 * x], 0u, 0x3120), a1 = __byte_perm(vf[2 * x + 1], 0u, 0x3120);
+                // channels 0, 2, ..., 14 of the 16; then 1, 3, ..., 15
+                ptx::mma_16816_f16(o[4 * c + 2 * x], a, ptx::e4m3x2_to_f16((uint16_t)a0), ptx::e4m3x2_to_f16((uint16_t)a1));
+                ptx::mma_16816_f16(o[4 * c + 2 * x + 1], a, ptx::e4m3x2_to_f16((uint16_t)(a0 >> 16)),
+                                   ptx::e4m3x2_to_f16((uint16_t)(a1 >> 16)));
               }
             }
           } else {
@@ -407,6 +486,21 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
+      }
+      if constexpr (k8) {  // the row's maximum of s for all four lanes, and for O
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          float mx = fmaxf(lane_m[w], __shfl_xor_sync(0xffffffffu, lane_m[w], 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          l[w] *= lane_m[w] == -INFINITY ? 0.f : exp2f(lane_m[w] - mx);
+          const float f = mx == -INFINITY ? 0.f : exp2f(m[w] - kWeightsUp - mx);
+          m[w] = mx;
+#pragma unroll
+          for (int e = 0; e < HD / 8; ++e) {
+            o[e][2 * w] *= f;
+            o[e][2 * w + 1] *= f;
+          }
+        }
       }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {

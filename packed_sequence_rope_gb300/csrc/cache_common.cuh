@@ -49,6 +49,11 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float(byte << 23 | (byte == 255u ? 0x00400000u : 0u));
 }
 
+// The exponent that a scale's byte stands for; NaN for 255.
+__device__ __forceinline__ float exponent_of(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(0x4b000000u | byte) - 8388735.0f;  // 2^23 + byte - (2^23 + 127)
+}
+
 // Sixteen codes of a row whose scale has the byte `scale` as bf16, exactly. Two codes at a
 // time go to the high bytes of 16-bit halves, from where their bits take two selections.
 // The factor is e4m3x4_to_bf16's 2^120 times the scale, 2^(scale - 7), in two parts where
