@@ -57,16 +57,17 @@ struct ShortParts {
   float2* ml;
 };
 
-// Keys of a tile.
+// Keys of a tile. With 8-bit pages what a tile costs beside its keys (waits, maxima across
+// lanes) counts for more: 64 sequences to 32K keys 522 us with 64 keys, 450 with 128.
 template <bool k8>
-constexpr int kTileOf = 64;
+constexpr int kTileOf = k8 ? 128 : 64;
 
 template <int HD, bool k8>
 struct ShortSmem {
   static constexpr int kTileKeys = kTileOf<k8>;
   static constexpr int kB = k8 ? 1 : HD / 64;            // column blocks of a tile
   static constexpr int kRowBytes = k8 ? HD : 128;        // of a key in a block
-  static constexpr int kStages = k8 ? 6 : HD == 128 ? 3 : 4;
+  static constexpr int kStages = k8 ? 3 : HD == 128 ? 3 : 4;
   static constexpr int kRowFloats = HD + 8;  // a warp's rows fall on different banks
   union {
     struct {
@@ -104,7 +105,7 @@ __device__ __forceinline__ uint32_t chunk_fp8(int key, int chunk) {
 }
 
 template <int HD, int RT, int kMask, bool k8>
-__global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
     attend_short_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ AttendParams P, const ShortParts S) {
   using Smem = ShortSmem<HD, k8>;
@@ -643,7 +644,10 @@ inline ShortShape shape_of(const aa_cache_s* c, int num_seqs, int max_q, int tab
   // then even out), as long as each has a few tiles. Measured on 256 units of
   // up to 8K keys, 64 channels: 4 per SM 70 us, 2 per SM 72 us, 8 per SM 80 us;
   // 512 units of up to 32K keys, 128 channels: 774, 818 and 771 us.
-  while (f.ranks < 8 && units * f.ranks < 4 * c->num_sms && tiles >= 4 * f.ranks) f.ranks *= 2;
+  // With 8-bit pages a second filling does not pay for CTAs of less than 40 tiles (16
+  // sequences of 16 kv heads to 8K keys of 64 channels: 59.9 us, without 55.9).
+  while (f.ranks < 8 && units * f.ranks < (c->fp8() && tiles < 80 * f.ranks ? 2 : 4) * c->num_sms && tiles >= 4 * f.ranks)
+    f.ranks *= 2;
   // Two CTAs fit on an SM. Where clusters of 8 do not come to that many, several
   // smaller clusters per unit do, if each CTA keeps kSplitTiles tiles: the
   // second launch costs some 2 us.
@@ -686,7 +690,10 @@ cudaError_t launch(const aa_cache_s* c, const AttendParams& P, const ShortShape&
 
 template <int HD, int kMask, bool k8>
 cudaError_t launch(const aa_cache_s* c, const AttendParams& P, const ShortShape& f, const ShortParts& S, cudaStream_t s) {
-  return f.rt == 1   ? launch<HD, 1, kMask, k8>(c, P, f, S, s)
+  if constexpr (k8)  // the chunk kernel takes more than 32 rows
+    return f.rt == 1 ? launch<HD, 1, kMask, k8>(c, P, f, S, s) : launch<HD, 2, kMask, k8>(c, P, f, S, s);
+  else
+    return f.rt == 1 ? launch<HD, 1, kMask, k8>(c, P, f, S, s)
          : f.rt == 2 ? launch<HD, 2, kMask, k8>(c, P, f, S, s)
                      : launch<HD, 4, kMask, k8>(c, P, f, S, s);
 }

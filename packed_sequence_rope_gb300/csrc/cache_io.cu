@@ -155,8 +155,14 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
 #pragma unroll
     for (int e = 0; e < 8; ++e) mine[e] = cs[tok][8 * chunk + e];
   }
+  Pairs8<HD, L == 2 ? 0 : L> next;
   for (int h = row % kRows; h < heads; h += kRows) {
-    if (h >= kRows) load(x, h);
+    if constexpr (k8) {  // quantising takes longer: the next row is in flight meanwhile
+      if (h >= kRows) x = next;
+      load(next, h + kRows);
+    } else {
+      if (h >= kRows) load(x, h);
+    }
     const int g = h - P.Hq;
     if constexpr (k8) {
       if (g >= 0) {
@@ -244,7 +250,7 @@ cudaError_t launch_read(const ReadParams& P, cudaStream_t s) {
   if (P.batch.T <= kFewTokens)
     cache_read_kernel<HD, 1, k8><<<(unsigned)P.batch.T, kThreads, 0, s>>>(P);
   else
-    cache_read_kernel<HD, 2, k8><<<(unsigned)((P.batch.T + 1) / 2), kThreads, 0, s>>>(P);
+    cache_read_kernel<HD, 4, k8><<<(unsigned)((P.batch.T + 3) / 4), kThreads, 0, s>>>(P);
   return cudaGetLastError();
 }
 

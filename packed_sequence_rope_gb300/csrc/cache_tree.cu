@@ -59,39 +59,37 @@ struct AcceptParams {
   int width, page_shift, row_shift;  // row_shift: log2 of a row's 16-byte chunks
 };
 
-constexpr int kMoves = 4;  // 16-byte chunks a thread moves at a time
+constexpr int kMoves = 2;  // 16-byte chunks of keys, and of values, that a thread moves at a time
 
-// One block per (layer, keys or values; sequence). Row path[i] goes to row i of the new
+// One block per layer and sequence. Row path[i] goes to row i of the new
 // tokens. Since the path ascends, path[i] >= i: a row is overwritten only after it has
 // been read if the rows are moved in order, a batch at a time, all loads of a batch
 // before its stores.
+// The warps read the path for themselves: nothing stands between it and the rows' loads
+// but the page table.
 __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant__ AcceptParams P) {
-  __shared__ int kept, bad;
   const BatchParams& b = P.batch;
-  const int seq = (int)blockIdx.y, layer = (int)blockIdx.x >> 1, is_v = (int)blockIdx.x & 1;
+  const int seq = (int)blockIdx.y, layer = (int)blockIdx.x, lane = threadIdx.x & 31;
   const int32_t* path = P.path + (int64_t)seq * P.width;
   const int n = __ldg(b.cu_q + seq + 1) - __ldg(b.cu_q + seq), base = __ldg(b.kv_len + seq) - n;
-  if (threadIdx.x == 0) {
-    kept = P.width;
-    bad = 0;
+  int count = 0, last = -1;
+  bool bad_path = false;
+  for (bool more = true; more && count < P.width;) {
+    const int at = count + lane, x = at < P.width ? __ldg(path + at) : -1;
+    const uint32_t none = __ballot_sync(0xffffffffu, x < 0);
+    const int some = none ? __ffs((int)none) - 1 : 32;
+    int before = __shfl_up_sync(0xffffffffu, x, 1);
+    if (lane == 0) before = last;
+    bad_path |= __any_sync(0xffffffffu, lane < some && (x >= n || x <= before));
+    last = __shfl_sync(0xffffffffu, x, max(some - 1, 0));
+    count += some;
+    more = none == 0;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < P.width; i += kThreads)
-    if (__ldg(path + i) < 0) atomicMin(&kept, i);
-  __syncthreads();
-  const int count = kept;
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    const int x = __ldg(path + i);
-    if (x >= n || (i > 0 && x <= __ldg(path + i - 1))) atomicOr(&bad, 1);
-  }
-  if (threadIdx.x == 0 && count > 0 && (base < 0 || (int64_t)base + n > (int64_t)b.W << P.page_shift)) atomicOr(&bad, 2);
-  __syncthreads();
-  if (bad) {  // nothing of the sequence is moved
-    if (threadIdx.x == 0) atomicCAS(b.err, 0, bad & 1 ? kCacheBadPath : kCacheBadPosition);
+  if (count == 0) return;
+  if (bad_path || base < 0 || (int64_t)base + n > (int64_t)b.W << P.page_shift) {  // nothing of the sequence is moved
+    if (threadIdx.x == 0) atomicCAS(b.err, 0, bad_path ? kCacheBadPath : kCacheBadPosition);
     return;
   }
-  uint8_t* pages = is_v ? P.v_pages : P.k_pages;
-  uint8_t* scales = is_v ? P.v_scales : P.k_scales;
   const int chunks = 1 << P.row_shift;
   // pool row of position p for kv head g; -1: no page
   auto row_of = [&](int p, int g) -> int64_t {
@@ -104,29 +102,38 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
   };
   const int64_t all = (int64_t)count * b.Hkv << P.row_shift;
   for (int64_t x0 = 0; x0 < all; x0 += kThreads * kMoves) {
-    uint4 v[kMoves];
-    uint8_t scale[kMoves];
+    uint4 k[kMoves], v[kMoves];
+    uint8_t k_scale[kMoves], v_scale[kMoves];
     int64_t to[kMoves];
 #pragma unroll
     for (int m = 0; m < kMoves; ++m) {
       const int64_t x = x0 + m * kThreads + threadIdx.x;
       to[m] = -1;
       if (x >= all) continue;
-      const int i = (int)((x >> P.row_shift) / b.Hkv), g = (int)((x >> P.row_shift) % b.Hkv), from_i = __ldg(path + i);
+      const int r = (int)(x >> P.row_shift), i = r / b.Hkv, g = r - i * b.Hkv, from_i = __ldg(path + i);
       if (from_i == i) continue;
       const int64_t from = row_of(base + from_i, g), into = row_of(base + i, g);
       if (from < 0 || into < 0) continue;
       to[m] = into;
-      v[m] = *reinterpret_cast<const uint4*>(pages + (((from << P.row_shift) + (x & (chunks - 1))) << 4));
-      if (scales) scale[m] = scales[from];
+      const int64_t at = ((from << P.row_shift) + (x & (chunks - 1))) << 4;
+      k[m] = *reinterpret_cast<const uint4*>(P.k_pages + at);
+      v[m] = *reinterpret_cast<const uint4*>(P.v_pages + at);
+      if (P.k_scales) {
+        k_scale[m] = P.k_scales[from];
+        v_scale[m] = P.v_scales[from];
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < kMoves; ++m) {
       if (to[m] < 0) continue;
-      const int64_t x = x0 + m * kThreads + threadIdx.x;
-      *reinterpret_cast<uint4*>(pages + (((to[m] << P.row_shift) + (x & (chunks - 1))) << 4)) = v[m];
-      if (scales && (x & (chunks - 1)) == 0) scales[to[m]] = scale[m];
+      const int64_t chunk = (x0 + m * kThreads + threadIdx.x) & (chunks - 1), at = ((to[m] << P.row_shift) + chunk) << 4;
+      *reinterpret_cast<uint4*>(P.k_pages + at) = k[m];
+      *reinterpret_cast<uint4*>(P.v_pages + at) = v[m];
+      if (P.k_scales && chunk == 0) {
+        P.k_scales[to[m]] = k_scale[m];
+        P.v_scales[to[m]] = v_scale[m];
+      }
     }
     __syncthreads();
   }
@@ -176,6 +183,8 @@ extern "C" aa_status aa_cache_accept(aa_cache_t c, const aa_cache_batch* batch, 
   if (st != AA_OK) return st;
   if ((st = check_batch(c, batch)) != AA_OK) return st;
   if (path_width < 0 || path_width >= (1 << 30)) return fail(AA_ERR_INVALID_ARG, "path_width must be in [0, 2^30)");
+  if ((int64_t)path_width * c->cfg.num_kv_heads >= (1ll << 31))
+    return fail(AA_ERR_INVALID_ARG, "path_width * Hkv must stay below 2^31");
   if (path_width == 0) return AA_OK;
   if (!path || (reinterpret_cast<uintptr_t>(path) & 3u))
     return fail(AA_ERR_INVALID_ARG, "path must be a device pointer to int32");
@@ -197,7 +206,7 @@ extern "C" aa_status aa_cache_accept(aa_cache_t c, const aa_cache_batch* batch, 
     S.batch.cu_q += first;
     S.batch.kv_len += first;
     S.path += (int64_t)first * path_width;
-    accept_kernel<<<dim3((unsigned)(2 * c->cfg.num_layers), (unsigned)some), kThreads, 0,
+    accept_kernel<<<dim3((unsigned)c->cfg.num_layers, (unsigned)some), kThreads, 0,
                     reinterpret_cast<cudaStream_t>(stream)>>>(S);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "accept_kernel launch");
