@@ -76,16 +76,23 @@ __device__ __forceinline__ uint64_t tree_keys(const AttendParams& P, int64_t t, 
   return n - c < 64 ? bits & ((1ull << (n - c)) - 1) : bits;
 }
 
+// Bit x: key j + x lies in [lo, hi], x < 64.
+__device__ __forceinline__ uint64_t keys_between(int j, int lo, int hi) {
+  const int last = hi - j, first = lo - j;
+  const uint64_t upto = last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1ull;
+  return first <= 0 ? upto : first > 63 ? 0ull : upto & (~0ull << first);
+}
+
 // seen_keys() for drafted trees: bit x, some of the tokens q_row + i (i < tokens, the
-// sequence's new tokens i0 + i) sees key j + x (a whole warp asks). Keys in front of
-// base count as seen: together the rows see all from their smallest first key on.
+// sequence's new tokens i0 + i) sees key j + x (a whole warp asks). Keys that are no new
+// tokens count as seen: in front of base the rows together see all from their smallest
+// first key on, and behind the last there are none.
 __device__ __forceinline__ uint64_t tree_seen_keys(const AttendParams& P, int q_row, int i0, int tokens, int base, int n, int j) {
   uint64_t any = 0;
   for (int i = threadIdx.x & 31; i < tokens; i += 32)
     if (base + i0 + i >= 0) any |= tree_keys(P, q_row + i, base, n, j);
   any = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)any);
-  const int c = base - j;  // keys of the window in front of base
-  return c <= 0 ? any : c >= 64 ? ~0ull : any | ((1ull << c) - 1);
+  return any | ~keys_between(j, base, base + n - 1);
 }
 
 // Four channels of a row divided by its sum, in bf16; 0 for a row that saw

@@ -305,13 +305,6 @@ __device__ __forceinline__ void convert_half(const uint8_t* codes, const uint8_t
   }
 }
 
-// Bit x: key j + x lies in [lo, hi], x < 64.
-__device__ __forceinline__ uint64_t keys_between(int j, int lo, int hi) {
-  const int last = hi - j, first = lo - j;
-  const uint64_t upto = last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1ull;
-  return first <= 0 ? upto : first > 63 ? 0ull : upto & (~0ull << first);
-}
-
 // Barrier phases: pieces count the piece ring; the K and V rings count the
 // CTA's key tiles over all its pieces; s_full / p_full count each row tile's
 // softmax steps; q_full and q_free the CTA's row tiles of Q; o_full the pieces
@@ -771,18 +764,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool full0 = __all_sync(0xffffffffu, lo <= j0 && j0 + 31 <= hi);
         const bool full1 = __all_sync(0xffffffffu, lo <= j0 + 32 && j0 + 63 <= hi);
         ptx::tmem_wait_ld();
-        uint64_t tree = 0;  // new tokens among the warp's keys
-        if constexpr (kTree) {
-          if (j0 + 64 > w.gaps && row_valid && w.p0 + t * C.tile_tokens + in_tile >= 0)
-            tree = tree_keys(P, w.q_row + t * C.tile_tokens + in_tile, w.gaps, w.hi + 1 - w.gaps, j0);
-        }
+        // of a drafted tree: the new tokens among keys j, j + 1, ..., j + 31 that the row sees (its hi ends in front of them)
+        auto drafted = [&](int j) {
+          if constexpr (!kTree) return 0u;
+          const int i = t * C.tile_tokens + in_tile;
+          return row_valid && w.p0 + i >= 0 ? (uint32_t)tree_keys(P, w.q_row + i, w.gaps, w.hi + 1 - w.gaps, j) : 0u;
+        };
         if (!full0) {
-          const uint32_t bits = visible_bits(j0, lo, hi) | (j0 == 0 && anchored ? 1u : 0u) | (uint32_t)tree;
+          const uint32_t bits = visible_bits(j0, lo, hi) | (j0 == 0 && anchored ? 1u : 0u) | drafted(j0);
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[e] = (bits >> e) & 1u ? sv[e] : -INFINITY;
         }
         if (!full1) {
-          const uint32_t bits = visible_bits(j0 + 32, lo, hi) | (uint32_t)(tree >> 32);
+          const uint32_t bits = visible_bits(j0 + 32, lo, hi) | drafted(j0 + 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[32 + e] = (bits >> e) & 1u ? sv[32 + e] : -INFINITY;
         }
