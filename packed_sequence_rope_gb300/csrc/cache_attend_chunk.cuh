@@ -219,15 +219,17 @@ struct ChunkSmem {
   static constexpr int kStages = HD == 128 ? 2 : 4;
   // a piece's two row tiles of Q and one of the next piece: its first S product
   // does not wait for a copy
-  static constexpr int kQ = k8 ? 2 : 3;
+  static constexpr int kQ = k8 ? 1 : 3;
+  static constexpr int kHalves = k8 ? 4 : 1;  // 8-bit pages: half tiles of codes on their way, of keys and of values
   alignas(1024) uint8_t q[kQ][kB][16384];
   alignas(1024) uint8_t k[kStages][kB][16384];
   alignas(1024) uint8_t v[kStages][kB][16384];
   // 8-bit pages: codes of half a tile, keys (0) and values (1), and their scales
-  alignas(1024) uint8_t codes[2][k8 ? 2 : 1][k8 ? kKeys / 2 * HD : 16];
-  alignas(16) uint8_t scales[2][k8 ? 2 : 1][k8 ? kKeys / 2 : 16];
-  uint64_t c_full[2][2], c_empty[2][2];
+  alignas(1024) uint8_t codes[2][kHalves][k8 ? kKeys / 2 * HD : 16];
+  alignas(16) uint8_t scales[2][kHalves][k8 ? kKeys / 2 : 16];
+  uint64_t c_full[2][kHalves], c_empty[2][kHalves];
   uint64_t k_ready[kStages];  // the keys are bf16
+  uint64_t o_done;            // a step's product with the values
   uint64_t q_full[kQ], q_free[kQ];
   uint64_t piece_full[2], piece_empty[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
@@ -238,6 +240,7 @@ struct ChunkSmem {
   // issued only after both warps have handed over the last step's weights, and so
   // have read its maxima. In fp32: a base that is off by a fraction of a large
   // maximum leaves weights that underflow to 0.
+  // 8-bit pages: S is issued earlier, and the exchanges take turns in two buffers.
   float pair[2][4][2][32];
   uint32_t tmem_base;
   int abort_flag;
@@ -352,9 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sm.k_ready[s], kConvertWarps);
       ptx::mbar_init(&sm.v_clean[s], k8 ? kConvertWarps : 2);
     }
-    for (int s = 0; s < 4; ++s) {
-      ptx::mbar_init(&sm.c_full[s >> 1][s & 1], 1);
-      ptx::mbar_init(&sm.c_empty[s >> 1][s & 1], kConvertWarps);
+    ptx::mbar_init(&sm.o_done, 1);
+    for (int s = 0; s < 2 * Smem::kHalves; ++s) {
+      ptx::mbar_init(&sm.c_full[s / Smem::kHalves][s % Smem::kHalves], 1);
+      ptx::mbar_init(&sm.c_empty[s / Smem::kHalves][s % Smem::kHalves], kConvertWarps);
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Cut cut{-1, 0, 0, 0};
     int nq = 0, ks = 0, nk = 0;  // row tiles of Q, key tiles whose V, whose K has been asked for
-    int nc[2][2] = {{0, 0}, {0, 0}};  // 8-bit pages: halves of each buffer
+    int nc[2] = {0, 0};               // 8-bit pages: half tiles of keys, of values
     bool ok = true;
     // a key tile is `pieces` page pieces, each kB column blocks of K, then of V
     const int piece_shift = min(P.page_shift, 6), pieces = kKeys >> piece_shift;
@@ -452,23 +456,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (k8) {
           for (int h = 0; h < 2; ++h)
             for (int v = 0; v < 2; ++v) {
-              if (ks > 0) ok = warp_wait(&sm.c_empty[v][h], (ks - 1) & 1, b.err, abort_flag, 451);
+              constexpr int kHalves = Smem::kHalves;
+              const int x = nc[v] % kHalves;
+              if (nc[v] >= kHalves) ok = warp_wait(&sm.c_empty[v][x], (nc[v] / kHalves - 1) & 1, b.err, abort_flag, 451);
               if (!ok) return;
               const bool mine = lane < copies && part / (pieces / 2) == h;
               const int at = (part - h * (pieces / 2)) << piece_shift;
-              uint8_t* scales = sm.scales[v][h] + at;
+              uint8_t* scales = sm.scales[v][x] + at;
               // the scales of pieces that are not looked up: zeros, as their codes will be
               if (mine && row < 0)
-                for (int x = 0; x < 1 << piece_shift; x += 16) *reinterpret_cast<uint4*>(scales + x) = make_uint4(0, 0, 0, 0);
+                for (int y = 0; y < 1 << piece_shift; y += 16) *reinterpret_cast<uint4*>(scales + y) = make_uint4(0, 0, 0, 0);
               const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
-              if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][h], kTileBytes / 4 + (uint32_t)(scaled << piece_shift));
+              if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][x], kTileBytes / 4 + (uint32_t)(scaled << piece_shift));
               __syncwarp();
               if (mine) {
-                ptx::tma_load_2d(sm.codes[v][h] + at * HD, v ? &tmV : &tmK, &sm.c_full[v][h], 0, row);
+                ptx::tma_load_2d(sm.codes[v][x] + at * HD, v ? &tmV : &tmK, &sm.c_full[v][x], 0, row);
                 if (row >= 0)
-                  ptx::bulk_load(scales, (v ? P.v_scales : P.k_scales) + row, 1u << piece_shift, &sm.c_full[v][h]);
+                  ptx::bulk_load(scales, (v ? P.v_scales : P.k_scales) + row, 1u << piece_shift, &sm.c_full[v][x]);
               }
-              nc[v][h] = ks + 1;
+              ++nc[v];
             }
         } else {
           // K's buffer is free one product earlier than V's, and V is wanted later
@@ -509,8 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = max(nq - kQ, 0); u < nq; ++u)
       ptx::mbar_wait(&sm.q_full[u % kQ], (u / kQ) & 1, kDrainNs, b.err, 459);
     if constexpr (k8) {
-      for (int x = 0; x < 4; ++x)
-        if (nc[x >> 1][x & 1] > 0) ptx::mbar_wait(&sm.c_full[x >> 1][x & 1], (nc[x >> 1][x & 1] - 1) & 1, kDrainNs, b.err, 459);
+      for (int v = 0; v < 2; ++v)
+        for (int u = max(nc[v] - Smem::kHalves, 0); u < nc[v]; ++u)
+          ptx::mbar_wait(&sm.c_full[v][u % Smem::kHalves], (u / Smem::kHalves) & 1, kDrainNs, b.err, 459);
       ks = nk = 0;
     }
     for (int u = max(nk - kStages, 0); u < nk; ++u)
@@ -547,6 +554,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = __all_sync(0xffffffffu, w.tokens > C.tile_tokens) ? 2 : 1;
       const int q[2] = {nq % kQ, (nq + 1) % kQ};
       const uint64_t qd[2] = {q0 + q[0] * (kTileBytes >> 4), q0 + q[1] * (kTileBytes >> 4)};
+      if constexpr (k8) {
+        // One row tile, but two S: the next tile's product is issued ahead of this one's with
+        // the values, so that the softmax passes from one to the next without a wait. The tensor
+        // core takes the products in order: S(i + 1) replaces weights that PV(i - 1) has read.
+        if (!(ok = wait(&k_in[ks % kStages], (ks / kStages) & 1, 463))) break;
+        if (!(ok = wait(&sm.q_full[q[0]], (nq / kQ) & 1, 462))) break;
+        ptx::tc_fence_after();
+        issue_s(0, qd[0], k0 + (ks % kStages) * (kTileBytes >> 4));
+        ptx::mma_commit_warp(&sm.k_empty[ks % kStages]);
+        auto step = [&](int buf, int i) {
+          const int s = ks % kStages, s1 = (ks + 1) % kStages;
+          if (i + 1 < take) {
+            if (!wait(&k_in[s1], ((ks + 1) / kStages) & 1, 463)) return false;
+            ptx::tc_fence_after();
+            issue_s(buf ^ 1, qd[0], k0 + s1 * (kTileBytes >> 4));
+            ptx::mma_commit_warp(&sm.k_empty[s1]);
+          }
+          if (i + 2 == take || take == 1) ptx::mma_commit_warp(&sm.q_free[q[0]]);
+          if (!wait(&sm.v_clean[s], (ks / kStages) & 1, 464)) return false;
+          if (!wait(&sm.p_full[buf], ph_p[buf], 461)) return false;
+          ph_p[buf] ^= 1;
+          ptx::tc_fence_after();
+          ptx::mma8_ts_seq_warp(tmem + 256, tmem + 128 * buf, v0 + s * (kTileBytes >> 4), idesc_pv, i == 0 ? 0u : 1u);
+          ptx::mma_commit_warp(&sm.o_done);
+          if (i + 1 == take) ptx::mma_commit_warp(&sm.o_full[0]);
+          ptx::mma_commit_warp(&sm.v_empty[s]);
+          ++ks;
+          return true;
+        };
+        for (int i = 0; i < take && ok; i += 2) {
+          ok = step(0, i);
+          if (ok && i + 1 < take) ok = step(1, i + 1);
+        }
+        nq += 1;
+        continue;
+      }
       // the first S products, as the piece's K and Q land
       if (!(ok = wait(&k_in[ks % kStages], (ks / kStages) & 1, 463))) break;
 #pragma unroll
@@ -617,10 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               seen &= kTree ? tree_seen_keys(P, w.q_row, w.p0 - w.gaps, w.tokens, w.gaps, w.hi + 1 - w.gaps, j)
                             : seen_keys(P, w.q_row, w.p0, w.tokens, j);
           }
-          if (!(ok = warp_wait(&sm.c_full[v][h], ks & 1, b.err, abort_flag, 471))) break;
-          convert_half<HD>(sm.codes[v][h], sm.scales[v][h], v ? sm.v[s][0] : sm.k[s][0], 64 * h, tc, seen);
+          const int half = 2 * ks + h, x = half % Smem::kHalves;
+          if (!(ok = warp_wait(&sm.c_full[v][x], (half / Smem::kHalves) & 1, b.err, abort_flag, 471))) break;
+          convert_half<HD>(sm.codes[v][x], sm.scales[v][x], v ? sm.v[s][0] : sm.k[s][0], 64 * h, tc, seen);
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sm.c_empty[v][h]);
+          if (lane == 0) ptx::mbar_arrive(&sm.c_empty[v][x]);
         }
         if (!ok) break;
         ptx::fence_proxy_async_smem();
@@ -688,11 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
     const int pair_bar = 1 + t * 4 + (warp & 3);  // named barrier of the two warps with the same rows
     auto& pair = sm.pair[t][warp & 3];
+    auto* const pairs = &sm.pair[0][warp & 3];  // 8-bit pages: [0] and [4] of these
     const float sl2 = P.scale_log2;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + 128 * t + lane_off, t_o = tmem + 256 + HD * t + half * (HD / 2) + lane_off;
-    uint32_t ph_s = 0;
-    int nq = 0;
+    const uint32_t t_s0 = tmem + 128 * t + lane_off, t_o = tmem + 256 + HD * t + half * (HD / 2) + lane_off;
+    uint32_t ph_s = 0, ph_s1 = 0;
+    int nq = 0, steps = 0, exchanges = 0;
     // a warp that gives up still meets its partner: both leave together
     for (int li = 0;; ++li) {
       const Piece& w = sm.piece[li & 1];  // released after the epilogue
@@ -720,19 +765,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int i = 0; i < take; ++i, j0 = next_j0, next_j0 += kKeys) {
-        ok = warp_wait(&sm.s_full[t], ph_s, b.err, abort_flag, 482);
+        const int buf = k8 ? i & 1 : t;  // of S
+        ok = warp_wait(&sm.s_full[buf], k8 && buf ? ph_s1 : ph_s, b.err, abort_flag, 482);
         if (!ok) {
           ptx::bar_and(pair_bar, 64, false);
           break;
         }
-        ph_s ^= 1;
+        if (k8 && buf)
+          ph_s1 ^= 1;
+        else
+          ph_s ^= 1;
         ptx::tc_fence_after();
+        const uint32_t t_s = k8 ? t_s0 + 128 * buf : t_s0;
         // The row's maximum over both column halves, and what it changes. Also the
         // point where both warps have read their columns of S: P may overwrite them.
         auto agree = [&](float mt) {
-          pair[half][lane] = mt;
+          auto& both = k8 ? pairs[4 * (exchanges++ & 1)] : pair;
+          both[half][lane] = mt;
           if (!ptx::bar_and(pair_bar, 64, true)) return false;
-          mt = fmaxf(pair[0][lane], pair[1][lane]) * sl2;
+          mt = fmaxf(both[0][lane], both[1][lane]) * sl2;
           // TMEM access is warp-collective, so a rescale of O is decided per warp (alike
           // for both), and by rows that hold a token alone: what lies in the others
           // (the next sequence's queries, old shared memory) must not change a bit
@@ -741,7 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mn = fmaxf(m, mt);
             const float f = (m == -INFINITY) ? 0.f : exp2f(m - mn);
             l *= f;
-            if (i > 0) {  // O holds earlier tiles: S(i) done implies their PV is done
+            if (i > 0) {  // O holds earlier tiles: S(i) done implies their PV is done; with two S it does not
+              if (k8 && !warp_wait(&sm.o_done, (steps - 1) & 1, b.err, abort_flag, 484)) return false;
+              if (k8) ptx::tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < HD / 32; ++c) {
                 float ov[16];
@@ -806,13 +859,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.p_full[t]);
+        if (lane == 0) ptx::mbar_arrive(&sm.p_full[buf]);
+        ++steps;
       }
       if (!ok) break;
       ok = warp_wait(&sm.o_full[t], nq & 1, b.err, abort_flag, 483);
-      pair[half][lane] = l;  // the partner has read the last step's maxima: O is complete
+      auto& sums = k8 ? pairs[4 * (exchanges++ & 1)] : pair;
+      sums[half][lane] = l;  // the partner has read the last step's maxima: O is complete
       if (!ptx::bar_and(pair_bar, 64, ok)) break;
-      l += pair[half ^ 1][lane];
+      l += sums[half ^ 1][lane];
       // ---- epilogue, half of the channels per warp. Its TMEM reads complete
       // (tmem_wait_ld) before this thread's next p_full arrival, which the next
       // piece's first PV of this tile (overwriting O) waits for.
