@@ -37,26 +37,25 @@ static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_
          (int64_t)num_seqs * c->cfg.num_kv_heads < 64;
 }
 
-// 8-bit pages: the kernel of few rows makes codes bf16 once per 16 rows, the chunk kernel
+// 8-bit pages: the kernel of few rows converts codes once per 16 rows, the chunk kernel
 // once per 128; with more rows the codes are made bf16 ahead of the chunk kernel of 16-bit
-// pages. Measured, microseconds of the three, 8 kv heads of 128, group 4:
+// pages (kWide). Measured, microseconds of the three, 8 kv heads of 128, group 4:
 //   rows, sequences   300 keys             2048                 16384
-//   32, 1             14.6 / 16.5 / 18.6   14.6 / 22.4 / 24.7   28.9 / 37.8 / 51.6
-//   32, 42            41.2 / 39.3 / 47.9   99.0 / 137 / 181     597 / 802 / 1236
-//   64, 1             22.0 / 16.5 / 18.6   22.7 / 22.8 / 25.6   45.3 / 39.1 / 53.4
-//   64, 42            67.9 / 42.4 / 47.7   193 / 139 / 184      1258 / 804 / 1239
-//   128, 42           131 / 58.3 / 49.6    373 / 143 / 187      2512 / 809 / 1247
-//   256, 1            71.8 / 16.8 / 20.9   78.0 / 25.0 / 28.8   156 / 59.6 / 56.7
-//   256, 42           248 / 68.4 / 72.4    735 / 260 / 206      5030 / 1584 / 1294
+//   32, 1             15.0 / 16.4 / 18.6   14.5 / 20.9 / 24.9   26.9 / 35.0 / 51.7
+//   32, 42            33.0 / 36.0 / 47.4   99.0 / 119 / 181     466 / 654 / 1238
+//   64, 1             26.9 / 16.7 / 18.6   24.7 / 20.8 / 25.9   45.1 / 36.3 / 53.4
+//   64, 42            59.7 / 37.7 / 47.3   173 / 121 / 183      923 / 657 / 1243
+//   256, 8            92.3 / 26.8 / 23.3   207 / 58.0 / 59.7    787 / 269 / 268
+//   256, 42           219 / 58.1 / 71.9    679 / 226 / 206      3682 / 1292 / 1297
+//   512, 42           407 / 100 / 76.9     1359 / 413 / 277     7355 / 2546 / 1783
+// With D = 64: 64 rows of 42 sequences 40.9 / 32.9 / 37.0, 134 / 98.8 / 124 and 962 / 423 /
+// 804, 256 rows 138 / 51.4 / 59.6, 520 / 185 / 129 and 3698 / 1109 / 761.
 enum Path { kShort, kChunk, kShortCodes, kChunkCodes, kWide };
 
 static Path path_of(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
   if (!c->fp8()) return takes_short(c, num_seqs, max_q, table_width, group) ? kShort : kChunk;
   const int64_t rows = (int64_t)std::max(max_q, 1) * group;
-#ifdef AA_TUNE
-  if (const char* e = getenv("AA_PATH")) return e[0] == 's' ? kShortCodes : e[0] == 'c' ? kChunkCodes : kWide;
-#endif
-  return rows <= 32 ? kShortCodes : rows <= 128 || !wide_fits(c, table_width) ? kChunkCodes : kWide;
+  return rows <= 32 ? kShortCodes : rows <= 2 * c->cfg.head_dim || !wide_fits(c, table_width) ? kChunkCodes : kWide;
 }
 
 extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs, int32_t total_tokens, int32_t max_q,

@@ -36,7 +36,8 @@
 // 8-bit pages (k8): a unit is one row tile. Warps 12-15 make the tiles of keys bf16,
 // scales included, warps 16-19 the values, so that the products and the softmax are those
 // of 16-bit pages. The codes come in halves of a tile, through buffers of their own. The
-// values that no row sees become zeros on the way, and warps 2 and 3 have nothing to do.
+// values that no row sees become zeros on the way. Warp 0 copies the keys', warp 2 the
+// values' (one warp for both was what the kernel waited for); warp 3 has nothing to do.
 // Converting costs about as many instructions as the softmax of a row tile, so the second
 // row tile's warps do it; four more warps beside them leave 80 registers a thread, which
 // the softmax does not fit. The loops are kept rolled: their code, the softmax's and the
@@ -57,8 +58,8 @@ constexpr int kThreads = 32 * (4 + kSoftmaxWarps);
 // Where keys and values are read: 16-bit pages, 8-bit pages, or what wide_kernel has made of 8-bit pages.
 enum ChunkFrom { kFromPages, kFromCodes, kFromWide };
 constexpr int kConvertWarps = 4;             // for keys, and as many for values
-template <bool k8>  // of a published piece: all warps but the first; with 8-bit pages without warps 2 and 3
-constexpr int kReaders = kThreads / 32 - (k8 ? 3 : 1);
+template <bool k8>  // of a published piece: all warps but the first; with 8-bit pages without warp 3
+constexpr int kReaders = kThreads / 32 - (k8 ? 2 : 1);
 // Row tiles of a unit.
 inline __host__ __device__ constexpr int tiles_of(bool k8) { return k8 ? 1 : 2; }
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
@@ -295,7 +296,7 @@ __device__ __forceinline__ void convert_half(const uint8_t* codes, const uint8_t
   // Eight lanes take four chunks of rows r and r ^ 5: they meet eight different groups of
   // banks in both swizzles, where they read and where they write.
   const int c = tc & 3, flip = tc & 4 ? 5 : 0, r0 = tc >> 3 << 1;
-#pragma unroll 4
+#pragma unroll 2
   for (int i = 0; i < kChunks; ++i) {
     const int row = (i / kPerRow * 32 + r0) ^ flip, block = i % kPerRow;
     const uint4 x = *reinterpret_cast<const uint4*>(
@@ -307,6 +308,68 @@ __device__ __forceinline__ void convert_half(const uint8_t* codes, const uint8_t
     *reinterpret_cast<uint4*>(out + sw128_chunk(row0 + row, 2 * c + 1)) = y[1];
   }
 }
+
+// 8-bit pages: a warp's copies of key tiles, half by half, of keys (v = 0) or values. A
+// tile's pages are asked for one tile ahead and not looked at before.
+template <int HD>
+struct CodeCopies {
+  int part, pieces, piece_shift;  // a tile's pages: lane `part` copies one of `pieces`
+  int page = -1, j = -1;          // of the next tile; j < 0: not looked up
+  int n = 0;                      // half tiles asked for
+  __device__ __forceinline__ explicit CodeCopies(int page_shift) {
+    piece_shift = min(page_shift, 6);
+    pieces = kKeys >> piece_shift;
+    part = (int)(threadIdx.x & 31);
+  }
+  // Tile i of a piece of work, if it has one.
+  __device__ __forceinline__ void ask(const AttendParams& P, const Piece& w, const KeyTiles<kKeys>& keys, bool anchor, int i) {
+    j = keys.tile(i) * kKeys + (part << piece_shift);
+    // pieces that no row sees are not looked up (lo > hi: the rows see the anchor at most)
+    const bool seen = j <= w.hi && ((w.lo <= w.hi && j + (1 << piece_shift) > w.lo) || (j == 0 && anchor));
+    if (!(part < pieces && i < w.first + w.take && i < keys.count && seen)) j = -1;
+    page = j >= 0 ? __ldg(P.batch.table + (int64_t)w.seq * P.batch.W + (j >> P.page_shift)) : -1;
+  }
+  template <class Smem>
+  __device__ __forceinline__ bool load(Smem& sm, const AttendParams& P, const CUtensorMap& tm, int v, int g, int from_j,
+                                       int from_page, volatile int* abort_flag) {
+    const BatchParams& b = P.batch;
+    int row = kNoRow;
+    if (from_j >= 0) {
+      if (from_page >= 0 && from_page < b.num_pages)
+        row = (int)((((b.layer_page0 + from_page) * b.Hkv + g) << P.page_shift) + (from_j & ((1 << P.page_shift) - 1)));
+      else
+        atomicCAS(b.err, 0, kCacheBadPage);
+    }
+    const uint8_t* from = (v ? P.v_scales : P.k_scales) + row;
+    const uint32_t bytes = 1u << piece_shift;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const int x = n % Smem::kHalves;
+      if (n >= Smem::kHalves && !warp_wait(&sm.c_empty[v][x], (n / Smem::kHalves - 1) & 1, b.err, abort_flag, 451)) return false;
+      const bool mine = part < pieces && part / (pieces / 2) == h;
+      const int at = (part & (pieces / 2 - 1)) << piece_shift;
+      uint8_t* scales = sm.scales[v][x] + at;
+      // the scales of pieces that are not looked up: zeros, as their codes will be
+      if (mine && row < 0)
+        for (uint32_t y = 0; y < bytes; y += 16) *reinterpret_cast<uint4*>(scales + y) = make_uint4(0, 0, 0, 0);
+      const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
+      if (part == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][x], kKeys / 2 * HD + ((uint32_t)scaled << piece_shift));
+      __syncwarp();
+      if (mine) {
+        ptx::tma_load_2d(sm.codes[v][x] + at * HD, &tm, &sm.c_full[v][x], 0, row);
+        if (row >= 0) ptx::bulk_load(scales, from, bytes, &sm.c_full[v][x]);
+      }
+      ++n;
+    }
+    return true;
+  }
+  // every copy lands before the CTA exits
+  template <class Smem>
+  __device__ __forceinline__ void drain(Smem& sm, int v, int32_t* err) const {
+    for (int u = max(n - Smem::kHalves, 0); u < n; ++u)
+      ptx::mbar_wait(&sm.c_full[v][u % Smem::kHalves], (u / Smem::kHalves) & 1, kDrainNs, err, 459);
+  }
+};
 
 // Barrier phases: pieces count the piece ring; the K and V rings count the
 // CTA's key tiles over all its pieces; s_full / p_full count each row tile's
@@ -383,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Cut cut{-1, 0, 0, 0};
     int nq = 0, ks = 0, nk = 0;  // row tiles of Q, key tiles whose V, whose K has been asked for
-    int nc[2] = {0, 0};               // 8-bit pages: half tiles of keys, of values
+    CodeCopies<HD> codes(P.page_shift);
     bool ok = true;
     // a key tile is `pieces` page pieces, each kB column blocks of K, then of V
     const int piece_shift = min(P.page_shift, 6), pieces = kKeys >> piece_shift;
@@ -449,34 +512,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(lane < copies && i < w.first + w.take && i < keys.count && seen)) return kNoRow;
         return kFrom == kFromWide ? (int)((w.seq * b.Hkv + w.g) * C.wide_keys + j) : pool_row(b, w.seq, w.g, j, P.page_shift);
       };
-      int next = row_of(w.first);
+      int next = kNoRow;
+      if constexpr (k8)
+        codes.ask(P, w, keys, anchor, w.first);
+      else
+        next = row_of(w.first);
       auto load_keys = [&](int i) {
-        const int s = ks % kStages, row = next;
-        next = row_of(i + 1);  // in flight while this stage is waited for
         if constexpr (k8) {
-          for (int h = 0; h < 2; ++h)
-            for (int v = 0; v < 2; ++v) {
-              constexpr int kHalves = Smem::kHalves;
-              const int x = nc[v] % kHalves;
-              if (nc[v] >= kHalves) ok = warp_wait(&sm.c_empty[v][x], (nc[v] / kHalves - 1) & 1, b.err, abort_flag, 451);
-              if (!ok) return;
-              const bool mine = lane < copies && part / (pieces / 2) == h;
-              const int at = (part - h * (pieces / 2)) << piece_shift;
-              uint8_t* scales = sm.scales[v][x] + at;
-              // the scales of pieces that are not looked up: zeros, as their codes will be
-              if (mine && row < 0)
-                for (int y = 0; y < 1 << piece_shift; y += 16) *reinterpret_cast<uint4*>(scales + y) = make_uint4(0, 0, 0, 0);
-              const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
-              if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][x], kTileBytes / 4 + (uint32_t)(scaled << piece_shift));
-              __syncwarp();
-              if (mine) {
-                ptx::tma_load_2d(sm.codes[v][x] + at * HD, v ? &tmV : &tmK, &sm.c_full[v][x], 0, row);
-                if (row >= 0)
-                  ptx::bulk_load(scales, (v ? P.v_scales : P.k_scales) + row, 1u << piece_shift, &sm.c_full[v][x]);
-              }
-              ++nc[v];
-            }
+          const int j = codes.j, page = codes.page;
+          codes.ask(P, w, keys, anchor, i + 1);
+          ok = codes.load(sm, P, tmK, 0, w.g, j, page, abort_flag);
         } else {
+          const int s = ks % kStages, row = next;
+          next = row_of(i + 1);  // in flight while this stage is waited for
           // K's buffer is free one product earlier than V's, and V is wanted later
           for (int v = 0; v < 2; ++v) {
             uint64_t* full = v ? &sm.v_full[s] : &sm.k_full[s];
@@ -515,9 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = max(nq - kQ, 0); u < nq; ++u)
       ptx::mbar_wait(&sm.q_full[u % kQ], (u / kQ) & 1, kDrainNs, b.err, 459);
     if constexpr (k8) {
-      for (int v = 0; v < 2; ++v)
-        for (int u = max(nc[v] - Smem::kHalves, 0); u < nc[v]; ++u)
-          ptx::mbar_wait(&sm.c_full[v][u % Smem::kHalves], (u / Smem::kHalves) & 1, kDrainNs, b.err, 459);
+      codes.drain(sm, 0, b.err);
       ks = nk = 0;
     }
     for (int u = max(nk - kStages, 0); u < nk; ++u)
@@ -633,7 +679,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     ptx::mma_commit_warp(&sm.drain);
     ptx::mbar_wait(&sm.drain, 0, kDrainNs, b.err, 469);
-  } else if (k8 && warp < 4) {
+  } else if (k8 && warp == 3) {
+  } else if (k8 && warp == 2) {
+    // ------------------------------------------------------------ the values' codes
+    CodeCopies<HD> codes(P.page_shift);
+    bool ok = true;
+    for (int li = 0; ok; ++li) {
+      Piece w;
+      if (!read_piece(sm, li, b.err, abort_flag, 453, &w)) break;
+      const bool anchor = P.anchor && (!kTree || w.gaps > 0);
+      const KeyTiles<kKeys> keys(w.lo, w.hi, anchor);
+      codes.ask(P, w, keys, anchor, w.first);
+      for (int i = w.first; i < w.first + w.take && ok; ++i) {
+        const int j = codes.j, page = codes.page;
+        codes.ask(P, w, keys, anchor, i + 1);
+        ok = codes.load(sm, P, tmV, 1, w.g, j, page, abort_flag);
+      }
+    }
+    codes.drain(sm, 1, b.err);
   } else if (k8 && warp >= 12) {
     // ------------------------------------------------------------ codes to bf16: keys (warps 12-15), values (16-19)
     const int v = warp >= 16, tc = tid & (32 * kConvertWarps - 1);

@@ -644,10 +644,16 @@ inline ShortShape shape_of(const aa_cache_s* c, int num_seqs, int max_q, int tab
   // then even out), as long as each has a few tiles. Measured on 256 units of
   // up to 8K keys, 64 channels: 4 per SM 70 us, 2 per SM 72 us, 8 per SM 80 us;
   // 512 units of up to 32K keys, 128 channels: 774, 818 and 771 us.
-  // With 8-bit pages a second filling does not pay for CTAs of less than 40 tiles (16
-  // sequences of 16 kv heads to 8K keys of 64 channels: 59.9 us, without 55.9).
-  while (f.ranks < 8 && units * f.ranks < (c->fp8() && tiles < 80 * f.ranks ? 2 : 4) * c->num_sms && tiles >= 4 * f.ranks)
-    f.ranks *= 2;
+  // With 8-bit pages a tile takes less time, a CTA's start and join do not: where most of
+  // the room is taken, CTAs of less than 80 tiles of 64 keys do not get smaller (64 sequences of 8 kv
+  // heads over 4000 keys of 128 channels 132 us, halved 144; 8 over 1000 10.3, halved
+  // 16.8; 16 of 16 kv heads to 8K keys of 64 channels 55.9, halved 59.9).
+  const int64_t at_once = (c->cfg.head_dim == 128 ? 2 : 4) * c->num_sms;
+  auto enough = [&] {
+    const int64_t ctas = units * f.ranks;
+    return ctas >= 4 * c->num_sms || (c->fp8() && tiles < 80 * f.ranks && 2 * ctas > at_once);
+  };
+  while (f.ranks < 8 && !enough() && tiles >= 4 * f.ranks) f.ranks *= 2;
   // Two CTAs fit on an SM. Where clusters of 8 do not come to that many, several
   // smaller clusters per unit do, if each CTA keeps kSplitTiles tiles: the
   // second launch costs some 2 us.

@@ -54,9 +54,7 @@ __device__ __forceinline__ float exponent_of(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(0x4b000000u | byte) - 8388735.0f;  // 2^23 + byte - (2^23 + 127)
 }
 
-// Sixteen codes of a row whose scale has the byte `scale` as bf16, exactly. Two codes at a
-// time go to the high bytes of 16-bit halves, from where their bits take two selections.
-// The factor is e4m3x4_to_bf16's 2^120 times the scale, 2^(scale - 7), in two parts where
+// Sixteen codes of a row whose scale has the byte `scale` as bf16, exactly. The factor is e4m3x4_to_bf16's 2^120 times the scale, 2^(scale - 7), in two parts where
 // bf16 does not reach. zero: zeros instead.
 __device__ __forceinline__ void decode16(const uint4& x, int scale, bool zero, uint4 (&y)[2]) {
   uint32_t up = scale == 255 ? 0x7fc0u : (uint32_t)min(scale + 120, 254) << 7;
@@ -64,10 +62,10 @@ __device__ __forceinline__ void decode16(const uint4& x, int scale, bool zero, u
   const uint32_t four[4] = {x.x, x.y, x.z, x.w};
   uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t two = __byte_perm(four[e >> 1], 0u, e & 1 ? 0x3424 : 0x1404);
-    const uint32_t b = ((two >> 4) & 0x07f007f0u) | (two & 0x80008000u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[e]) : "r"(b), "r"(up));
+  for (int e = 0; e < 4; ++e) {  // even and odd codes, then side by side
+    const uint2 z = e4m3x4_to_bf16(four[e], up);
+    w[2 * e] = __byte_perm(z.x, z.y, 0x5410);
+    w[2 * e + 1] = __byte_perm(z.x, z.y, 0x7632);
   }
   if (scale > 134 && scale < 255) {
     const uint32_t more = (uint32_t)(scale - 7) << 7, more2 = more | more << 16;  // 2^(scale - 134)
