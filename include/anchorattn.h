@@ -422,9 +422,9 @@ aa_status aa_rope_axes_apply(const aa_rope_axes* rope, const int32_t* pos, int32
  * the (rotated) fp32 values once, to the nearest, ties to even: within 2^-4 of the value
  * or 2^-10 of the power, whichever is more (magnitudes above 448 * 2^119, bf16's
  * largest 14 %, become that). A row with a value that is not finite gets byte 255 and
- * is NaN as a whole. Pages that the caller fills have bytes in [1, 254] or 255 for
- * NaN and no NaN codes (0x7f, 0xff read as +-480). All other calls are the same for
- * both kinds.
+ * is NaN as a whole. Pages that the caller fills have bytes in [1, 254], or 255 for
+ * NaN, and no NaN codes (what 0x7f and 0xff give is not defined). All other calls are
+ * the same for both kinds.
  *
  * Two halves:
  *  - Bookkeeping on the host (aa_cache_resize, _fork, _compact, _tables,
@@ -556,6 +556,8 @@ aa_status aa_cache_read(aa_cache_t cache, const aa_cache_batch* batch, void* k, 
  * document; or p - W + 1 for a sliding window):
  *   O_i = sum_j softmax_j(scale * q_i . k_j) v_j,  LSE_i = ln sum_j exp(...).
  * A row that sees no key, or whose logits are all -inf, gives O = 0 and LSE = -inf.
+ * With 8-bit pages the result is that of the values that they stand for, and a key may
+ * take 2^-32 of the row's largest weight times value out of it.
  * Keys that no new token of their sequence sees do not reach the result, whatever
  * they hold (NaN, infinities); what a row sees makes it NaN as the formula does, and a value that
  * is not finite may reach the other rows of its sequence in the call too.
@@ -614,7 +616,9 @@ aa_status aa_cache_accept(aa_cache_t cache, const aa_cache_batch* batch, const i
  * (partial results of keys that are split among CTAs). Chunks: 20 MB at D = 64, 40 at
  * 128, and 32 bytes per sequence and per 256 rows of a kv head more. Few new tokens
  * over long contexts: the results of up to 76 splits, 4 * D + 8 bytes per row and split.
- * 256 bytes where nothing is split. A smaller batch may need more. 0 for invalid
+ * 256 bytes where nothing is split. Chunks over 8-bit pages whose sequences have more
+ * than 2 * D rows (max_q times the query heads of a kv head): 16-bit copies of a few
+ * sequences' keys and values more, 4 * D * Hkv bytes per position of their tables, up to 1 GiB. A smaller batch may need more. 0 for invalid
  * sizes. */
 size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
                                        int32_t table_width, int32_t q_heads);

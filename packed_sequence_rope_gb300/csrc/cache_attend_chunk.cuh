@@ -353,6 +353,7 @@ struct CodeCopies {
       if (mine && row < 0)
         for (uint32_t y = 0; y < bytes; y += 16) *reinterpret_cast<uint4*>(scales + y) = make_uint4(0, 0, 0, 0);
       const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
+      __syncwarp();  // the zeros before the arrival
       if (part == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][x], kKeys / 2 * HD + ((uint32_t)scaled << piece_shift));
       __syncwarp();
       if (mine) {

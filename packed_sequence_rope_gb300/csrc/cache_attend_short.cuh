@@ -26,13 +26,13 @@
 // sequences to 32K keys 627 us) they are the step's operand with its channels in another
 // order, which the queries' operand shares. Loaded transposed, a lane's codes are two
 // channels of two keys: operands of two products, for the even and the odd channels.
-// The other operands are f16 then, within its range by powers of two: a row of queries
-// times the one that brings its maximum to 2^14, which keeps every value down to 2^-39 of it exact; and
-// the weights. The keys' scales multiply the logits. A value's scale 2^e joins its weight,
-// 2^(s + e - m) with m the row's running maximum of s + e, so that weights lie below 2^15,
-// are rounded to 11 bits down to 2^-21 of the largest at least, and to multiples of 2^-24 of 2^7 below:
-// the weights smaller than that take 2^-32 of the largest value times weight each at most out of
-// the result. Their sum has its own maximum, since scales of tokens may lie far apart.
+// The other operands are f16 then, brought into its range by powers of two. A row of
+// queries is multiplied by the one that takes its maximum to 2^14: what is above 2^-21 of
+// the maximum stays exact, the rest is off by at most 2^-39 of it. The keys' scales
+// multiply the logits s. A value's scale 2^e joins its weight, 2^(s + e - m) with m the
+// row's running maximum of s + e, times 2^7. Weights are then below 2^15; those above 2^-21
+// of the largest are rounded to 11 bits, the others are off by at most 2^-32 of it. The
+// weights' sum is fp32 with a maximum of its own: scales of tokens may lie far apart.
 #pragma once
 
 #include "cache_attend.cuh"
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
           if (none)
             for (int x = 0; x < 1 << piece_shift; x += 16) *reinterpret_cast<uint4*>(scales + x) = make_uint4(0, 0, 0, 0);
           const int scaled = __popc(__ballot_sync(0xffffffffu, lane < copies && row >= 0));
+          __syncwarp();  // the zeros before the arrival
           if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.full[s], kStageBytes + (uint32_t)(scaled << piece_shift));
           __syncwarp();
           if (lane < copies) {

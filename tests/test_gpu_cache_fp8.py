@@ -382,6 +382,26 @@ def test_layers_strides_streams_and_graphs(aa, new):
         ref.check_attend(out, c.attend(*args, layer=2, return_lse=True)[1], want)
 
 
+@pytest.mark.parametrize("max_q", [0, 1, 4, 60, 1000])
+def test_max_q_is_a_hint(aa, max_q):
+    d = dr.make_batch8(8, [60, 500, 129], [1, 150, 40], 8, 2, 128, 64, device="cuda") | {"max_q": max_q}
+    _attend(aa, d, 64, 2, 128)
+
+
+@pytest.mark.parametrize("width", [1030, 4700])
+@pytest.mark.parametrize("lo", [0, 170])
+def test_wide_tables(aa, width, lo):
+    """Rows for which 16-bit copies are made, of four sequences at a time because of their tables' width; and, where one
+    sequence's would be too large, are not."""
+    new, kv, ps, Hq, Hkv, D = [70, 0, 90, 66, 80], [300, 50, 90, 200, 700], 64, 32, 8, 128
+    d = dr.make_batch8(width, kv, new, Hq, Hkv, D, ps, device="cuda")
+    d["table"] = torch.cat([d["table"], torch.full((5, width - d["table"].shape[1]), -1, dtype=torch.int32, device="cuda")], 1)
+    key_lo = torch.full((sum(new),), lo, dtype=torch.int32, device="cuda")
+    key_lo[::9] += 40
+    _attend(aa, d, ps, Hkv, D)
+    _attend(aa, d, ps, Hkv, D, key_lo=key_lo, anchor=True)
+
+
 # ------------------------------------------------------------------ pages and bookkeeping
 @pytest.mark.parametrize("n,ps,Hkv,D,L", [(1, 16, 1, 64, 1), (70, 16, 3, 64, 2), (9, 128, 8, 128, 3)])
 def test_copy_pages(aa, n, ps, Hkv, D, L):

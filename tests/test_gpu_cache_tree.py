@@ -130,6 +130,18 @@ def test_a_chain_is_what_attend_does_without_a_tree(aa, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("max_q", [0, 1, 5, 40, 1000])
+@pytest.mark.parametrize("Hq,D", [(8, 128), (2, 64)])
+def test_max_q_is_a_hint(aa, fp8, max_q, Hq, D):
+    new = [1, 150, 40]
+    d = _batch(fp8, 8, [60, 500, 129], new, Hq, 2, D, 64, device="cuda") | {"max_q": max_q}
+    seen, _ = dr.masks_of(dr.random_tree(torch.Generator().manual_seed(max_q), new).tolist(), d["cu"].tolist(), 0)
+    lo = torch.arange(sum(new), dtype=torch.int32, device="cuda") * 7 % 90
+    _attend(aa, d, 64, 2, D, dr.pack(seen, 3).cuda())
+    _attend(aa, d, 64, 2, D, dr.pack(seen, 3).cuda(), key_lo=lo, anchor=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("anchor", [False, True])
 @pytest.mark.parametrize("new", [3, 40, 150])
 def test_any_mask_with_windows_anchors_and_empty_rows(aa, fp8, anchor, new):
