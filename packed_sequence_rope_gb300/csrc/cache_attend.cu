@@ -7,8 +7,8 @@
 //   drafted tree the cached keys from key_lo on and the new ones of the row's mask
 //   O_i = sum_j softmax_j(scale * q_i . k_j) v_j, LSE_i = ln sum_j exp(...)
 // in one pass with the running maximum and sum of the softmax. This file checks the
-// arguments and chooses between cache_attend_short.cu (few rows per sequence: the
-// keys are read once, HBM-bound) and cache_attend_chunk.cu (tcgen05 products).
+// arguments and chooses between cache_attend_short.cuh (few rows per sequence: the
+// keys are read once, HBM-bound) and cache_attend_chunk.cuh (tcgen05 products).
 #include <algorithm>
 #include <cmath>
 

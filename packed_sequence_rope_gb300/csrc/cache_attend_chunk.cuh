@@ -1,5 +1,5 @@
 // Attention of chunks of new tokens over the paged cache (prompts, and any
-// batch with more rows per sequence than cache_attend_short.cu takes).
+// batch with more rows per sequence than cache_attend_short.cuh takes).
 //
 // Rows are packed: row r of a 128-row tile is (token r / group, query head
 // r % group) of one kv head, so a grouped-query layer fills the tensor cores'
