@@ -617,7 +617,7 @@ aa_status aa_cache_accept(aa_cache_t cache, const aa_cache_batch* batch, const i
  * 128, and 32 bytes per sequence and per 256 rows of a kv head more. Few new tokens
  * over long contexts: the results of up to 76 splits, 4 * D + 8 bytes per row and split.
  * 256 bytes where nothing is split. Chunks over 8-bit pages whose sequences have more
- * than 2 * D rows (max_q times the query heads of a kv head): 16-bit copies of a few
+ * than 256 rows (max_q times the query heads of a kv head): 16-bit copies of a few
  * sequences' keys and values more, 4 * D * Hkv bytes per position of their tables, up to 1 GiB. A smaller batch may need more. 0 for invalid
  * sizes. */
 size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32_t total_tokens, int32_t max_q,

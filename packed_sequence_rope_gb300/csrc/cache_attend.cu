@@ -41,21 +41,22 @@ static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_
 // once per 128; with more rows the codes are made bf16 ahead of the chunk kernel of 16-bit
 // pages (kWide). Measured, microseconds of the three, 8 kv heads of 128, group 4:
 //   rows, sequences   300 keys             2048                 16384
-//   32, 1             15.0 / 16.4 / 18.6   14.5 / 20.9 / 24.9   26.9 / 35.0 / 51.7
-//   32, 42            33.0 / 36.0 / 47.4   99.0 / 119 / 181     466 / 654 / 1238
-//   64, 1             26.9 / 16.7 / 18.6   24.7 / 20.8 / 25.9   45.1 / 36.3 / 53.4
-//   64, 42            59.7 / 37.7 / 47.3   173 / 121 / 183      923 / 657 / 1243
-//   256, 8            92.3 / 26.8 / 23.3   207 / 58.0 / 59.7    787 / 269 / 268
-//   256, 42           219 / 58.1 / 71.9    679 / 226 / 206      3682 / 1292 / 1297
-//   512, 42           407 / 100 / 76.9     1359 / 413 / 277     7355 / 2546 / 1783
-// With D = 64: 64 rows of 42 sequences 40.9 / 32.9 / 37.0, 134 / 98.8 / 124 and 962 / 423 /
-// 804, 256 rows 138 / 51.4 / 59.6, 520 / 185 / 129 and 3698 / 1109 / 761.
+//   32, 1             15.0 / 16.6 / 18.6   14.5 / 21.8 / 24.9   26.9 / 34.2 / 51.7
+//   32, 42            33.0 / 35.4 / 47.4   99.0 / 114 / 181     466 / 603 / 1238
+//   64, 1             26.9 / 16.5 / 18.6   24.7 / 22.7 / 24.7   45.1 / 35.3 / 53.7
+//   64, 42            59.7 / 36.8 / 47.3   173 / 117 / 183      923 / 609 / 1243
+//   256, 8            92.3 / 25.3 / 24.0   207 / 58.1 / 62.3    787 / 251 / 269
+//   256, 42           219 / 58.2 / 71.9    679 / 214 / 205      3682 / 1190 / 1310
+//   512, 42           407 / 105 / 77.3     1359 / 396 / 279     7355 / 2350 / 1791
+// With D = 64: 64 rows of 42 sequences 40.9 / 31.0 / 36.8, 134 / 89.2 / 126 and 962 / 358 /
+// 820, 256 rows 138 / 48.7 / 59.6, 520 / 169 / 131 and 3698 / 697 / 780, 512 rows 248 /
+// 84.5 / 60.6, 1035 / 297 / 189 and 7362 / 1379 / 1183.
 enum Path { kShort, kChunk, kShortCodes, kChunkCodes, kWide };
 
 static Path path_of(const aa_cache_s* c, int num_seqs, int max_q, int table_width, int group) {
   if (!c->fp8()) return takes_short(c, num_seqs, max_q, table_width, group) ? kShort : kChunk;
   const int64_t rows = (int64_t)std::max(max_q, 1) * group;
-  return rows <= 32 ? kShortCodes : rows <= 2 * c->cfg.head_dim || !wide_fits(c, table_width) ? kChunkCodes : kWide;
+  return rows <= 32 ? kShortCodes : rows <= 256 || !wide_fits(c, table_width) ? kChunkCodes : kWide;
 }
 
 extern "C" size_t aa_cache_attend_workspace_bytes(aa_cache_t c, int32_t num_seqs, int32_t total_tokens, int32_t max_q,

@@ -35,14 +35,15 @@
 //
 // 8-bit pages (k8): a unit is one row tile. Warps 12-15 make the tiles of keys bf16,
 // scales included, warps 16-19 the values, so that the products and the softmax are those
-// of 16-bit pages. The codes come in halves of a tile, through buffers of their own. The
+// of 16-bit pages. The codes come through buffers of their own. The
 // values that no row sees become zeros on the way. Warp 0 copies the keys', warp 2 the
 // values' (one warp for both was what the kernel waited for); warp 3 has nothing to do.
 // Converting costs about as many instructions as the softmax of a row tile, so the second
 // row tile's warps do it; four more warps beside them leave 80 registers a thread, which
 // the softmax does not fit. The loops are kept rolled: their code, the softmax's and the
-// issue loop's run at the same time and share the instruction cache (unrolled, five of
-// six cycles of a warp passed waiting for instructions).
+// issue loop's run at the same time and share the instruction cache (64 rows of 42
+// sequences over 16K keys of 128 channels: every second pass unrolled 693 us, the two halves of
+// a row alone 619, neither 608).
 #pragma once
 
 #include <algorithm>
@@ -221,14 +222,14 @@ struct ChunkSmem {
   // a piece's two row tiles of Q and one of the next piece: its first S product
   // does not wait for a copy
   static constexpr int kQ = k8 ? 1 : 3;
-  static constexpr int kHalves = k8 ? 4 : 1;  // 8-bit pages: half tiles of codes on their way, of keys and of values
+  static constexpr int kCodes = !k8 ? 1 : HD == 128 ? 2 : 4;  // 8-bit pages: tiles of codes on their way, of keys and of values
   alignas(1024) uint8_t q[kQ][kB][16384];
   alignas(1024) uint8_t k[kStages][kB][16384];
   alignas(1024) uint8_t v[kStages][kB][16384];
-  // 8-bit pages: codes of half a tile, keys (0) and values (1), and their scales
-  alignas(1024) uint8_t codes[2][kHalves][k8 ? kKeys / 2 * HD : 16];
-  alignas(16) uint8_t scales[2][kHalves][k8 ? kKeys / 2 : 16];
-  uint64_t c_full[2][kHalves], c_empty[2][kHalves];
+  // 8-bit pages: codes of keys (0) and values (1), and their scales
+  alignas(1024) uint8_t codes[2][kCodes][k8 ? kKeys * HD : 16];
+  alignas(16) uint8_t scales[2][kCodes][k8 ? kKeys : 16];
+  uint64_t c_full[2][kCodes], c_empty[2][kCodes];
   uint64_t k_ready[kStages];  // the keys are bf16
   uint64_t o_done;            // a step's product with the values
   uint64_t q_full[kQ], q_free[kQ];
@@ -287,35 +288,42 @@ __device__ __forceinline__ uint32_t visible_bits(int j, int lo, int hi) {
   return first <= 0 ? upto : first > 31 ? 0u : upto & (~0u << first);
 }
 
-// Half a tile of codes becomes rows [row0, row0 + 64) of a bf16 tile, by kConvertWarps
-// warps (thread tc of them). Rows whose bit of `seen` is 0 become zeros.
+// A tile of codes becomes a bf16 tile, by kConvertWarps warps (thread tc of them). Rows
+// whose bit of `seen` (64 rows each) is 0 become zeros.
 template <int HD>
-__device__ __forceinline__ void convert_half(const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int row0, int tc,
-                                             uint64_t seen) {
-  constexpr int kPerRow = HD / 64, kChunks = kKeys / 2 * HD / 16 / (32 * kConvertWarps);  // 16-byte chunks of codes a thread takes
-  // Eight lanes take four chunks of rows r and r ^ 5: they meet eight different groups of
-  // banks in both swizzles, where they read and where they write.
-  const int c = tc & 3, flip = tc & 4 ? 5 : 0, r0 = tc >> 3 << 1;
-#pragma unroll 2
-  for (int i = 0; i < kChunks; ++i) {
-    const int row = (i / kPerRow * 32 + r0) ^ flip, block = i % kPerRow;
-    const uint4 x = *reinterpret_cast<const uint4*>(
-        codes + (HD == 128 ? sw128_chunk(row, block * 4 + c) : (uint32_t)(row * 64 + ((c ^ (row >> 1 & 3)) << 4))));
-    uint4 y[2];
-    decode16(x, scales[row], !(seen >> row & 1), y);
-    uint8_t* out = tile + block * 16384;
-    *reinterpret_cast<uint4*>(out + sw128_chunk(row0 + row, 2 * c)) = y[0];
-    *reinterpret_cast<uint4*>(out + sw128_chunk(row0 + row, 2 * c + 1)) = y[1];
+__device__ __forceinline__ void convert_tile(const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int tc,
+                                             uint64_t seen0, uint64_t seen1) {
+  // Eight lanes take four 16-byte chunks of rows r and r ^ 5: they meet eight different
+  // groups of banks in both swizzles, where they read and where they write. A thread's
+  // rows are 32 apart, so that its places in the swizzles stay the same.
+  constexpr int kStep = 8 * kConvertWarps;
+  static_assert(kStep == 32, "rows of a pass");
+  const int c = tc & 3, r = (tc >> 3 << 1) ^ (tc & 4 ? 5 : 0);
+  const uint8_t* from = codes + (HD == 128 ? sw128_chunk(r, c) : (uint32_t)(r * 64 + ((c ^ (r >> 1 & 3)) << 4)));
+  const uint32_t to = sw128_chunk(r, 2 * c);
+#pragma unroll 1
+  for (int row = r; row < kKeys; row += kStep) {
+    const int byte = scales[row];
+    const uint32_t up = (row < 64 ? seen0 : seen1) >> (row & 63) & 1 ? factor_of(byte) : 0u;
+#pragma unroll 1
+    for (int block = 0; block < HD / 64; ++block) {  // of 64 channels
+      uint4 y[2];
+      decode16(*reinterpret_cast<const uint4*>(codes + (uint32_t)((from - codes) ^ (block << 6)) + (row - r) * HD), up, y);
+      if (has_more(byte)) times16(y, more_of(byte));
+      uint8_t* out = tile + block * 16384 + (row - r) * 128;
+      *reinterpret_cast<uint4*>(out + to) = y[0];
+      *reinterpret_cast<uint4*>(out + (to ^ 16)) = y[1];
+    }
   }
 }
 
-// 8-bit pages: a warp's copies of key tiles, half by half, of keys (v = 0) or values. A
-// tile's pages are asked for one tile ahead and not looked at before.
+// 8-bit pages: a warp's copies of the codes of key tiles, of keys (v = 0) or values. A tile's
+// pages are asked for one tile ahead and not looked at before.
 template <int HD>
 struct CodeCopies {
   int part, pieces, piece_shift;  // a tile's pages: lane `part` copies one of `pieces`
   int page = -1, j = -1;          // of the next tile; j < 0: not looked up
-  int n = 0;                      // half tiles asked for
+  int n = 0;                      // tiles asked for
   __device__ __forceinline__ explicit CodeCopies(int page_shift) {
     piece_shift = min(page_shift, 6);
     pieces = kKeys >> piece_shift;
@@ -342,33 +350,29 @@ struct CodeCopies {
     }
     const uint8_t* from = (v ? P.v_scales : P.k_scales) + row;
     const uint32_t bytes = 1u << piece_shift;
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int x = n % Smem::kHalves;
-      if (n >= Smem::kHalves && !warp_wait(&sm.c_empty[v][x], (n / Smem::kHalves - 1) & 1, b.err, abort_flag, 451)) return false;
-      const bool mine = part < pieces && part / (pieces / 2) == h;
-      const int at = (part & (pieces / 2 - 1)) << piece_shift;
-      uint8_t* scales = sm.scales[v][x] + at;
-      // the scales of pieces that are not looked up: zeros, as their codes will be
-      if (mine && row < 0)
-        for (uint32_t y = 0; y < bytes; y += 16) *reinterpret_cast<uint4*>(scales + y) = make_uint4(0, 0, 0, 0);
-      const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
-      __syncwarp();  // the zeros before the arrival
-      if (part == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][x], kKeys / 2 * HD + ((uint32_t)scaled << piece_shift));
-      __syncwarp();
-      if (mine) {
-        ptx::tma_load_2d(sm.codes[v][x] + at * HD, &tm, &sm.c_full[v][x], 0, row);
-        if (row >= 0) ptx::bulk_load(scales, from, bytes, &sm.c_full[v][x]);
-      }
-      ++n;
+    const int x = n % Smem::kCodes, at = part << piece_shift;
+    if (n >= Smem::kCodes && !warp_wait(&sm.c_empty[v][x], (n / Smem::kCodes - 1) & 1, b.err, abort_flag, 451)) return false;
+    const bool mine = part < pieces;
+    uint8_t* scales = sm.scales[v][x] + at;
+    // the scales of pieces that are not looked up: zeros, as their codes will be
+    if (mine && row < 0)
+      for (uint32_t y = 0; y < bytes; y += 16) *reinterpret_cast<uint4*>(scales + y) = make_uint4(0, 0, 0, 0);
+    const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
+    __syncwarp();  // the zeros before the arrival
+    if (part == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][x], kKeys * HD + ((uint32_t)scaled << piece_shift));
+    __syncwarp();
+    if (mine) {
+      ptx::tma_load_2d(sm.codes[v][x] + at * HD, &tm, &sm.c_full[v][x], 0, row);
+      if (row >= 0) ptx::bulk_load(scales, from, bytes, &sm.c_full[v][x]);
     }
+    ++n;
     return true;
   }
   // every copy lands before the CTA exits
   template <class Smem>
   __device__ __forceinline__ void drain(Smem& sm, int v, int32_t* err) const {
-    for (int u = max(n - Smem::kHalves, 0); u < n; ++u)
-      ptx::mbar_wait(&sm.c_full[v][u % Smem::kHalves], (u / Smem::kHalves) & 1, kDrainNs, err, 459);
+    for (int u = max(n - Smem::kCodes, 0); u < n; ++u)
+      ptx::mbar_wait(&sm.c_full[v][u % Smem::kCodes], (u / Smem::kCodes) & 1, kDrainNs, err, 459);
   }
 };
 
@@ -420,9 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sm.v_clean[s], k8 ? kConvertWarps : 2);
     }
     ptx::mbar_init(&sm.o_done, 1);
-    for (int s = 0; s < 2 * Smem::kHalves; ++s) {
-      ptx::mbar_init(&sm.c_full[s / Smem::kHalves][s % Smem::kHalves], 1);
-      ptx::mbar_init(&sm.c_empty[s / Smem::kHalves][s % Smem::kHalves], kConvertWarps);
+    for (int s = 0; s < 2 * Smem::kCodes; ++s) {
+      ptx::mbar_init(&sm.c_full[s / Smem::kCodes][s % Smem::kCodes], 1);
+      ptx::mbar_init(&sm.c_empty[s / Smem::kCodes][s % Smem::kCodes], kConvertWarps);
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -710,27 +714,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const KeyTiles<kKeys> keys(w.lo, w.hi, anchor);
       for (int i = w.first; i < w.first + w.take; ++i, ++ks) {
         const int s = ks % kStages, j0 = keys.tile(i) * kKeys;
-        if (ks >= kStages) ok = warp_wait(v ? &sm.v_empty[s] : &sm.k_empty[s], (ks / kStages - 1) & 1, b.err, abort_flag, 473);
-#pragma unroll 1
-        for (int h = 0; h < 2 && ok; ++h) {
-          // Values that no row sees have weight 0, but 0 * NaN is not: they become zeros. These are
-          // the rows outside [lo, hi] but for the anchor's, and where rows of the unit see
-          // nothing (or of a tree some only) those of the new tokens that none of them sees.
-          const int j = j0 + 64 * h;
-          uint64_t seen = ~0ull;
-          if (v) {
-            seen = keys_between(j, w.lo, w.hi) | (j == 0 && anchor && w.hi >= 0 ? 1ull : 0ull);
-            if (kTree ? j + 64 > w.gaps : w.gaps && j + 63 > w.p0)
-              seen &= kTree ? tree_seen_keys(P, w.q_row, w.p0 - w.gaps, w.tokens, w.gaps, w.hi + 1 - w.gaps, j)
-                            : seen_keys(P, w.q_row, w.p0, w.tokens, j);
+        // Values that no row sees have weight 0, but 0 * NaN is not: they become zeros. These are
+        // the rows outside [lo, hi] but for the anchor's, and where rows of the unit see
+        // nothing (or of a tree some only) those of the new tokens that none of them sees.
+        uint64_t seen[2] = {~0ull, ~0ull};
+        if (v && (j0 < w.lo || j0 + kKeys > (kTree ? min(w.gaps, w.hi + 1) : w.gaps ? w.p0 : w.hi + 1))) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = j0 + 64 * h;
+            seen[h] = keys_between(j, w.lo, w.hi) | (j == 0 && anchor && w.hi >= 0 ? 1ull : 0ull);
+            if (kTree)
+              seen[h] &= tree_seen_keys(P, w.q_row, w.p0 - w.gaps, w.tokens, w.gaps, w.hi + 1 - w.gaps, j);
+            else if (w.gaps && j + 63 > w.p0)
+              seen[h] &= seen_keys(P, w.q_row, w.p0, w.tokens, j);
           }
-          const int half = 2 * ks + h, x = half % Smem::kHalves;
-          if (!(ok = warp_wait(&sm.c_full[v][x], (half / Smem::kHalves) & 1, b.err, abort_flag, 471))) break;
-          convert_half<HD>(sm.codes[v][x], sm.scales[v][x], v ? sm.v[s][0] : sm.k[s][0], 64 * h, tc, seen);
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sm.c_empty[v][x]);
         }
-        if (!ok) break;
+        const int x = ks % Smem::kCodes;
+        if (ks >= kStages) ok = warp_wait(v ? &sm.v_empty[s] : &sm.k_empty[s], (ks / kStages - 1) & 1, b.err, abort_flag, 473);
+        if (!ok || !(ok = warp_wait(&sm.c_full[v][x], (ks / Smem::kCodes) & 1, b.err, abort_flag, 471))) break;
+        convert_tile<HD>(sm.codes[v][x], sm.scales[v][x], v ? sm.v[s][0] : sm.k[s][0], tc, seen[0], seen[1]);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.c_empty[v][x]);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(v ? &sm.v_clean[s] : &sm.k_ready[s]);

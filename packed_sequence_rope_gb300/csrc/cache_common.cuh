@@ -33,8 +33,7 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* __restrict__ cu_q, i
 // Four e4m3 numbers b0 .. b3 as bf16 pairs (b0, b2) and (b1, b3), exactly: sign, exponent
 // and significand moved to their places in bf16 mean 2^-120 times the number (a
 // subnormal one lands among bf16's subnormals), which one product undoes. NaN codes
-// become 480. Shifts and selections, two of the five on 16-bit halves, are
-// cheaper than the conversion to f16, which would also need f16 weights.
+// become 480. (There is a conversion to f16, but none to bf16.)
 __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t x, uint32_t up = 0x7b807b80u) {  // up: 2^120 twice
   const uint32_t even = ((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u);
   const uint32_t odd = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
@@ -54,11 +53,17 @@ __device__ __forceinline__ float exponent_of(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(0x4b000000u | byte) - 8388735.0f;  // 2^23 + byte - (2^23 + 127)
 }
 
-// Sixteen codes of a row whose scale has the byte `scale` as bf16, exactly. The factor is e4m3x4_to_bf16's 2^120 times the scale, 2^(scale - 7), in two parts where
-// bf16 does not reach. zero: zeros instead.
-__device__ __forceinline__ void decode16(const uint4& x, int scale, bool zero, uint4 (&y)[2]) {
-  uint32_t up = scale == 255 ? 0x7fc0u : (uint32_t)min(scale + 120, 254) << 7;
-  up = zero ? 0u : up | up << 16;
+// What a row's codes are multiplied by, twice: e4m3x4_to_bf16's 2^120 times its scale, for a
+// byte 2^(byte - 7). bf16 reaches 2^127; what is left is more_of(byte).
+__device__ __forceinline__ uint32_t factor_of(int byte) {
+  const uint32_t up = byte == 255 ? 0x7fc0u : (uint32_t)min(byte + 120, 254) << 7;
+  return up | up << 16;
+}
+__device__ __forceinline__ bool has_more(int byte) { return byte > 134 && byte < 255; }
+__device__ __forceinline__ uint32_t more_of(int byte) { return ((uint32_t)(byte - 7) << 7) * 0x10001u; }  // 2^(byte - 134)
+
+// Sixteen codes as bf16, times `up`, exactly.
+__device__ __forceinline__ void decode16(const uint4& x, uint32_t up, uint4 (&y)[2]) {
   const uint32_t four[4] = {x.x, x.y, x.z, x.w};
   uint32_t w[8];
 #pragma unroll
@@ -67,13 +72,18 @@ __device__ __forceinline__ void decode16(const uint4& x, int scale, bool zero, u
     w[2 * e] = __byte_perm(z.x, z.y, 0x5410);
     w[2 * e + 1] = __byte_perm(z.x, z.y, 0x7632);
   }
-  if (scale > 134 && scale < 255) {
-    const uint32_t more = (uint32_t)(scale - 7) << 7, more2 = more | more << 16;  // 2^(scale - 134)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[e]) : "r"(w[e]), "r"(more2));
-  }
   y[0] = make_uint4(w[0], w[1], w[2], w[3]);
   y[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void times16(uint4 (&y)[2], uint32_t by) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    for (uint32_t* w : {&y[i].x, &y[i].y, &y[i].z, &y[i].w}) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(*w) : "r"(*w), "r"(by));
+}
+// Sixteen codes of a row whose scale has the byte `byte`.
+__device__ __forceinline__ void decode16(const uint4& x, int byte, uint4 (&y)[2]) {
+  decode16(x, factor_of(byte), y);
+  if (has_more(byte)) times16(y, more_of(byte));
 }
 
 // One batch as the kernels see it.

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       const uint8_t* pages = h < b.Hkv ? P.k_pages : P.v_pages;
       if constexpr (k8) {
         const uint4 x = *reinterpret_cast<const uint4*>(pages + from * HD + 16 * chunk);
-        decode16(x, (h < b.Hkv ? P.k_scales : P.v_scales)[from], false, y);
+        decode16(x, (int)(h < b.Hkv ? P.k_scales : P.v_scales)[from], y);
       } else {
         const uint4* x = reinterpret_cast<const uint4*>(pages + (from * HD + 16 * chunk) * 2);
         y[0] = x[0];
