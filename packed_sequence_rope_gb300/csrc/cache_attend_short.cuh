@@ -45,7 +45,6 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
 
 constexpr float kWeightsUp = 7.0f;      // 8-bit pages: weights are 2^7 times what the maximum gives, at most 2^15
-constexpr float kLaneThreshold = 64.0f;  // and their sum is brought to a new maximum only where that is 2^64 times the last
 
 constexpr int kSplitRanks = 4, kSplitTiles = 8;
 
@@ -387,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
             mv[w] = fmaxf(mv[w], __shfl_xor_sync(0xffffffffu, mv[w], 1));
             mv[w] = fmaxf(mv[w], __shfl_xor_sync(0xffffffffu, mv[w], 2));
             need |= mv[w] > m[w] + kRescaleThreshold || (m[w] == -INFINITY && mv[w] > -INFINITY);
-            if (mt[w] > lane_m[w] + kLaneThreshold || (lane_m[w] == -INFINITY && mt[w] > -INFINITY)) {
+            if (mt[w] > lane_m[w] + kRescaleThreshold || (lane_m[w] == -INFINITY && mt[w] > -INFINITY)) {
               l[w] *= lane_m[w] == -INFINITY ? 0.f : exp2f(lane_m[w] - mt[w]);
               lane_m[w] = mt[w];
             }

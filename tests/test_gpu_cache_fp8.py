@@ -351,6 +351,25 @@ def test_scales_far_from_one(aa):
             _attend(aa, d, 16, 2, 128, tag=f"{new} {shift}")
 
 
+@pytest.mark.parametrize("new", [1, 7, 90])
+def test_growing_logits_over_large_values(aa, new):
+    """Later keys outweigh earlier ones by up to 2^60, step by step, over values of 2^100: what rows keep on the way stays in range."""
+    d = dr.make_batch8(9, [new + 1500], [new], 4, 2, 128, 64, device="cuda")
+    e = d["v_scales"].view(torch.uint8)
+    e.copy_((e.int() - e.int().min() + 217).clamp(27, 246).to(torch.uint8))
+    d["vd"] = dr.as_bf16(d["v_pages"], d["v_scales"]).cuda()
+    d["q"].fill_(0.25)
+    j = torch.arange(new + 1500, device="cuda")
+    # one code for all channels; logits 0.25 * 128 * value / sqrt(128) from 0 to 42 in steps
+    code = torch.round(j * 14.0 / len(j)).to(torch.float8_e4m3fn)
+    page = d["table"][0, (j // 64)].long()
+    d["k_pages"].view(torch.uint8)[0, page, :, j % 64] = code.view(torch.uint8)[:, None, None]
+    d["k_scales"].view(torch.uint8)[0, page, :, j % 64] = 127
+    d["kd"] = dr.as_bf16(d["k_pages"], d["k_scales"]).cuda()
+    o, _ = _attend(aa, d, 64, 2, 128)
+    assert torch.isfinite(o.float()).all()
+
+
 @pytest.mark.parametrize("new", [1, 5, 90])
 def test_layers_strides_streams_and_graphs(aa, new):
     kv, ps, Hq, Hkv, D = [new + 300, new + 7], 32, 8, 2, 128
