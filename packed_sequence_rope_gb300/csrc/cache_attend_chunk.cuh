@@ -861,7 +861,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = (m == -INFINITY) ? 0.f : exp2f(m - mn);
             l *= f;
             if (i > 0) {  // O holds earlier tiles: S(i) done implies their PV is done; with two S it does not
-              if (k8 && !warp_wait(&sm.o_done, (steps - 1) & 1, b.err, abort_flag, 484)) return false;
+              if (k8 && !warp_wait(&sm.o_done, (steps - 1) & 1, b.err, abort_flag, 484)) {
+                ptx::bar_and(pair_bar, 64, false);  // the partner's next meeting, if it has not given up here too
+                return false;
+              }
               if (k8) ptx::tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < HD / 32; ++c) {
