@@ -41,8 +41,8 @@ static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_
 // once per 128; with more rows the codes are made bf16 ahead of the chunk kernel of 16-bit
 // pages (kWide). Measured, microseconds of the three, 8 kv heads of 128, group 4:
 //   rows, sequences   300 keys             2048                 16384
-//   32, 1             15.0 / 16.6 / 18.6   14.5 / 21.8 / 24.9   26.9 / 34.2 / 51.7
-//   32, 42            33.0 / 35.4 / 47.4   99.0 / 114 / 181     466 / 603 / 1238
+//   32, 1             14.5 / 16.6 / 18.6   14.5 / 21.8 / 24.9   26.9 / 34.2 / 51.7
+//   32, 42            28.8 / 35.4 / 47.4   90.3 / 114 / 181     482 / 603 / 1238
 //   64, 1             26.9 / 16.5 / 18.6   24.7 / 22.7 / 24.7   45.1 / 35.3 / 53.7
 //   64, 42            59.7 / 36.8 / 47.3   173 / 117 / 183      923 / 609 / 1243
 //   256, 8            92.3 / 25.3 / 24.0   207 / 58.1 / 62.3    787 / 251 / 269

@@ -57,16 +57,19 @@ struct ShortParts {
 };
 
 // Keys of a tile. With 8-bit pages what a tile costs beside its keys (waits, maxima across
-// lanes) counts for more: 64 sequences to 32K keys 522 us with 64 keys, 450 with 128.
-template <bool k8>
-constexpr int kTileOf = k8 ? 128 : 64;
+// lanes) counts for more: 64 sequences to 32K keys 522 us with 64 keys, 450 with 128. At 32
+// rows a warp has 64 of 128 keys, which its registers do not hold: 42 sequences over 2048
+// and 16K keys 90.3 and 482 us with 64, 98.1 and 466 with 128; of 64 channels 57.5 and 335,
+// 69.7 and 502.
+template <int RT, bool k8>
+constexpr int kTileOf = k8 && RT == 1 ? 128 : 64;
 
-template <int HD, bool k8>
+template <int HD, int RT, bool k8>
 struct ShortSmem {
-  static constexpr int kTileKeys = kTileOf<k8>;
+  static constexpr int kTileKeys = kTileOf<RT, k8>;
   static constexpr int kB = k8 ? 1 : HD / 64;            // column blocks of a tile
   static constexpr int kRowBytes = k8 ? HD : 128;        // of a key in a block
-  static constexpr int kStages = k8 ? 3 : HD == 128 ? 3 : 4;
+  static constexpr int kStages = k8 ? (RT == 1 ? 3 : 6) : HD == 128 ? 3 : 4;
   static constexpr int kRowFloats = HD + 8;  // a warp's rows fall on different banks
   union {
     struct {
@@ -107,7 +110,7 @@ template <int HD, int RT, int kMask, bool k8>
 __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
     attend_short_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ AttendParams P, const ShortParts S) {
-  using Smem = ShortSmem<HD, k8>;
+  using Smem = ShortSmem<HD, RT, k8>;
   constexpr bool kLo = kMask != kMaskNone, kTree = kMask == kMaskTree;
   constexpr int kTileKeys = Smem::kTileKeys, kB = Smem::kB, kRowBytes = Smem::kRowBytes, kStages = Smem::kStages;
   constexpr int kKeyGroups = kWarps / RT, kWarpKeys = kTileKeys / kKeyGroups;
@@ -671,7 +674,7 @@ inline ShortShape shape_of(const aa_cache_s* c, int num_seqs, int max_q, int tab
 template <int HD, int RT, int kMask, bool k8>
 cudaError_t launch(const aa_cache_s* c, const AttendParams& P, const ShortShape& f, const ShortParts& S, cudaStream_t s) {
   const auto kernel = attend_short_kernel<HD, RT, kMask, k8>;
-  const size_t smem = sizeof(ShortSmem<HD, k8>);
+  const size_t smem = sizeof(ShortSmem<HD, RT, k8>);
   static std::once_flag once[kMaxDevices];
   static cudaError_t result[kMaxDevices];
   cudaError_t e = once_per_device(once, result, c->device, [&] {
