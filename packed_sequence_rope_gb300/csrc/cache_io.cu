@@ -10,7 +10,7 @@
 // attention in bf16's normal range, e <= 119 what a page holds within its range. A row with a value that is not finite has byte
 // 255, which makes all of it NaN.
 //
-// Both are bound by HBM (a decoding step's few rows by the launch): every byte
+// They are bound by HBM (a decoding step's few rows by the launch): every byte
 // is read and written once, in 16-byte accesses. A compaction of 256 pages of
 // 128 KB in 32 layers takes 615 us, 7.0 TB/s (a copy of the same bytes: 6.77).
 #include <algorithm>
@@ -117,8 +117,10 @@ __device__ __forceinline__ int64_t find_slot(const BatchParams& b, int t, int pa
 // L: the pairing (0, 1), or 2 to store the keys as they are. A block takes
 // kTokens rows; as in rope_axes_kernel the angles of a token are computed once
 // for all heads, while the first row is in flight.
+// k8: four blocks per SM, 64 registers (13.7 thousand tokens with their reading back 84.6 us;
+// left alone it takes 80, 89.2; five blocks spill, 110).
 template <int HD, int L, int kTokens, bool k8>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kThreads, k8 ? 4 : 1) cache_append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int kHalf = HD / 2, kChunks = HD / 16, kRows = kThreads / kChunks / kTokens;
   static_assert(kTokens <= kThreads / 32, "a warp looks up each token");
   __shared__ float2 cs[L == 2 ? 1 : kTokens][kHalf];
@@ -144,7 +146,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   if constexpr (L != 2) {
     for (int e = kThreads - 1 - (int)threadIdx.x; e < kTokens * kHalf; e += kThreads) {  // the searching warps come last
       const int at = e / kHalf, p = e % kHalf;
-      if (t0 + at < b.T) cs[at][p] = axes_cs(P.tab, P.pos, b.T, t0 + at, p);
+      if (t0 + at < b.T)
+        cs[at][p] = k8 ? axes_cs_fine(P.tab, P.pos, b.T, t0 + at, p) : axes_cs(P.tab, P.pos, b.T, t0 + at, p);
     }
   }
   __syncthreads();

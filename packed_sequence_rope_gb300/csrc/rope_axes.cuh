@@ -42,6 +42,22 @@ __device__ __forceinline__ float2 axes_cs(const AxesTable& tab, const int32_t* _
   return make_float2(c, s);
 }
 
+// The same where the result is rounded to few bits from fp32 itself, and an angle that is
+// off by 1e-7 moves some values across a border: the quarter turn is taken off in integers, so
+// that what is left, at most 1/8 turn, loses at most 2e-8 rad to fp32.
+__device__ __forceinline__ float2 axes_cs_fine(const AxesTable& tab, const int32_t* __restrict__ pos, int64_t T, int64_t t,
+                                               int p) {
+  const int64_t at = __ldg(pos + tab.axis[p] * T + t);
+  const uint64_t turns = (uint64_t)at * tab.turn[p];
+  const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62) & 3u;
+  const int64_t rest = (int64_t)(turns - ((uint64_t)quarter << 62));       // in [-2^61, 2^61)
+  const int32_t half_turns = (int32_t)((rest + (1ll << 30)) >> 31);        // angle / pi * 2^32
+  float c, s;
+  sincospif((float)half_turns * 0x1p-32f, &s, &c);
+  const float x = quarter & 1u ? -s : c, y = quarter & 1u ? c : s;
+  return quarter & 2u ? make_float2(-x, -y) : make_float2(x, y);
+}
+
 // Eight pairs of one row in registers: elements [16 i, 16 i + 16) for adjacent
 // pairs (L = 0), [8 i, 8 i + 8) and HD / 2 further for split halves (L = 1).
 template <int HD, int L>
