@@ -35,9 +35,9 @@
 //
 // 8-bit pages (k8): a unit is one row tile. Warps 12-15 make the tiles of keys bf16,
 // scales included, warps 16-19 the values, so that the products and the softmax are those
-// of 16-bit pages. The codes come through buffers of their own. The
-// values that no row sees become zeros on the way. Warp 0 copies the keys', warp 2 the
-// values' (one warp for both was what the kernel waited for); warp 3 has nothing to do.
+// of 16-bit pages. The codes come through buffers of their own; the values that no row
+// sees become zeros on the way. Warp 0 copies the keys' codes, warp 2 the values' (one
+// warp for both was what the kernel waited for); warp 3 has nothing to do.
 // Converting costs about as many instructions as the softmax of a row tile, so the second
 // row tile's warps do it; four more warps beside them leave 80 registers a thread, which
 // the softmax does not fit. The loops are kept rolled: their code, the softmax's and the
@@ -220,7 +220,7 @@ struct ChunkSmem {
   static constexpr int kB = HD / 64;
   static constexpr int kStages = HD == 128 ? 2 : 4;
   // a piece's two row tiles of Q and one of the next piece: its first S product
-  // does not wait for a copy
+  // does not wait for a copy (8-bit pages: the codes have that room)
   static constexpr int kQ = k8 ? 1 : 3;
   static constexpr int kCodes = !k8 ? 1 : HD == 128 ? 2 : 4;  // 8-bit pages: tiles of codes on their way, of keys and of values
   alignas(1024) uint8_t q[kQ][kB][16384];

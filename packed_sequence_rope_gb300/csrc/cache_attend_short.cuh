@@ -128,19 +128,25 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
   const int64_t shares = (int64_t)ranks * S.splits, share = (int64_t)ranks * blockIdx.y + rank;  // of a unit's tiles
   const int unit = (int)(blockIdx.x / ranks);
   const int g = unit % b.Hkv, seq = unit / b.Hkv;
-  const SeqSpan span = load_seq(b, seq, P.page_shift);
   const int tile_tokens = 16 * RT / P.group;
-
-  if (tid == 0) {
-    ptx::tma_prefetch_desc(&tmK);
-    ptx::tma_prefetch_desc(&tmV);
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&sm.full[s], 1);
-      ptx::mbar_init(&sm.empty[s], kWarps);
+  auto set_up = [&] {
+    if (tid == 0) {
+      ptx::tma_prefetch_desc(&tmK);
+      ptx::tma_prefetch_desc(&tmV);
+      for (int s = 0; s < kStages; ++s) {
+        ptx::mbar_init(&sm.full[s], 1);
+        ptx::mbar_init(&sm.empty[s], kWarps);
+      }
+      ptx::fence_mbar_init();
     }
-    ptx::fence_mbar_init();
+    __syncthreads();
+  };
+  if constexpr (k8) {  // launched as a dependent: the start-up overlaps the kernel before (one token over 1000 keys 7.7 us, else 10.2)
+    set_up();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   }
-  __syncthreads();
+  const SeqSpan span = load_seq(b, seq, P.page_shift);
+  if constexpr (!k8) set_up();
 
   int steps = 0;  // tiles this CTA has taken so far: the ring's position
   // one pass, unless the sequence has more new tokens than max_q promised
@@ -686,12 +692,14 @@ cudaError_t launch(const aa_cache_s* c, const AttendParams& P, const ShortShape&
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)f.ranks;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)f.ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = k8 ? 2 : 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, c->k_map64, c->v_map64, P, S)) != cudaSuccess || f.splits == 1) return e;
   const int64_t threads = (int64_t)P.batch.T * P.Hq * (HD / 4);
   return launch_after(short_join_kernel<HD>, dim3((unsigned)((threads + 255) / 256)), 256, 0, s, P, S);
