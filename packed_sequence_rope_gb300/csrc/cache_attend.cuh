@@ -132,23 +132,6 @@ __device__ __forceinline__ int pool_row(const BatchParams& b, int seq, int g, in
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Launch a kernel whose start-up may overlap the kernel before it (it waits with
-// griddepcontrol.wait before it reads anything).
-template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Up to so many keys per page table the chunk kernel takes whole units. Measured,
 // 32 / 8 heads of 128, microseconds whole / cut: 8 sequences of 32 new tokens over
 // 700 keys 17.5 / 21.5, 42 of 128 over 500 65.6 / 85.4; over 1000 keys 21.0 / 22.9

@@ -86,6 +86,23 @@ __device__ __forceinline__ void decode16(const uint4& x, int byte, uint4 (&y)[2]
   if (has_more(byte)) times16(y, more_of(byte));
 }
 
+// Launch a kernel whose start-up may overlap the kernel before it (it waits with
+// griddepcontrol.wait before it reads anything).
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // One batch as the kernels see it.
 struct BatchParams {
   const int32_t *table, *cu_q, *kv_len;

@@ -118,7 +118,7 @@ __device__ __forceinline__ int64_t find_slot(const BatchParams& b, int t, int pa
 // kTokens rows; as in rope_axes_kernel the angles of a token are computed once
 // for all heads, while the first row is in flight.
 // k8: four blocks per SM, 64 registers (13.7 thousand tokens with their reading back 84.6 us;
-// left alone it takes 80, 89.2; five blocks spill, 110).
+// left alone it takes 80, 89.2; five blocks spill, 110), and launched as a dependent (81.4).
 template <int HD, int L, int kTokens, bool k8>
 __global__ void __launch_bounds__(kThreads, k8 ? 4 : 1) cache_append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int kHalf = HD / 2, kChunks = HD / 16, kRows = kThreads / kChunks / kTokens;
@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, k8 ? 4 : 1) cache_append_kernel(cons
            chunk);
   };
   Pairs8<HD, L == 2 ? 0 : L> x;
+  if constexpr (k8) asm volatile("griddepcontrol.wait;" ::: "memory");
   load(x, row % kRows);
   if (warp < kTokens) {
     const int64_t at = find_slot(b, t0 + warp, P.page_shift);
@@ -191,6 +192,10 @@ __global__ void __launch_bounds__(kThreads, k8 ? 4 : 1) cache_append_kernel(cons
 
 template <int HD, int L, bool k8>
 cudaError_t launch_append(const AppendParams& P, cudaStream_t s) {
+  if constexpr (k8)
+    return P.batch.T <= kFewTokens
+               ? launch_after(cache_append_kernel<HD, L, 1, k8>, dim3((unsigned)P.batch.T), kThreads, 0, s, P)
+               : launch_after(cache_append_kernel<HD, L, 2, k8>, dim3((unsigned)((P.batch.T + 1) / 2)), kThreads, 0, s, P);
   if (P.batch.T <= kFewTokens)
     cache_append_kernel<HD, L, 1, k8><<<(unsigned)P.batch.T, kThreads, 0, s>>>(P);
   else
@@ -219,6 +224,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   __shared__ int64_t slot[kTokens];
   const BatchParams& b = P.batch;
   const int t0 = (int)blockIdx.x * kTokens, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp < kTokens) {
     const int64_t at = find_slot(b, t0 + warp, P.page_shift);
     if ((threadIdx.x & 31) == 0) slot[warp] = at;
@@ -250,11 +256,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 
 template <int HD, bool k8>
 cudaError_t launch_read(const ReadParams& P, cudaStream_t s) {
-  if (P.batch.T <= kFewTokens)
-    cache_read_kernel<HD, 1, k8><<<(unsigned)P.batch.T, kThreads, 0, s>>>(P);
-  else
-    cache_read_kernel<HD, 4, k8><<<(unsigned)((P.batch.T + 3) / 4), kThreads, 0, s>>>(P);
-  return cudaGetLastError();
+  return P.batch.T <= kFewTokens
+             ? launch_after(cache_read_kernel<HD, 1, k8>, dim3((unsigned)P.batch.T), kThreads, 0, s, P)
+             : launch_after(cache_read_kernel<HD, 4, k8>, dim3((unsigned)((P.batch.T + 3) / 4)), kThreads, 0, s, P);
 }
 
 // The pairs of a copy travel as a kernel argument: no device memory, nothing to

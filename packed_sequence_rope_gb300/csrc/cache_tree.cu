@@ -19,6 +19,7 @@ struct MaskParams {
 // its row is complete when the walk leaves it.
 __global__ void __launch_bounds__(kThreads) tree_masks_kernel(const MaskParams P) {
   const int t0 = (int)blockIdx.x * kThreads + (int)(threadIdx.x & ~31u), t = t0 + (int)(threadIdx.x & 31);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t0 >= P.T) return;
   // the sequence of the warp's first token; later ones follow from it
   int seq = warp_find_seq(P.cu_q, P.B, t0);
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
   const BatchParams& b = P.batch;
   const int seq = (int)blockIdx.y, layer = (int)blockIdx.x, lane = threadIdx.x & 31;
   const int32_t* path = P.path + (int64_t)seq * P.width;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = __ldg(b.cu_q + seq + 1) - __ldg(b.cu_q + seq), base = __ldg(b.kv_len + seq) - n;
   int count = 0, last = -1;
   bool bad_path = false;
@@ -172,8 +174,8 @@ extern "C" aa_status aa_cache_tree_masks(aa_cache_t c, const int32_t* parents, c
         return fail(AA_ERR_INVALID_ARG, std::string(all[w].name) + " overlaps " + all[r].name);
   }
   const MaskParams P{parents, cu_q, kv_len, mask, pos, c->err, num_seqs, total_tokens, tree_words};
-  tree_masks_kernel<<<(unsigned)((T + kThreads - 1) / kThreads), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(tree_masks_kernel, dim3((unsigned)((T + kThreads - 1) / kThreads)), kThreads, 0,
+                                     reinterpret_cast<cudaStream_t>(stream), P);
   return e == cudaSuccess ? AA_OK : cuda_fail(e, "tree_masks_kernel launch");
 }
 
@@ -206,9 +208,8 @@ extern "C" aa_status aa_cache_accept(aa_cache_t c, const aa_cache_batch* batch, 
     S.batch.cu_q += first;
     S.batch.kv_len += first;
     S.path += (int64_t)first * path_width;
-    accept_kernel<<<dim3((unsigned)c->cfg.num_layers, (unsigned)some), kThreads, 0,
-                    reinterpret_cast<cudaStream_t>(stream)>>>(S);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(accept_kernel, dim3((unsigned)c->cfg.num_layers, (unsigned)some), kThreads, 0,
+                                       reinterpret_cast<cudaStream_t>(stream), S);
     if (e != cudaSuccess) return cuda_fail(e, "accept_kernel launch");
   }
   return AA_OK;
