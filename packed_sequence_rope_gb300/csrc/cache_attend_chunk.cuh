@@ -355,8 +355,10 @@ struct CodeCopies {
     const bool mine = part < pieces;
     uint8_t* scales = sm.scales[v][x] + at;
     // the scales of pieces that are not looked up: zeros, as their codes will be
-    if (mine && row < 0)
+    if (mine && row < 0) {
       for (uint32_t y = 0; y < bytes; y += 16) *reinterpret_cast<uint4*>(scales + y) = make_uint4(0, 0, 0, 0);
+      ptx::fence_proxy_async_smem();  // this lane's next copy to the same bytes comes after
+    }
     const int scaled = __popc(__ballot_sync(0xffffffffu, mine && row >= 0));
     __syncwarp();  // the zeros before the arrival
     if (part == 0) ptx::mbar_arrive_expect_tx(&sm.c_full[v][x], kKeys * HD + ((uint32_t)scaled << piece_shift));

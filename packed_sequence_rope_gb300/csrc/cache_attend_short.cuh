@@ -191,8 +191,10 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
           // the scales of pieces that are not looked up: zeros, as their codes will be
           const bool none = lane < copies && row < 0;
           uint8_t* scales = sm.scales[s][is_v] + (at << piece_shift);
-          if (none)
+          if (none) {
             for (int x = 0; x < 1 << piece_shift; x += 16) *reinterpret_cast<uint4*>(scales + x) = make_uint4(0, 0, 0, 0);
+            ptx::fence_proxy_async_smem();  // this lane's next copy to the same bytes comes after
+          }
           const int scaled = __popc(__ballot_sync(0xffffffffu, lane < copies && row >= 0));
           __syncwarp();  // the zeros before the arrival
           if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.full[s], kStageBytes + (uint32_t)(scaled << piece_shift));

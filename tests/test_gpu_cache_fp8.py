@@ -421,6 +421,38 @@ def test_wide_tables(aa, width, lo):
     _attend(aa, d, ps, Hkv, D, key_lo=key_lo, anchor=True)
 
 
+@pytest.mark.parametrize("new,max_q", [(1, 1), (6, 6), (40, 1), (100, 100)])
+@pytest.mark.parametrize("ps", [16, 64])
+@pytest.mark.parametrize("D", [64, 128])
+def test_buffers_of_unread_pages_are_used_again(aa, new, max_q, ps, D):
+    """Pages that are not read, for a bad number, in front of a window or behind the last key, leave zeros for scales; the same
+    buffers then take tiles whose scales are far from those. A bad page's keys and values are zeros."""
+    Hq, Hkv, kv = 4, 2, [new + 3000, new + 1777]
+    d = dr.make_batch8(new + ps, kv, [new, new], Hq, Hkv, D, ps, device="cuda")
+    spare = next(p for p in range(d["P"]) if p not in d["used"])  # what the bad numbers stand for
+    for x in "kv":
+        d[x + "_pages"].view(torch.uint8)[:, spare].zero_()
+        d[x + "d"] = dr.as_bf16(d[x + "_pages"], d[x + "_scales"]).cuda()
+    holes = torch.zeros(d["table"].shape, dtype=torch.bool)
+    holes[:, 1::5] = True  # behind the last page too, where nothing is looked up
+    holes[:, (max(kv) - new) // ps:] = False
+    holes &= (d["table"] >= 0).cpu()
+    bad = torch.where(holes.cuda(), d["P"] + 5, d["table"])
+    zeros = torch.where(holes.cuda(), spare, d["table"])
+    p = torch.cat([torch.arange(k - new, k) for k in kv])
+    with _cache(aa, d, ps, Hkv, D) as c:
+        for lo, anchor in ((None, False), ((p - 1500).clamp(min=0), True)):
+            lo = None if lo is None else lo.to(torch.int32).cuda()
+            first = c.attend(d["q"], bad, d["cu"], d["kv"], max_q, key_lo=lo, anchor=anchor, return_lse=True)
+            with pytest.raises(aa.AAError):
+                c.check_device_error()
+            want = ref.attend(d["q"], d["kd"], d["vd"], zeros, d["cu"], d["kv"], 0, lo, anchor)
+            ref.check_attend(*first, want)
+            for _ in range(3):
+                again = c.attend(d["q"], bad, d["cu"], d["kv"], max_q, key_lo=lo, anchor=anchor, return_lse=True)
+                assert all(torch.equal(a, b) for a, b in zip(again, first))
+
+
 # ------------------------------------------------------------------ pages and bookkeeping
 @pytest.mark.parametrize("n,ps,Hkv,D,L", [(1, 16, 1, 64, 1), (70, 16, 3, 64, 2), (9, 128, 8, 128, 3)])
 def test_copy_pages(aa, n, ps, Hkv, D, L):
