@@ -120,7 +120,7 @@ __device__ __forceinline__ int64_t find_slot(const BatchParams& b, int t, int pa
 // k8: four blocks per SM, 64 registers (13.7 thousand tokens with their reading back 84.6 us;
 // left alone it takes 80, 89.2; five blocks spill, 110), and launched as a dependent (81.4).
 template <int HD, int L, int kTokens, bool k8>
-__global__ void __launch_bounds__(kThreads, k8 ? 4 : 1) cache_append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kThreads, k8 ? 4 : 0) cache_append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int kHalf = HD / 2, kChunks = HD / 16, kRows = kThreads / kChunks / kTokens;
   static_assert(kTokens <= kThreads / 32, "a warp looks up each token");
   __shared__ float2 cs[L == 2 ? 1 : kTokens][kHalf];
