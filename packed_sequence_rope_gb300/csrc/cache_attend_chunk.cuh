@@ -422,13 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kStages; ++s) {
       for (uint64_t* bar : {&sm.k_full[s], &sm.k_empty[s], &sm.v_full[s], &sm.v_empty[s]}) ptx::mbar_init(bar, 1);
-      ptx::mbar_init(&sm.k_ready[s], kConvertWarps);
       ptx::mbar_init(&sm.v_clean[s], k8 ? kConvertWarps : 2);
+      if constexpr (k8) ptx::mbar_init(&sm.k_ready[s], kConvertWarps);
     }
-    ptx::mbar_init(&sm.o_done, 1);
-    for (int s = 0; s < 2 * Smem::kCodes; ++s) {
-      ptx::mbar_init(&sm.c_full[s / Smem::kCodes][s % Smem::kCodes], 1);
-      ptx::mbar_init(&sm.c_empty[s / Smem::kCodes][s % Smem::kCodes], kConvertWarps);
+    if constexpr (k8) {
+      ptx::mbar_init(&sm.o_done, 1);
+      for (int s = 0; s < 2 * Smem::kCodes; ++s) {
+        ptx::mbar_init(&sm.c_full[s / Smem::kCodes][s % Smem::kCodes], 1);
+        ptx::mbar_init(&sm.c_empty[s / Smem::kCodes][s % Smem::kCodes], kConvertWarps);
+      }
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
