@@ -29,11 +29,13 @@
 // The other operands are f16 then, brought into its range by powers of two. A row of
 // queries is multiplied by the one that takes its maximum to 2^14: what is above 2^-21 of
 // the maximum stays exact, the rest is off by at most 2^-39 of it. The keys' scales
-// multiply the logits s. A value's scale 2^e joins its weight, 2^(s + e - m) with m the
+// multiply what the products give, the logits s. A value's scale 2^e joins its weight, 2^(s + e - m) with m the
 // row's running maximum of s + e, times 2^7. Weights are then below 2^15; those above 2^-21
 // of the largest are rounded to 11 bits, the others are off by at most 2^-32 of it. The
 // weights' sum is fp32 with a maximum of its own: scales of tokens may lie far apart.
 #pragma once
+
+#include <cfloat>
 
 #include "cache_attend.cuh"
 
@@ -224,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
       const int row0 = rg * 16 + (lane >> 2);
       int row_lo[2], row_hi[2];  // this lane's two rows' visible keys
       uint32_t qf[HD / 16][4];
-      float sl2[2] = {P.scale_log2, P.scale_log2};
+      float sl2[2] = {P.scale_log2, P.scale_log2};  // 8-bit pages: and what takes the row's power of two off again
+      bool apart = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = row0 + 8 * e, tok = row / P.group;
@@ -259,9 +262,22 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
             }
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const uint32_t up = min(268u - (top >> 7), 253u);  // biased exponent of the power
-          const float by = __uint_as_float(up << 23);
-          sl2[e] = P.scale_log2 * __uint_as_float((254u - up) << 23);
+          const uint32_t up = top ? min(268u - (top >> 7), 253u) : 127u;  // biased exponent of the power
+          const float by = __uint_as_float(up << 23), back = __uint_as_float((254u - up) << 23);
+          // A product (below 2^31) becomes a logit by way of sl2, then its key's scale (2^-124 to
+          // 2^119): what stands between stays in fp32's range for queries of some 2^-100 to 2^100. Of
+          // other rows a part of sl2 is left for the end.
+          float rest = 1.f;
+          sl2[e] *= back;
+          if (sl2[e] < 0x1p-120f) {
+            rest = P.scale_log2 * 0x1p100f * back;
+            sl2[e] = 0x1p-100f;
+          } else if (sl2[e] >= 0x1p90f) {
+            rest = fminf(P.scale_log2 * 0x1p-60f * back, FLT_MAX);
+            sl2[e] = 0x1p60f;
+          }
+          sm.m[warp][(lane >> 2) + 8 * e] = rest;
+          apart |= rest != 1.f;
 #pragma unroll
           for (int ks = 0; ks < HD / 16; ++ks) {
             const float2 a = ptx::unpack_bf16x2(qf[ks][e]), c = ptx::unpack_bf16x2(qf[ks][e + 2]);
@@ -269,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
             qf[ks][e + 2] = ptx::pack_f16x2(c.x * by, c.y * by);  // 2 and 3
           }
         }
+        apart = __any_sync(0xffffffffu, apart);
+        __syncwarp();
       }
       const int all_lo = __reduce_max_sync(0xffffffffu, max(row_lo[0], row_lo[1]));
       const int all_hi = __reduce_min_sync(0xffffffffu, min(row_hi[0], row_hi[1]));
@@ -301,10 +319,15 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
             const int at = kg * kWarpKeys + e * 8 + 2 * (lane & 3);
             const uint32_t of_k = *reinterpret_cast<const uint16_t*>(&sm.scales[s][0][at]);
             const float s0 = scale_of(of_k & 255u), s1 = scale_of(of_k >> 8);
-            sc[e][0] *= s0;
-            sc[e][1] *= s1;
-            sc[e][2] *= s0;
-            sc[e][3] *= s1;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[e][x] = sc[e][x] * sl2[x >> 1] * (x & 1 ? s1 : s0);
+          }
+          if (apart) {
+            const float rest[2] = {sm.m[warp][lane >> 2], sm.m[warp][(lane >> 2) + 8]};
+#pragma unroll
+            for (int e = 0; e < kWarpKeys / 8; ++e)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) sc[e][x] *= rest[x >> 1];
           }
         } else {
 #pragma unroll
@@ -385,7 +408,6 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
             const float e0 = exponent_of(of_v & 255u), e1 = exponent_of(of_v >> 8);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              sc[e][x] *= sl2[x >> 1];
               sv[e][x] = sc[e][x] + (x & 1 ? e1 : e0);
               mt[x >> 1] = fmaxf(mt[x >> 1], sc[e][x]);
               mv[x >> 1] = fmaxf(mv[x >> 1], sv[e][x]);

@@ -351,6 +351,40 @@ def test_scales_far_from_one(aa):
             _attend(aa, d, 16, 2, 128, tag=f"{new} {shift}")
 
 
+def _set_scales(d, x, top):
+    """Keys or values (x) moved by a power of two: the largest scale becomes 2^(top - 127)."""
+    e = d[x + "_scales"].view(torch.uint8)
+    by = top - int(e.max())
+    e.copy_((e.int() + by).clamp(27, 246).to(torch.uint8))
+    d[x + "d"] = dr.as_bf16(d[x + "_pages"], d[x + "_scales"]).cuda()
+    return by
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 5, 150])
+@pytest.mark.parametrize("top", [27, 60, 220, 232, 246])
+def test_queries_and_keys_far_from_one_that_meet_in_the_middle(aa, new, D, top):
+    """Keys at both ends of the range, queries that bring the logits back to ordinary sizes."""
+    d = dr.make_batch8(12, [new + 90, new + 300], [new, new], 4, 2, D, 16, device="cuda")
+    by = _set_scales(d, "k", top)
+    d["q"] = (d["q"].double() * 2.0 ** -by).to(torch.bfloat16)
+    lo = torch.arange(2 * new, dtype=torch.int32, device="cuda") % 40
+    _attend(aa, d, 16, 2, D, tag=str(top))
+    _attend(aa, d, 16, 2, D, tag=str(top), key_lo=lo, anchor=True)
+
+
+@pytest.mark.parametrize("new", [1, 5, 150])
+@pytest.mark.parametrize("scale", [1e-30, 1e-38, 1e-44])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -120, 1.0])
+def test_tiny_softmax_scales(aa, new, scale, size):
+    """All visible keys weigh the same; those that a mask hides weigh nothing, whatever the queries are."""
+    d = dr.make_batch8(14, [new + 130, new + 40], [new, new], 4, 2, 64, 16, device="cuda")
+    d["q"].mul_(size)
+    lo = (torch.arange(2 * new, dtype=torch.int32, device="cuda") * 5 % 37)
+    _attend(aa, d, 16, 2, 64, softmax_scale=scale)
+    _attend(aa, d, 16, 2, 64, softmax_scale=scale, key_lo=lo, anchor=True)
+
+
 @pytest.mark.parametrize("new", [1, 7, 90])
 def test_growing_logits_over_large_values(aa, new):
     """Later keys outweigh earlier ones by up to 2^60, step by step, over values of 2^100: what rows keep on the way stays in range."""
