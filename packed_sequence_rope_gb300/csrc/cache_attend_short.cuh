@@ -36,6 +36,7 @@
 #pragma once
 
 #include <cfloat>
+#include <type_traits>
 
 #include "cache_attend.cuh"
 
@@ -47,6 +48,7 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled only when the max grows by > 2^8
 
 constexpr float kWeightsUp = 7.0f;      // 8-bit pages: weights are 2^7 times what the maximum gives, at most 2^15
+constexpr float kFarLogit = 1024.0f;    // log2 units: logits and exponents below are added with an error of 2^-14
 
 constexpr int kSplitRanks = 4, kSplitTiles = 8;
 
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
       int row_lo[2], row_hi[2];  // this lane's two rows' visible keys
       uint32_t qf[HD / 16][4];
       float sl2[2] = {P.scale_log2, P.scale_log2};  // 8-bit pages: and what takes the row's power of two off again
-      bool apart = false;
+      bool careful = false;  // 8-bit pages: logits far from 0, see below
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = row0 + 8 * e, tok = row / P.group;
@@ -270,14 +272,15 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
           float rest = 1.f;
           sl2[e] *= back;
           if (sl2[e] < 0x1p-120f) {
-            rest = P.scale_log2 * 0x1p100f * back;
+            rest = fmaxf(P.scale_log2 * 0x1p100f * back, FLT_MIN);
             sl2[e] = 0x1p-100f;
           } else if (sl2[e] >= 0x1p90f) {
             rest = fminf(P.scale_log2 * 0x1p-60f * back, FLT_MAX);
             sl2[e] = 0x1p60f;
           }
           sm.m[warp][(lane >> 2) + 8 * e] = rest;
-          apart |= rest != 1.f;
+          sm.l[warp][(lane >> 2) + 8 * e] = 0.f;  // r, see below
+          careful |= rest != 1.f;
 #pragma unroll
           for (int ks = 0; ks < HD / 16; ++ks) {
             const float2 a = ptx::unpack_bf16x2(qf[ks][e]), c = ptx::unpack_bf16x2(qf[ks][e + 2]);
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
             qf[ks][e + 2] = ptx::pack_f16x2(c.x * by, c.y * by);  // 2 and 3
           }
         }
-        apart = __any_sync(0xffffffffu, apart);
+        careful = __any_sync(0xffffffffu, careful);
         __syncwarp();
       }
       const int all_lo = __reduce_max_sync(0xffffffffu, max(row_lo[0], row_lo[1]));
@@ -295,9 +298,15 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
 #pragma unroll
       for (int e = 0; e < HD / 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
 
-      for (int i = begin; i < end; ++i) {
+      // Tile i. 8-bit pages: a careful one multiplies what is left of sl2, and since next to a large
+      // logit an exponent loses bits (from 2^24 on all of them), its logits, m and lane_m are
+      // relative to a logit of the row's, r. A tile that is not gives up, before it changes anything,
+      // where it meets a logit that would need it. (In one loop that is 4 to 9 % of a call at D = 64.)
+      enum Outcome { kDone, kNeedsCare, kTimeout };
+      auto take = [&](auto with_care, int i) __attribute__((always_inline)) {
+        constexpr bool kCareful = decltype(with_care)::value;
         const int n = steps + i - begin, s = n % kStages;
-        if (!warp_wait(&sm.full[s], (n / kStages) & 1, b.err, 402)) break;
+        if (!warp_wait(&sm.full[s], (n / kStages) & 1, b.err, 402)) return kTimeout;
         const int j0 = keys.tile(i) * kTileKeys, jw = j0 + kg * kWarpKeys;  // the tile's, the warp's first key
         float sc[kWarpKeys / 8][4];
 #pragma unroll
@@ -321,13 +330,6 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
             const float s0 = scale_of(of_k & 255u), s1 = scale_of(of_k >> 8);
 #pragma unroll
             for (int x = 0; x < 4; ++x) sc[e][x] = sc[e][x] * sl2[x >> 1] * (x & 1 ? s1 : s0);
-          }
-          if (apart) {
-            const float rest[2] = {sm.m[warp][lane >> 2], sm.m[warp][(lane >> 2) + 8]};
-#pragma unroll
-            for (int e = 0; e < kWarpKeys / 8; ++e)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) sc[e][x] *= rest[x >> 1];
           }
         } else {
 #pragma unroll
@@ -401,6 +403,38 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
         uint32_t pf[kWarpKeys / 8][2];
         if constexpr (k8) {
           float mt[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};  // largest s, s + e
+          if constexpr (kCareful) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float rest = sm.m[warp][(lane >> 2) + 8 * w];
+              float* at = &sm.l[warp][(lane >> 2) + 8 * w];
+              float r = *at, top = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < kWarpKeys / 8; ++e)
+#pragma unroll
+                for (int x = 2 * w; x < 2 * w + 2; ++x) {
+                  sc[e][x] = __fmul_rn(sc[e][x], rest);  // rounded: the largest less r is to be 0
+                  top = fmaxf(top, sc[e][x]);
+                }
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              const float by = top - r;
+              // down only while the row has seen nothing
+              if (top > -INFINITY && (by > kFarLogit / 2 || (by < -kFarLogit / 2 && m[w] == -INFINITY))) {
+                m[w] -= by;
+                lane_m[w] -= by;
+                r = top;
+              }
+              __syncwarp();
+              if ((lane & 3) == 0) *at = r;
+#pragma unroll
+              for (int e = 0; e < kWarpKeys / 8; ++e) {
+                sc[e][2 * w] -= r;
+                sc[e][2 * w + 1] -= r;
+              }
+            }
+            __syncwarp();
+          }
           float sv[kWarpKeys / 8][4];
 #pragma unroll
           for (int e = 0; e < kWarpKeys / 8; ++e) {
@@ -413,18 +447,20 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
               mv[x >> 1] = fmaxf(mv[x >> 1], sv[e][x]);
             }
           }
-          bool need = false;
+          bool need = false, large = false;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             mv[w] = fmaxf(mv[w], __shfl_xor_sync(0xffffffffu, mv[w], 1));
             mv[w] = fmaxf(mv[w], __shfl_xor_sync(0xffffffffu, mv[w], 2));
             need |= mv[w] > m[w] + kRescaleThreshold || (m[w] == -INFINITY && mv[w] > -INFINITY);
+            large |= fabsf(mt[w]) > kFarLogit && mt[w] > -INFINITY;
             if (mt[w] > lane_m[w] + kRescaleThreshold || (lane_m[w] == -INFINITY && mt[w] > -INFINITY)) {
               l[w] *= lane_m[w] == -INFINITY ? 0.f : exp2f(lane_m[w] - mt[w]);
               lane_m[w] = mt[w];
             }
           }
-          if (__any_sync(0xffffffffu, need)) {
+          if (__any_sync(0xffffffffu, need || (!kCareful && large))) {
+            if (!kCareful && __any_sync(0xffffffffu, large)) return kNeedsCare;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const float mn = fmaxf(m[w], mv[w]);
@@ -520,6 +556,18 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
+        return kDone;
+      };
+      int i = begin;
+      Outcome last = kDone;
+      if (!careful)
+        for (; i < end && (last = take(std::false_type{}, i)) == kDone; ++i) {
+        }
+      if constexpr (k8) {
+        careful |= last == kNeedsCare;
+        if (careful && last != kTimeout)
+          for (; i < end && take(std::true_type{}, i) == kDone; ++i) {
+          }
       }
       if constexpr (k8) {  // the row's maximum of s for all four lanes, and for O
 #pragma unroll
@@ -528,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           l[w] *= lane_m[w] == -INFINITY ? 0.f : exp2f(lane_m[w] - mx);
           const float f = mx == -INFINITY ? 0.f : exp2f(m[w] - kWeightsUp - mx);
-          m[w] = mx;
+          m[w] = careful ? mx + sm.l[warp][(lane >> 2) + 8 * w] : mx;
 #pragma unroll
           for (int e = 0; e < HD / 8; ++e) {
             o[e][2 * w] *= f;

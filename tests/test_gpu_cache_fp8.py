@@ -385,6 +385,102 @@ def test_tiny_softmax_scales(aa, new, scale, size):
     _attend(aa, d, 16, 2, 64, softmax_scale=scale, key_lo=lo, anchor=True)
 
 
+@pytest.mark.parametrize("new", [1, 5])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_keys_under_ordinary_queries(aa, new, sign):
+    """Logits of 2^100 and more that fp32 holds, of one sign: the largest takes all of the weight."""
+    D = 128
+    d = dr.make_batch8(13, [new + 150], [new], 4, 2, D, 64, device="cuda")
+    _set_scales(d, "k", 232)  # 2^105
+    d["q"].fill_(1.0)
+    codes = d["k_pages"].view(torch.uint8)
+    codes.copy_(codes & 127 if sign > 0 else codes | 128)
+    d["kd"] = dr.as_bf16(d["k_pages"], d["k_scales"]).cuda()
+    o, lse = _attend(aa, d, 64, 2, D)
+    assert torch.isfinite(o.float()).all() and (lse * sign > 2.0 ** 100).all()
+    # a row's heads of a kv head see the same keys with the same queries; its result is one key's value
+    p = torch.arange(150, new + 150)
+    for g in range(2):
+        k, v = (ref.keys_of(d[x].cpu(), d["table"][0].cpu(), new + 150, 0, g) for x in ("kd", "vd"))
+        s = k.sum(-1)
+        for i in range(new):
+            best = s[:p[i] + 1].argmax()
+            second = s[:p[i] + 1].clone()
+            second[best] = -math.inf
+            if s[best] - second.max() > 2.0 ** -16 * s.abs().max():
+                assert ((o[i, 2 * g].cpu().double() - v[best]).abs() <= 2.0 ** -8 * v[best].abs()).all()
+
+
+def _logits(kind, n):
+    """A logit per key that 8 bits hold, and the keys that may have weight; between the others and these lie more than 2^9."""
+    j = torch.arange(n)
+    near = ((j * 37 % 25).double() - 12) / 4
+    if kind == "behind":  # far below the ones that come later
+        s, of = torch.where(j < n - n // 3, -2.0 ** 30, near), j >= n - n // 3
+    elif kind == "ahead":
+        s, of = torch.where(j < n // 3, near, -2.0 ** (10 + j % 90)), j < n // 3
+    elif kind == "low":  # all of them low, one the least
+        s = -2.0 ** 24 * torch.exp2((j * 7 % 60 + 1).double())
+        s[n // 2] = -2.0 ** 24
+        of = j == n // 2
+    elif kind == "growing":
+        s, of = torch.exp2(10 + (j // 4).double() * 100 // n), j == n - 1
+        s[-1] = 2.0 ** 112
+    else:  # one far above, early
+        s, of = near.clone(), j == 5
+        s[5] = 2.0 ** float(kind)
+    return s, of
+
+
+def check_far_logits(aa, kind, new, D, fp8, n=700):
+    """Queries and keys whose products are exact (one code times a power of two per key), over values whose scales lie far
+    apart: what has weight is known, and the result is off by the roundings of the weights and its own alone."""
+    Hq, Hkv, ps = 4, 2, 64
+    d = dr.make_batch8(15, [n], [new], Hq, Hkv, D, ps, device="cuda")
+    s, of = _logits(kind, n)
+    e = d["v_scales"].view(torch.uint8)
+    e.copy_(torch.randint(100, 150, e.shape, generator=torch.Generator().manual_seed(3), dtype=torch.uint8))
+    d["vd"] = dr.as_bf16(d["v_pages"], d["v_scales"]).cuda()
+    held, exp = dr.quantise(s[:, None])
+    assert torch.equal(held[:, 0], s)
+    codes = (held[:, 0] * torch.exp2(-exp.double())).float().to(torch.float8_e4m3fn).cuda()
+    j = torch.arange(n, device="cuda")
+    page = d["table"][0, j // ps].long()
+    d["k_pages"].view(torch.uint8)[0, page, :, j % ps] = codes.view(torch.uint8)[:, None, None]
+    d["k_scales"].view(torch.uint8)[0, page, :, j % ps] = (exp + 127).to(torch.uint8).cuda()[:, None]
+    d["kd"] = dr.as_bf16(d["k_pages"], d["k_scales"]).cuda()
+    d["q"].fill_(1.0)
+    pool = {x: d[x] for x in ("k_pages", "v_pages", "k_scales", "v_scales")} if fp8 else dict(k_pages=d["kd"], v_pages=d["vd"])
+    hi = torch.arange(n - new, n) if kind not in ("growing", "behind") else torch.full((new,), n - 1)
+    tree = torch.full((new, -(-new // 64)), -1, dtype=torch.int64, device="cuda") if kind in ("growing", "behind") else None
+    with aa.PagedCache(d["P"], ps, Hkv, D, **pool) as c:
+        o, lse = c.attend(d["q"], d["table"], d["cu"], d["kv"], new, softmax_scale=1.0 / D, return_lse=True, tree=tree)
+        c.check_device_error()
+    o, lse = o.double().cpu(), lse.double().cpu()
+    for g in range(Hkv):
+        v = ref.keys_of(d["vd"].cpu(), d["table"][0].cpu(), n, 0, g)
+        for i in range(new):
+            seen = of & (j.cpu() <= hi[i])
+            top = s[seen].max()
+            w = torch.where(seen, (s - top).exp(), 0.0)
+            p = w / w.sum()
+            want, bound = p @ v, (2.0 ** -8 + 2.0 ** -14) * (p @ v.abs())
+            for h in range(g * Hq // Hkv, (g + 1) * Hq // Hkv):
+                assert ((o[i, h] - want).abs() <= bound + 2.0 ** -8 * want.abs()).all(), (kind, i, h)
+                r = float(top + w.sum().log())
+                assert abs(float(lse[h, i]) - r) <= 2.0 ** -14 + 2.0 ** -21 * abs(r)
+
+
+FAR = ["behind", "ahead", "low", "growing", "11", "20", "40", "100"]
+
+
+@pytest.mark.parametrize("kind", FAR)
+@pytest.mark.parametrize("new", [1, 5, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_logits_of_any_size(aa, kind, new, D):
+    check_far_logits(aa, kind, new, D, True)
+
+
 @pytest.mark.parametrize("new", [1, 7, 90])
 def test_growing_logits_over_large_values(aa, new):
     """Later keys outweigh earlier ones by up to 2^60, step by step, over values of 2^100: what rows keep on the way stays in range."""
