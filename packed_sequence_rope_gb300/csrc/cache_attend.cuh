@@ -8,6 +8,13 @@ namespace aa {
 
 constexpr uint64_t kAttendWaitNs = 2000000000ull;  // limit of every wait on a copy or a product
 
+// A row's weights are 2^(sl2 * x - m), x its dot products, sl2 the softmax scale in log2 units: the
+// product is exact in the fused operation, m is the rounded maximum. What its rounding is off by
+// cancels in the weights and their sum, unless that is itself a large exponent: above this
+// magnitude, in log2 units, more than 1. Over 8-bit pages such rows take a dot product off theirs
+// first (1 % of a call, at 64 channels 2 %).
+constexpr float kFarMax = 16777216.0f;  // 2^24
+
 struct AttendParams {
   BatchParams batch;
   const __nv_bfloat16* q;

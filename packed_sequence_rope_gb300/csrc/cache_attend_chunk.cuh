@@ -835,6 +835,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int j0 = keys.tile(w.first) * kKeys + half * 64;  // this warp's first key
       int next_j0 = keys.tile(w.first + 1) * kKeys + half * 64;
       float m = -INFINITY, l = 0.f;
+      // Once a row of the warp has had a maximum above kFarMax, dot products and maxima are relative to
+      // one of the row's. It stays out of the registers, of which the loop has none to spare.
+      constexpr bool kFar = kFrom != kFromPages;
+      bool far = false;
+      volatile float from;
+      if constexpr (kFar) from = 0.f;
       bool ok = true;
       for (int i = 0; i < take; ++i, j0 = next_j0, next_j0 += kKeys) {
         const int buf = k8 ? i & 1 : t;  // of S
@@ -849,18 +855,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph_s ^= 1;
         ptx::tc_fence_after();
         const uint32_t t_s = k8 ? t_s0 + 128 * buf : t_s0;
+        float sv[64];
         // The row's maximum over both column halves, and what it changes. Also the
         // point where both warps have read their columns of S: P may overwrite them.
         auto agree = [&](float mt) {
           auto& both = k8 ? pairs[4 * (exchanges++ & 1)] : pair;
           both[half][lane] = mt;
           if (!ptx::bar_and(pair_bar, 64, true)) return false;
-          mt = fmaxf(both[0][lane], both[1][lane]) * sl2;
+          const float top = fmaxf(both[0][lane], both[1][lane]);
+          mt = top * sl2;
           // TMEM access is warp-collective, so a rescale of O is decided per warp (alike
           // for both), and by rows that hold a token alone: what lies in the others
           // (the next sequence's queries, old shared memory) must not change a bit
-          const bool need = row_valid && ((mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY));
+          const bool need = (kFar && far) || (row_valid && ((mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY)));
           if (__any_sync(0xffffffffu, need)) {
+            if constexpr (kFar) {
+              if (far || __any_sync(0xffffffffu, row_valid && fabsf(mt) > kFarMax && mt > -INFINITY)) {
+                float r = from;
+                const float by = (top - r) * sl2;
+                // down only while the row has seen nothing
+                if (row_valid && top > -INFINITY && (by > kFarMax / 2 || (by < -kFarMax / 2 && m == -INFINITY))) {
+                  m -= by;
+                  r = top;
+                }
+                from = r;
+                mt = (top - r) * sl2;
+#pragma unroll
+                for (int e = 0; e < 64; ++e) sv[e] -= r;
+                far = true;
+              }
+            }
             const float mn = fmaxf(m, mt);
             const float f = (m == -INFINITY) ? 0.f : exp2f(m - mn);
             l *= f;
@@ -885,7 +909,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         const uint32_t t_p = t_s + half * 32;
-        float sv[64];
 #pragma unroll
         for (int c = 0; c < 2; ++c) ptx::tmem_ld32(t_s + half * 64 + c * 32, sv + c * 32);
         // columns that every row of the warp sees skip the per-element mask
@@ -948,6 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // piece's first PV of this tile (overwriting O) waits for.
       ptx::tc_fence_after();
       ++nq;
+      if (kFar && far) m += from * sl2;
       if (w.whole) {
         const int head = w.g * P.group + r - in_tile * P.group;
         const int64_t row = w.q_row + t * C.tile_tokens + in_tile;

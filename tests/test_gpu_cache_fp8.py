@@ -385,7 +385,7 @@ def test_tiny_softmax_scales(aa, new, scale, size):
     _attend(aa, d, 16, 2, 64, softmax_scale=scale, key_lo=lo, anchor=True)
 
 
-@pytest.mark.parametrize("new", [1, 5])
+@pytest.mark.parametrize("new", [1, 5, 40, 150])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_large_keys_under_ordinary_queries(aa, new, sign):
     """Logits of 2^100 and more that fp32 holds, of one sign: the largest takes all of the weight."""
@@ -479,6 +479,14 @@ FAR = ["behind", "ahead", "low", "growing", "11", "20", "40", "100"]
 @pytest.mark.parametrize("D", [64, 128])
 def test_logits_of_any_size(aa, kind, new, D):
     check_far_logits(aa, kind, new, D, True)
+
+
+@pytest.mark.parametrize("kind", FAR)
+@pytest.mark.parametrize("new", [40, 150])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [700, 3000])
+def test_logits_of_any_size_in_chunks(aa, kind, new, D, n):
+    check_far_logits(aa, kind, new, D, True, n)
 
 
 @pytest.mark.parametrize("new", [1, 7, 90])
