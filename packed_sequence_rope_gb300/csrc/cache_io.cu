@@ -38,19 +38,22 @@ struct AppendParams {
   int Hq, page_shift;
 };
 
-// Sixteen values of a row in fp32, eight from each of the places where Pairs8 has them.
-template <int HD, int L>
+// Sixteen values of a row in fp32, eight from each of the places where Pairs8 has them; with
+// kHalved half of them, which fp32 also holds where a rotation makes bf16's largest longer by
+// sqrt 2. (Of values, which are not rotated, too: keys alone cost a register more, 1.7 %; both 0.4.)
+template <int HD, int L, bool kHalved>
 struct Values16 {
+  static constexpr float kBy = kHalved ? 0.5f : 1.f;
   float a[8], b[8];
   __device__ __forceinline__ explicit Values16(const Pairs8<HD, L>& x) {
     const uint32_t u[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 va = ptx::unpack_bf16x2(u[e]), vb = ptx::unpack_bf16x2(u[4 + e]);
-      a[2 * e] = va.x;
-      a[2 * e + 1] = va.y;
-      b[2 * e] = vb.x;
-      b[2 * e + 1] = vb.y;
+      a[2 * e] = kBy * va.x;
+      a[2 * e + 1] = kBy * va.y;
+      b[2 * e] = kBy * vb.x;
+      b[2 * e + 1] = kBy * vb.y;
     }
   }
   __device__ __forceinline__ void turn(const float2* cs) {
@@ -75,8 +78,8 @@ struct Values16 {
 #pragma unroll
     for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(lanes, top, d));
     // 448 = 1.75 * 2^8
-    const int e = min(max((int)(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 119);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    const int e = min(max((int)(top >> 23) - 135 + kHalved + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 119);
+    const float down = __uint_as_float((uint32_t)(127 - e + kHalved) << 23);
     uint32_t w[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, k8 ? 4 : 0) cache_append_kernel(cons
     if constexpr (k8) {
       if (g >= 0) {
         if (at < 0) continue;  // all lanes of a row
-        Values16<HD, L == 2 ? 0 : L> y(x);
+        Values16<HD, L == 2 ? 0 : L, L != 2> y(x);
         if constexpr (L != 2)
           if (g < b.Hkv) y.turn(mine);
         const int64_t row = at + ((int64_t)(g < b.Hkv ? g : g - b.Hkv) << P.page_shift);

@@ -145,6 +145,32 @@ def test_append_of_rows_at_the_borders(aa):
         assert torch.equal(got.cpu().double()[fine], held[fine]) and got.cpu()[~fine].isnan().all()
 
 
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_of_rotated_keys_that_fp32_does_not_hold(aa, half, D):
+    """Pairs of bf16's largest values are longer than fp32's largest: what passes 448 * 2^119 becomes that, and no row is NaN.
+    Bound: the angle's 2^-19 of the pair's length, then half a code's step."""
+    n = 40
+    top = 3.3895e38
+    k = torch.zeros(n, 1, D, dtype=torch.float64)
+    k[:, 0, :] = top * torch.where(torch.arange(n * D).view(n, D) % 7 < 3, 1.0, -1.0)
+    k[::3, 0, 2:] = 1.0e30
+    k = k.to(torch.bfloat16).cuda()
+    rope = aa.RopeAxes(D, sections=(D // 2,), base=1e4, layout=aa.ROPE_HALF if half else aa.ROPE_ADJACENT)
+    pos = (torch.arange(n, dtype=torch.int32) * 3).cuda()
+    table, cu, kv = torch.tensor([[2, 0, 1]], dtype=torch.int32).cuda(), *(torch.tensor(t, dtype=torch.int32).cuda() for t in ([0, n], [n]))
+    with aa.PagedCache(3, 16, 1, D, dtype=torch.float8_e4m3fn, device="cuda") as c:
+        c.append(k, k, table, cu, kv, rope=rope, pos=pos)
+        got, _ = c.read(table, cu, kv, n)
+        c.check_device_error()
+    want = ref.turn(k, pos[None], rope.axis_of_pair, [1e4 ** (-2.0 * i / D) for i in range(D // 2)], half)
+    off = ref.turn_bound(want, k, half) - want.abs() * 2.0 ** -8
+    assert (want.abs() > 3.5e38).any()
+    held = want.clamp(-448 * 2.0 ** 119, 448 * 2.0 ** 119)
+    err = (got.cpu().double() - held).abs()
+    assert (err <= torch.maximum(held.abs() * 2.0 ** -4, torch.tensor(2.0 ** 109, dtype=torch.float64)) + off * 1.0625).all()
+
+
 def test_append_of_slices_many_sequences_and_steps(aa):
     """Token by token, from slices of a joint projection, what one call writes."""
     B, ps, Hkv, D = 150, 32, 3, 128
