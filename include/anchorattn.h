@@ -422,9 +422,9 @@ aa_status aa_rope_axes_apply(const aa_rope_axes* rope, const int32_t* pos, int32
  * the (rotated) fp32 values once, to the nearest, ties to even: within 2^-4 of the value
  * or 2^-10 of the power, whichever is more (magnitudes above 448 * 2^119, bf16's
  * largest 14 %, become that). A row with a value that is not finite gets byte 255 and
- * is NaN as a whole. Pages that the caller fills have bytes in [1, 254], or 255 for
- * NaN, and no NaN codes (what 0x7f and 0xff give is not defined). All other calls are
- * the same for both kinds.
+ * is NaN as a whole. Pages that the caller fills have bytes in [3, 246], the range in which
+ * bf16 holds every code times the power of two, or 255 for NaN, and no NaN codes (what
+ * other bytes, 0x7f and 0xff give is not defined). All other calls are the same for both kinds.
  *
  * Two halves:
  *  - Bookkeeping on the host (aa_cache_resize, _fork, _compact, _tables,

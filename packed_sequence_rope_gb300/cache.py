@@ -61,7 +61,8 @@ def _i32p(a):
 class PagedCache:
     """The pool of pages, [num_layers, num_pages, Hkv, page_size, D] for keys and for values, and which sequence holds
     which page. dtype: torch.bfloat16, or torch.float8_e4m3fn for 8-bit pages with k_scales / v_scales, float8_e8m0fnu
-    [num_layers, num_pages, Hkv, page_size] (a token's power of two: page value * scale is what it stands for). k_pages /
+    [num_layers, num_pages, Hkv, page_size] (a token's power of two, 2^-124 to 2^119 or NaN: page value * scale is what it
+    stands for). k_pages /
     v_pages (and the scales): tensors to use as the pool, whose type they give (else allocated, uncleared, on `device`).
     max_seqs = 0: no bookkeeping, the caller has page tables of its own."""
 

@@ -32,9 +32,10 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* __restrict__ cu_q, i
 
 // Four e4m3 numbers b0 .. b3 as bf16 pairs (b0, b2) and (b1, b3), exactly: sign, exponent
 // and significand moved to their places in bf16 mean 2^-120 times the number (a
-// subnormal one lands among bf16's subnormals), which one product undoes. NaN codes
-// become 480. (There is a conversion to f16, but none to bf16.)
-__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t x, uint32_t up = 0x7b807b80u) {  // up: 2^120 twice
+// subnormal one lands among bf16's subnormals); a product with `up`, a power of two, twice,
+// makes that `up` * 2^-120 times. NaN codes become 480 times. (There is a conversion to f16,
+// but none to bf16.)
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t x, uint32_t up) {
   const uint32_t even = ((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u);
   const uint32_t odd = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
   uint2 r;

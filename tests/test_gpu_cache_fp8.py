@@ -65,6 +65,23 @@ def test_read_gives_every_code_at_every_scale(aa, D):
         assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
 
 
+@pytest.mark.parametrize("byte", [3, 4, 9, 246, 255])
+def test_read_at_the_ends_of_the_range(aa, byte):
+    codes = torch.tensor([x for x in range(256) if x & 127 != 127] + [0, 0], dtype=torch.uint8).view(4, 64)
+    pages = torch.zeros(1, 1, 1, 16, 64, dtype=torch.uint8)
+    pages[0, 0, 0, :4] = codes
+    scales = torch.full((1, 1, 1, 16), byte, dtype=torch.uint8)
+    k, s = pages.view(torch.float8_e4m3fn).cuda(), scales.view(torch.float8_e8m0fnu).cuda()
+    table, cu, kv = (torch.tensor(t, dtype=torch.int32).cuda() for t in ([[0]], [0, 4], [4]))
+    with aa.PagedCache(1, 16, 1, 64, k_pages=k, v_pages=k.clone(), k_scales=s, v_scales=s.clone()) as c:
+        got = c.read(table, cu, kv, 4)
+    want = dr.values(pages, scales)[0, 0, 0, :4]
+    assert torch.equal(want.to(torch.bfloat16).double().nan_to_num(9.0), want.nan_to_num(9.0))  # bf16 holds them
+    for g in got:
+        g = g.cpu().double().view(4, 64)
+        assert torch.equal(g.isnan(), want.isnan()) and torch.equal(g.nan_to_num(9.0), want.nan_to_num(9.0))
+
+
 @pytest.mark.parametrize("ps", [16, 128])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("half", [False, True, None])
@@ -397,6 +414,26 @@ def test_queries_and_keys_far_from_one_that_meet_in_the_middle(aa, new, D, top):
     lo = torch.arange(2 * new, dtype=torch.int32, device="cuda") % 40
     _attend(aa, d, 16, 2, D, tag=str(top))
     _attend(aa, d, 16, 2, D, tag=str(top), key_lo=lo, anchor=True)
+
+
+@pytest.mark.parametrize("x", ["k", "v"])
+@pytest.mark.parametrize("new", [1, 5, 40, 150])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_smallest_scales(aa, x, new, D):
+    """Scales from 2^-124 on, where bf16 still holds every code: keys under queries that meet them, and values."""
+    d = dr.make_batch8(16, [new + 90, new + 300], [new, new], 4, 2, D, 16, device="cuda")
+    e = d[x + "_scales"].view(torch.uint8)
+    by = 3 - int(e.min())
+    e.copy_((e.int() + by).to(torch.uint8))
+    d[x + "d"] = dr.as_bf16(d[x + "_pages"], d[x + "_scales"]).cuda()
+    if x == "k":
+        d["q"] = (d["q"].double() * 2.0 ** -by).to(torch.bfloat16)
+    with _cache(aa, d, 16, 2, D) as c:
+        o, lse = c.attend(d["q"], d["table"], d["cu"], d["kv"], new, return_lse=True)
+        c.check_device_error()
+    ro, rl, ob, lb = ref.attend(d["q"], d["kd"], d["vd"], d["table"], d["cu"], d["kv"])
+    # results below 2^-126 lie 2^-133 apart: rounding one is off by up to half of that, whatever its size
+    ref.check_attend(o, lse, (ro, rl, ob + 2.0 ** -134, lb))
 
 
 @pytest.mark.parametrize("new", [1, 5, 150])
