@@ -558,13 +558,18 @@ aa_status aa_cache_read(aa_cache_t cache, const aa_cache_batch* batch, void* k, 
  * A row that sees no key, or whose logits are all -inf, gives O = 0 and LSE = -inf.
  * With 8-bit pages the result is that of the values that they stand for, and a key may
  * take 2^-32 of the row's largest weight times value out of it.
+ * Sums are fp32: dot products that pass its range are infinite, and so may a result be whose
+ * |v| times the keys that the row sees passes 2^119. With 16-bit pages logits are below 2^30.
  * Keys that no new token of their sequence sees do not reach the result, whatever
  * they hold (NaN, infinities); what a row sees makes it NaN as the formula does, and a value that
  * is not finite may reach the other rows of its sequence in the call too.
  *  - q [T, q_heads, D] bf16, ROTATED (q_stride elements from token to token);
  *    q_heads % Hkv == 0, at most 64 query heads per kv head.
- *  - max_q: the most new tokens of a sequence. It chooses the kernel; a
- *    sequence with more is still computed, only slower.
+ *  - max_q: the most new tokens of a sequence. It chooses the kernel, for all
+ *    sequences of the call; a sequence with more is still computed, only slower.
+ *    One chunk among many single tokens takes these along: two calls are faster
+ *    where the contexts are long, most of all over 8-bit pages, where above 256
+ *    rows every sequence's keys are first copied to 16 bits.
  *  - key_lo: device int32 [T] or NULL (0 for every row).
  *  - softmax_scale <= 0 selects 1/sqrt(D).
  *  - o [T, q_heads, D] bf16; lse [q_heads, T] fp32 or NULL. They and the workspace's
@@ -582,8 +587,8 @@ aa_status aa_cache_attend(aa_cache_t cache, const aa_cache_batch* batch, const v
  * aa_cache_attend with other visible keys: new token i of sequence b sees the cached
  * j in [max(key_lo, 0), base), j = 0 if anchor != 0 and base > 0, and new token c of
  * its sequence if bit c % 64 of word c / 64 of its row of `tree` is set (device
- * uint64 [T, tree_words], 1 <= tree_words <= 2^14; bits at n_b and above are not looked at, tokens past the
- * masks' width are not seen). Any mask will do, also one where tokens see later ones.
+ * uint64 [T, tree_words], 1 <= tree_words <= 2^14; bits at n_b and above are not looked at, tokens at 64 *
+ * tree_words and above are not seen, by themselves neither). Any mask will do, also one where tokens see later ones.
  * Where base < 0 the tokens without a position see nothing. The workspace is
  * aa_cache_attend's. */
 aa_status aa_cache_attend_tree(aa_cache_t cache, const aa_cache_batch* batch, const void* q, int64_t q_stride,
@@ -594,8 +599,9 @@ aa_status aa_cache_attend_tree(aa_cache_t cache, const aa_cache_batch* batch, co
 /* Masks and positions of drafted trees: parents (device int32 [T]) gives each new
  * token's parent as its index among its sequence's new tokens, smaller than its own,
  * or -1 for one that follows the cached tokens. mask (uint64 [T, tree_words]): the
- * token's ancestors and itself; pos (int32 [T]): kv_len - n_b + the number of its
- * ancestors, the position that it is rotated at. A parent out of range counts as -1
+ * token's ancestors and itself, as far as they lie below 64 * tree_words (which has to
+ * cover the longest sequence's new tokens; no error word is set); pos (int32 [T]): kv_len - n_b + the
+ * number of its ancestors, the position that it is rotated at. A parent out of range counts as -1
  * and sets the error word. Rows outside [cu_q[0], cu_q[num_seqs]) are left as they were. */
 aa_status aa_cache_tree_masks(aa_cache_t cache, const int32_t* parents, const int32_t* cu_q, const int32_t* kv_len,
                               int32_t num_seqs, int32_t total_tokens, int32_t tree_words, uint64_t* mask, int32_t* pos,
@@ -614,12 +620,13 @@ aa_status aa_cache_accept(aa_cache_t cache, const aa_cache_batch* batch, const i
 
 /* Bytes of device scratch aa_cache_attend needs for a batch of these sizes
  * (partial results of keys that are split among CTAs). Chunks: 20 MB at D = 64, 40 at
- * 128, and 32 bytes per sequence and per 256 rows of a kv head more. Few new tokens
- * over long contexts: the results of up to 76 splits, 4 * D + 8 bytes per row and split.
- * 256 bytes where nothing is split. Chunks over 8-bit pages whose sequences have more
- * than 256 rows (max_q times the query heads of a kv head): 16-bit copies of a few
- * sequences' keys and values more, 4 * D * Hkv bytes per position of their tables, up to 1 GiB. A smaller batch may need more. 0 for invalid
- * sizes. */
+ * 128, and 32 bytes per sequence and per 256 rows of a kv head more (over 8-bit pages
+ * with up to 256 rows of a sequence: per 128). Few new tokens over long contexts: the
+ * results of up to 76 splits, 4 * D + 8 bytes per row and split. 256 bytes where nothing
+ * is split. Chunks over 8-bit pages whose sequences have more than 256 rows (max_q times
+ * the query heads of a kv head): 16-bit copies of a few sequences' keys and values more,
+ * 4 * D * Hkv bytes per position of their tables, up to 1 GiB; a smaller max_q asks for
+ * less, at the price of time. A smaller batch may need more. 0 for invalid sizes. */
 size_t aa_cache_attend_workspace_bytes(aa_cache_t cache, int32_t num_seqs, int32_t total_tokens, int32_t max_q,
                                        int32_t table_width, int32_t q_heads);
 

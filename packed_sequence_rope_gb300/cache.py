@@ -62,9 +62,8 @@ class PagedCache:
     """The pool of pages, [num_layers, num_pages, Hkv, page_size, D] for keys and for values, and which sequence holds
     which page. dtype: torch.bfloat16, or torch.float8_e4m3fn for 8-bit pages with k_scales / v_scales, float8_e8m0fnu
     [num_layers, num_pages, Hkv, page_size] (a token's power of two, 2^-124 to 2^119 or NaN: page value * scale is what it
-    stands for). k_pages /
-    v_pages (and the scales): tensors to use as the pool, whose type they give (else allocated, uncleared, on `device`).
-    max_seqs = 0: no bookkeeping, the caller has page tables of its own."""
+    stands for). k_pages / v_pages (and the scales): tensors to use as the pool, whose type they give (else allocated,
+    uncleared, on `device`). max_seqs = 0: no bookkeeping, the caller has page tables of its own."""
 
     def __init__(self, num_pages, page_size, num_kv_heads, head_dim, num_layers=1, max_seqs=0, k_pages=None, v_pages=None,
                  device=None, host_only=False, dtype=None, k_scales=None, v_scales=None):
@@ -224,7 +223,9 @@ class PagedCache:
 
     def tree_masks(self, parents, cu_q, kv_len, max_q, out_mask=None, out_pos=None, stream=None):
         """Masks int64 [T, ceil(max_q / 64)] and positions int32 [T] of drafted trees, for attend's tree and append's pos.
-        parents: int32 [T], each new token's parent among its sequence's new tokens before it, -1: the cached tokens."""
+        parents: int32 [T], each new token's parent among its sequence's new tokens before it, -1: the cached tokens.
+        Unlike attend's, this max_q is no hint: tokens of a sequence at and behind the masks' width are in no mask, their
+        own included."""
         r = native().cache_tree_masks(self._device_handle(), self._dev, parents, cu_q, kv_len, max_q, out_mask, out_pos, stream)
         if type(r) is int:
             _check(r)
