@@ -51,8 +51,8 @@ static bool takes_short(const aa_cache_s* c, int num_seqs, int max_q, int table_
 // With D = 64: 64 rows of 42 sequences 40.9 / 31.0 / 36.8, 134 / 89.2 / 126 and 962 / 358 /
 // 820, 256 rows 138 / 48.7 / 59.6, 520 / 169 / 131 and 3698 / 697 / 780, 512 rows 248 /
 // 84.5 / 60.6, 1035 / 297 / 189 and 7362 / 1379 / 1183.
-// At 256 rows neither leads everywhere: over 2048 keys the copies are faster (4 %, at D = 64
-// 22 %), over the others slower, and they ask for a workspace. The rule looks at max_q alone, so a
+// At 256 rows neither leads everywhere: for 42 sequences over 2048 keys the copies are faster (4 %,
+// at D = 64 22 %), in most others slower, and they ask for a workspace. The rule looks at max_q alone, so a
 // chunk takes single tokens beside it along: 63 of these over 16K keys with one of 512 tokens 2008
 // us, as two calls 501 (16-bit pages 889 and 710).
 enum Path { kShort, kChunk, kShortCodes, kChunkCodes, kWide };

@@ -654,6 +654,22 @@ def test_buffers_of_unread_pages_are_used_again(aa, new, max_q, ps, D):
                 assert all(torch.equal(a, b) for a, b in zip(again, first))
 
 
+@pytest.mark.parametrize("chunk,width", [(300, 1030), (60, 1030), (300, 40)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_chunk_among_single_tokens(aa, chunk, width, D):
+    """One prompt chunk beside single tokens, sequences without any and rows that see nothing: where tables are wide, in several slices."""
+    new = [1, 1, 0, chunk, 1, 1, 1, 7, 1, 1, 0, 1]
+    kv = [1, 700, 50, chunk + 1000, 64, 65, 1, 300, 0, 2000, 0, 129]
+    ps, Hq, Hkv = 64, 16 if D == 128 else 32, 8
+    d = dr.make_batch8(chunk + width, kv, new, Hq, Hkv, D, ps, device="cuda")
+    d["table"] = torch.cat([d["table"], torch.full((len(kv), width - d["table"].shape[1]), -1, dtype=torch.int32, device="cuda")], 1)
+    _attend(aa, d, ps, Hkv, D)
+    lo = torch.tensor([max(0, k - n - 100) for k, n in zip(kv, new) for _ in range(n)], dtype=torch.int32, device="cuda")
+    lo[5::11] = 2 ** 30
+    for anchor in (False, True):
+        _attend(aa, d, ps, Hkv, D, key_lo=lo, anchor=anchor)
+
+
 # ------------------------------------------------------------------ pages and bookkeeping
 @pytest.mark.parametrize("n,ps,Hkv,D,L", [(1, 16, 1, 64, 1), (70, 16, 3, 64, 2), (9, 128, 8, 128, 3)])
 def test_copy_pages(aa, n, ps, Hkv, D, L):

@@ -179,6 +179,19 @@ def test_trees_over_long_contexts(aa, fp8, new, kv, Hq, Hkv, D):
         _attend(aa, d, 64, Hkv, D, tree, key_lo=lo, anchor=True)
 
 
+@pytest.mark.parametrize("width", [1030, 4700])
+def test_trees_over_wide_tables(aa, width):
+    """Ragged trees over 8-bit pages for which 16-bit copies are made of some sequences at a time, or of none."""
+    g = torch.Generator().manual_seed(width)
+    new, kv, ps, Hq, Hkv, D = [70, 0, 1, 90, 66, 33, 80], [300, 50, 900, 90, 200, 33, 700], 64, 32, 8, 128
+    d = _batch(True, width, kv, new, Hq, Hkv, D, ps, device="cuda")
+    d["table"] = torch.cat([d["table"], torch.full((len(kv), width - d["table"].shape[1]), -1, dtype=torch.int32, device="cuda")], 1)
+    seen, _ = dr.masks_of(dr.random_tree(g, new).tolist(), d["cu"].tolist(), 0)
+    lo = torch.randint(0, 300, (sum(new),), generator=g, dtype=torch.int32).cuda()
+    _attend(aa, d, ps, Hkv, D, dr.pack(seen, 2).cuda())
+    _attend(aa, d, ps, Hkv, D, dr.pack(seen, 2).cuda(), key_lo=lo, anchor=True)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("new", [5, 24, 130])
 @pytest.mark.parametrize("ps", [16, 128])
