@@ -413,7 +413,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto cache = as_handle<aa_cache_t>(a[0]);
   const at::Device dev(at::kCUDA, (c10::DeviceIndex)as_int(a[1]));
   const int64_t H = as_int(a[2]), D = as_int(a[3]), T = as_i32(a[7], "total_tokens");
-  TORCH_CHECK_VALUE(T >= 0, "total_tokens must be >= 0");
+  TORCH_CHECK_VALUE(T >= 0 && T < 1 << 30, "total_tokens must be in [0, 2^30)");
   const aa_cache_batch batch = batch_of(a[4], a[5], a[6], T, as_i32(a[8], "layer"), dev);
   const Tensor *out_k = given(a[9], "out_k"), *out_v = given(a[10], "out_v");
   const OnStream on(a[11], dev);
@@ -447,7 +447,8 @@ PyObject* cache_tree_masks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& cu = ints(a[3], "cu_q", B + 1, dev);
   TORCH_CHECK_VALUE(B <= INT32_MAX && T <= INT32_MAX, "the batch is too large");
   const int32_t max_q = as_i32(a[5], "max_q");
-  TORCH_CHECK_VALUE(max_q >= 0, "max_q must be >= 0");
+  // before the masks are allocated: tree_words is at most 2^14
+  TORCH_CHECK_VALUE(max_q >= 0 && max_q <= 1 << 20, "max_q must be in [0, 2^20]");
   const int64_t words = std::max<int64_t>(1, ((int64_t)max_q + 63) / 64);
   const Tensor *out_mask = given(a[6], "out_mask"), *out_pos = given(a[7], "out_pos");
   const OnStream on(a[8], dev);

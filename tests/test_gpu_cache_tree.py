@@ -286,6 +286,20 @@ def test_attend_refusals(aa):
         c.check_device_error()
 
 
+def test_sizes_out_of_range_are_refused_before_results_are_allocated(aa):
+    d = _batch(False, 1, [30], [2], 4, 2, 64, 16, device="cuda")
+    torch.cuda.synchronize()
+    with _cache(aa, d, 16, 2, 64) as c:
+        before = torch.cuda.max_memory_allocated()
+        for max_q in ((1 << 20) + 1, 2 ** 31 - 1):
+            with pytest.raises(ValueError):
+                c.tree_masks(_i32([-1] * 5000), _i32([0, 5000]), _i32([5000]), max_q)
+        for T in (1 << 30, 2 ** 31 - 1):
+            with pytest.raises(ValueError):
+                c.read(d["table"], d["cu"], d["kv"], T)
+        assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
 # ------------------------------------------------------------------ accepting
 PATHS = [[[0], [3], []], [[0, 1, 2], [0, 2, 3], [9]], [[5, 6, 7, 39], [1, 2, 3, 4], list(range(20))], [[], [], []],
          [list(range(1, 40)), list(range(25)), [0, 24]]]
