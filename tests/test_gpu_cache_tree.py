@@ -351,6 +351,63 @@ def test_accept_moves_nothing_along_a_bad_path(aa, bad):
             assert torch.equal(d["k_pages"], now)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [3, 60])
+def test_a_captured_step_on_several_streams(aa, fp8, new):
+    """The calls behind a copy, a clear and another stream's work, in one graph: what they read is there."""
+    ps, Hq, Hkv, D = 32, 8, 2, 128
+    kv = [new + 300, new + 7]
+    d = _batch(fp8, 4, kv, [new, new], Hq, Hkv, D, ps, layers=2, device="cuda")
+    g = torch.Generator().manual_seed(2)
+    parents = dr.random_tree(g, [new, new]).cuda()
+    path = _i32([[1, 2], [2, -1]])
+    with _cache(aa, d, ps, Hkv, D) as c:
+        work = [c.alloc_workspace(2, d["T"], new, d["table"].shape[1], Hq) for _ in range(2)]
+        q, out, here = torch.empty_like(d["q"]), torch.empty_like(d["q"]), torch.zeros_like(parents)
+        plain = torch.empty_like(d["q"])
+        k, v = torch.empty_like(d["k"]), torch.empty_like(d["v"])
+        mask, pos = c.tree_masks(parents, d["cu"], d["kv"], new)
+        rk, rv = c.read(d["table"], d["cu"], d["kv"], d["T"])
+
+        def step(side):
+            main = torch.cuda.current_stream()
+            q.copy_(d["q"])
+            k.copy_(d["k"])
+            v.copy_(d["v"])
+            side.wait_stream(main)
+            with torch.cuda.stream(side):  # the first call behind another stream's copies
+                c.append(k, v, d["table"], d["cu"], d["kv"])
+                c.attend(q, d["table"], d["cu"], d["kv"], new, out=plain, workspace=work[0])
+            here.zero_()
+            here.copy_(parents)
+            mask.zero_()
+            c.tree_masks(here, d["cu"], d["kv"], new, out_mask=mask, out_pos=pos)
+            main.wait_stream(side)
+            c.attend(q, d["table"], d["cu"], d["kv"], new, out=out, tree=mask, workspace=work[1])
+            out.mul_(1.0)
+            c.accept(d["table"], d["cu"], d["kv"], path)
+            rk.zero_()
+            rv.zero_()
+            c.read(d["table"], d["cu"], d["kv"], d["T"], out_k=rk, out_v=rv)
+
+        side = torch.cuda.Stream()
+        step(side)
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (out, plain, mask, pos, rk, rv)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(side)
+        for _ in range(3):
+            for x in (q, out, plain, mask, pos, rk, rv, here, k, v):
+                x.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((out, plain, mask, pos, rk, rv), want))
+        c.check_device_error()
+        seen, _ = dr.masks_of(parents.tolist(), d["cu"].tolist(), 0)
+        assert torch.equal(mask.cpu(), dr.pack(seen, 1))
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("fp8", [False, True])
 def test_drafting_run(aa, fp8):
