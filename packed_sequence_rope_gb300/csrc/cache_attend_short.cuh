@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, HD == 128 ? 2 : k8 ? 4 : 3)
     }
     __syncthreads();
   };
-  if constexpr (k8) {  // launched as a dependent: the start-up overlaps the kernel before (one token over 1000 keys 7.7 us, else 10.2)
+  if constexpr (k8) {  // launched as a dependent: the start-up overlaps the kernel before (one token over 1000 keys 7.9 us, some 10.4 without)
     set_up();
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
